@@ -1,7 +1,8 @@
 /*
- * ctconv.h -- dense transposed convolution (ConvTranspose1d/2d, groups = 1)
- * and depthwise transposed convolution (groups = C_in) on AMD Instinct MI355X
- * (gfx950).  C ABI.
+ * ctconv.h -- dense transposed convolution (ConvTranspose1d/2d, groups = 1),
+ * depthwise transposed convolution (groups = C_in), and the operators of the
+ * transformer block before them in a streaming decoder, on AMD Instinct
+ * MI355X (gfx950).  C ABI.
  *
  * Operation (scatter definition).  Every input element x[n, ci, i] adds
  * x[n, ci, i] * w[ci, co, t] to the output element at o = i*s - p + t*d for
@@ -436,6 +437,217 @@ ctconv_status ctconv_depthwise_query_kernel(int64_t N, int64_t C_in, int64_t C_o
 size_t ctconv_clock_probe_bytes(void);
 ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int iters, double* mhz,
                                  double* tflops, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The transformer block of a streaming decoder.
+ *
+ * A codec decoder that turns one frame per call into audio (the Phonon TTS
+ * example of ExecuTorch PR #25037) runs transformer blocks on the frame
+ * before the transposed convolutions above: attention of the new frame over
+ * a cache of the past ones, attention over the encoder's states, and a norm,
+ * a gate and a residual scale at each seam.  The functions below are those
+ * steps apart from the plain matrix products.  Forward only, like the rest
+ * of the library; one element type per call; statistics, softmax sums and
+ * accumulated weights in fp32; 16-bit operands of a matrix product are
+ * accumulated in fp32, and softmax weights are rounded to the element type
+ * where they multiply the values (a matrix instruction takes both operands
+ * in one type).
+ *
+ * Common rules.  Sizes and strides are int64, strides in elements, at least
+ * 0, the last dimension contiguous.  Device pointers are 16-byte aligned and
+ * so are the rows they step to (every stride a multiple of 16 bytes) unless
+ * a function says otherwise; CTCONV_ERR_ALIGN if not.  Index arrays are
+ * int32.  A size below its minimum, or one that does not fit the kernel's
+ * 64-bit addressing, is CTCONV_ERR_SHAPE.  With no row to compute (B, Lq or
+ * rows of 0) nothing is enqueued and pointers may be NULL.  Results do not
+ * depend on the launch: no atomics, every sum in a fixed order.
+ *
+ * The paged cache.  k_cache and v_cache hold num_pages pages of page_size
+ * slots for Hkv heads of D values: slot t of sequence b lies at
+ *     page_table[b * table_stride + t / page_size] * kv_strides[0]
+ *       + (t % page_size) * kv_strides[1] + head * kv_strides[2]
+ * in both (kv_strides = page, slot, head).  The library's own layout is
+ * [num_pages][Hkv][page_size][D]; any other order works by its strides.  A
+ * page may be any size from 1 and page_table has max_pages columns.  Slots
+ * whose table entry is outside [0, num_pages) are never touched: attention
+ * does not see them, append and evict leave them out.  lengths[b], the
+ * slots in use, is clamped to [0, min(max_length, max_pages * page_size)] by
+the calls that take max_length.
+ * What lies past lengths[b] in a page is never used, whatever bits it holds.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Append rows to the cache.  Sequence b gets counts[b] new rows (n for every
+ * sequence when counts is NULL; clamped to [0, min(n, lengths[b])]):
+ * k_new[b][i], v_new[b][i] for i < counts[b] go to slot
+ * lengths[b] - counts[b] + i, so lengths already counts them, as it does for
+ * the attention that follows.
+ *   k_new, v_new   device [B, n, Hkv, D], new_strides = batch, row, head (both)
+ *   positions      device int32 [B, Hkv, slots] or NULL: gets the row's
+ *                  position, now[b] - counts[b] + i
+ *   weight_sum     device fp32 [B, Hkv, slots] or NULL: gets 0
+ *   now            device int32 [B], the rows each sequence has seen in all,
+ *                  with the new ones; NULL: lengths
+ *   slot_strides   batch, head strides of positions and weight_sum (the slot
+ *                  stride is 1); any value, no alignment
+ * lengths is not clamped from above: slots past the table are left out.  D a
+ * multiple of 8 up to 256.  k_cache and v_cache must not overlap the new
+ * rows or each other, and no slot may be written for two sequences.
+ */
+ctconv_status ctconv_cache_append(const void* k_new, const void* v_new, void* k_cache,
+                                  void* v_cache, const int32_t* page_table,
+                                  const int32_t* lengths, const int32_t* counts,
+                                  const int32_t* now, int32_t* positions, float* weight_sum,
+                                  int64_t B, int64_t n, int64_t Hkv, int64_t D,
+                                  int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                  const int64_t* new_strides, const int64_t* kv_strides,
+                                  int64_t table_stride, const int64_t* slot_strides,
+                                  ctconv_dtype dtype, void* stream);
+
+/*
+ * Attention of one new row per sequence over the paged cache:
+ *     s[t] = scale * q . k[t],  p[t] = exp(s[t] - lse),  out = sum_t p[t] v[t]
+ * over the slots t of [max(0, lengths[b] - window), lengths[b]) (window 0:
+ * all of them), lse = log sum_t exp(s[t]).  Query heads
+ * [h * Hq / Hkv, (h + 1) * Hq / Hkv) share cache head h.
+ *   q, out        device [B, Hq, D], q_strides, out_strides = batch, head
+ *   lse           device fp32 [B, Hq] dense, or NULL
+ *   weight_sum    device fp32 [B, Hkv, slots] or NULL: weight_sum[b][h][t]
+ *                 += the sum of p[t] over the query heads of h (slots outside
+ *                 the window and past lengths[b] are left as they are);
+ *                 slot_strides as in ctconv_cache_append
+ * A sequence without a visible slot gets out = 0 and lse = -infinity.
+ * max_length: a bound on lengths that the caller knows (the work is split
+ * and the workspace sized by it), 0 .. max_pages * page_size.  The reduction
+ * over slots is split over workgroups and joined in a fixed order.
+ *   workspace     device, 16-byte aligned, of ctconv_paged_attention_workspace_bytes
+ *                 bytes (0: may be NULL); contents ignored and left undefined;
+ *                 not shared by concurrent calls
+ * D a multiple of 8 up to 256, Hq a multiple of Hkv, scale finite
+ * (CTCONV_ERR_PARAM).  out must not overlap an input.
+ */
+ctconv_status ctconv_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                                     int64_t max_length, int64_t window,
+                                                     int weights, ctconv_dtype dtype,
+                                                     size_t* bytes);
+ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* page_table, const int32_t* lengths, void* out,
+                                     float* lse, float* weight_sum, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                                     int64_t max_pages, int64_t max_length, int64_t window,
+                                     const int64_t* q_strides, const int64_t* kv_strides,
+                                     const int64_t* out_strides, int64_t table_stride,
+                                     const int64_t* slot_strides, float scale, ctconv_dtype dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Cut every head of a sequence back to its `keep` most useful slots, by the
+ * attention weight that ctconv_paged_attention has accumulated.  With n =
+ * lengths[b] and m = min(n, keep), each head keeps m of its n slots: those
+ * whose position is below `sink` or at least now[b] - recent, then those of
+ * largest weight (a NaN weight counts as the smallest, weights above the
+ * largest finite number as that); ties go to the lowest slot.  Kept slots
+ * below m stay where they are, and the slots below m that are given up, in
+ * ascending order, take the kept slots from m on, in ascending order: only
+ * as many rows move as there are holes, and the result is dense in [0, m).
+ *   weight_sum, positions   device [B, Hkv, slots], slot_strides = batch, head;
+ *                 positions may be NULL (the slot's own number)
+ *   now           device int32 [B] (rows seen in all), or NULL: lengths
+ *   weight_out, positions_out   device [B, Hkv, keep], out_slot_strides =
+ *                 batch, head: the values that slots [0, m) now have, then 0
+ *                 and -1 up to keep; may be the input buffers (same strides),
+ *                 in which case slots from keep on are left as they are.
+ *                 positions_out may be NULL when positions is.
+ *   lengths_out   device int32 [B], gets m; may be lengths; or NULL
+ *   source        device int32 [B, Hkv, keep] dense: the slot that each of
+ *                 the slots [0, m) came from, then -1 up to keep
+ * K and V rows move in place; no page of the sequences may be shared with
+ * another sequence.  A row whose old or new slot has no page is not moved.
+ * keep >= 1, sink >= 0, recent >= 0 (CTCONV_ERR_PARAM); max_length (a bound
+ * on lengths) at most max_pages * page_size and 524288 (CTCONV_ERR_SHAPE).
+ * keep may exceed the lengths: then nothing is given up.
+ */
+ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* page_table,
+                                 const int32_t* lengths, const int32_t* now,
+                                 const float* weight_sum, const int32_t* positions,
+                                 float* weight_out, int32_t* positions_out, int32_t* lengths_out,
+                                 int32_t* source, int64_t B, int64_t Hkv, int64_t D,
+                                 int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                 int64_t max_length, int64_t keep, int64_t sink, int64_t recent,
+                                 const int64_t* kv_strides, int64_t table_stride,
+                                 const int64_t* slot_strides, const int64_t* out_slot_strides,
+                                 ctconv_dtype dtype, void* stream);
+
+/*
+ * Attention of Lq rows per sequence to Lk rows of another sequence (an
+ * encoder's states, the other branch of a two-branch decoder), no causal
+ * order: s, p, out and lse as in ctconv_paged_attention, over the rows
+ * t < lengths[b] whose mask byte is not 0.
+ *   q, out       device [B, Lq, Hq, D], q_strides, out_strides = batch, row, head
+ *   k, v         device [B, Lk, Hkv, D], k_strides, v_strides = batch, row, head
+ *   lengths      device int32 [B] or NULL (Lk); clamped to [0, Lk]
+ *   mask         device uint8 [B, Lk] or NULL (all seen), mask_stride per
+ *                sequence, no alignment
+ *   lse          device fp32 [B, Hq, Lq] dense, or NULL
+ * Rows of k and v that are not seen are never used, whatever bits they hold.
+ * A sequence that sees no row gets out = 0 and lse = -infinity.
+ * k and v may be NULL when Lk = 0.  Workspace, D, heads and scale as in
+ * ctconv_paged_attention.
+ */
+ctconv_status ctconv_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
+                                                     int64_t Hkv, int64_t D, ctconv_dtype dtype,
+                                                     size_t* bytes);
+ctconv_status ctconv_cross_attention(const void* q, const void* k, const void* v,
+                                     const int32_t* lengths, const uint8_t* mask, void* out,
+                                     float* lse, int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
+                                     int64_t Hkv, int64_t D, const int64_t* q_strides,
+                                     const int64_t* k_strides, const int64_t* v_strides,
+                                     const int64_t* out_strides, int64_t mask_stride, float scale,
+                                     ctconv_dtype dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+typedef enum {
+    CTCONV_NORM_NONE = 0,
+    CTCONV_NORM_RMS = 1,  /* u / sqrt(mean(u^2) + eps) * weight (+ bias) */
+    CTCONV_NORM_LAYER = 2 /* the same of u - mean(u) */
+} ctconv_norm;
+
+typedef enum {
+    CTCONV_GATE_NONE = 0,    /* no gate tensor */
+    CTCONV_GATE_LINEAR = 1,  /* gate */
+    CTCONV_GATE_SIGMOID = 2, /* 1 / (1 + exp(-gate)) */
+    CTCONV_GATE_TANH = 3     /* tanh(gate) */
+} ctconv_gate;
+
+/*
+ * The seam between two blocks, one pass over each row:
+ *     x_out = x + scale * g(gate) * post(h),    y = pre(x_out)
+ * with x the residual stream, h the block's output, post a norm after the
+ * block, scale one factor per channel (layer scale), and pre the next
+ * block's norm, taken of x_out before it is rounded.
+ *   x, h, x_out, y  device [rows, C]; strides = row strides of x, h, gate,
+ *                 x_out, y (5 values; unused ones ignored), at least C where
+ *                 rows > 1 (0 is allowed for x, h and gate)
+ *   post_weight, post_bias   device [C] or NULL (1, 0); post NONE: ignored
+ *   scale         device [C] or NULL (1)
+ *   gate          device [ceil(rows / rows_per_gate), C]: row r uses gate row
+ *                 r / rows_per_gate (1: one per row; the rows of a sequence:
+ *                 one per sequence); required unless gate_fn is NONE
+ *   pre_weight, pre_bias     device [C] or NULL; pre NONE: ignored, y may be NULL
+ * x_out may be x, and y may be h (same pointer and stride); otherwise
+ * outputs must not overlap inputs or each other.  Channel arrays and rows
+ * are read in 16-byte pieces where every row starts on 16 bytes (C and the
+ * strides multiples of it), else value by value: any stride is allowed.
+ * 1 <= C <= 16384, eps >= 0 and finite.  All arithmetic in fp32, each output
+ * rounded once.
+ */
+ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* post_weight,
+                                   const void* post_bias, const void* scale, const void* gate,
+                                   const void* pre_weight, const void* pre_bias, void* x_out,
+                                   void* y, int64_t rows, int64_t C, const int64_t* strides,
+                                   int64_t rows_per_gate, ctconv_norm post, ctconv_norm pre,
+                                   ctconv_gate gate_fn, float eps, ctconv_dtype dtype,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

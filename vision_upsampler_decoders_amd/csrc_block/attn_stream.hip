@@ -1,0 +1,507 @@
+// Attention of few query rows per cache head: one new row over the paged
+// cache, single tokens over an encoder's states.
+//
+// With at most 16 query rows per tile every key and value is used once per
+// tile, so the work is reading them: keys and values go from memory straight
+// to registers in 16-byte pieces and never through LDS.  A wave takes blocks
+// of KB keys.
+//  - Scores: S^T = K Q^T by 16x16 matrix instructions, a key per row, a query
+//    per column, so a lane holds 4 consecutive keys (4g .. 4g + 3 for lane
+//    group g = lane / 16) of one query, lane % 16.
+//  - The output is O^T = V^T P^T.  A matrix instruction sums over its k slots
+//    in whatever order, so slot j of lane group g stands for exactly the keys
+//    whose scores the group already holds, and P needs no exchange between
+//    lanes.  V^T needs, per lane, one value column over those keys: lane c of
+//    a group loads the c-th piece of VPL values of each key's row (whole rows,
+//    coalesced) and turns its keys x VPL block in registers.  Output tile e
+//    holds the value columns c * VPL + e.
+//  - Softmax is the one-pass one, base 2, per wave: a running maximum m that
+//    is only raised when a score passes it by 2^8 (the weights stay below
+//    2^8, far from overflow in every type, and rescaling is rare), and the
+//    sum of the weights, in fp32.
+// The waves of a workgroup are merged in LDS, the workgroups of one row tile
+// by a second kernel, both in a fixed order.
+
+#include "block_internal.h"
+#include "mfma_common.h"
+
+namespace ctconv {
+namespace block {
+
+namespace {
+
+using mfma::Mma;
+using mfma::u32x2;
+using mfma::u32x4;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kRaise = 8.f;
+
+__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The keys of sequence b that the call sees: [first, first + span).
+template <bool PAGED>
+__device__ inline void visible(const AttnArgs& a, int b, int& first, int& span) {
+    const int hi = PAGED ? a.pages.slots : a.Lk;
+    const int n = a.lengths ? clamped(a.lengths[b], hi) : hi;
+    first = PAGED && a.window > 0 && n > a.window ? n - a.window : 0;
+    span = n - first;
+}
+
+template <class TR, int DP, bool PAGED, bool EXACT>
+__global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
+    using S = typename TR::storage;
+    constexpr int ES = sizeof(S), VEC = 16 / ES;
+    constexpr int KB = ES == 2 ? 32 : 16;  // keys per block
+    constexpr int NT = KB / 16;            // score tiles per block
+    constexpr int NF = DP / (4 * VEC);     // 16-byte pieces of a key per lane
+    constexpr int VPL = DP / 16;           // values of a row per lane
+    constexpr int VW = VPL * ES / 4;       // the same in dwords
+    constexpr int VK = 4 * NT;             // keys per lane group
+    constexpr int DS = DP + 4;             // LDS row of a merged output
+    extern __shared__ __align__(16) char lds[];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int col = lane & 15, g = lane >> 4;
+    int item = blockIdx.x;
+    const int split = item % a.splits;
+    item /= a.splits;
+    const int tile = item % a.row_tiles;
+    const int bh = item / a.row_tiles;
+    const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+    const int row0 = tile * 16;
+    const int rows = a.R - row0 < 16 ? a.R - row0 : 16;
+
+    int first, span;
+    visible<PAGED>(a, b, first, span);
+    const int start = split * a.chunk;  // relative to first
+    if (a.splits > 1 && start >= span) return;
+    int n = span - start;
+    n = n < a.chunk ? n : a.chunk;
+    n = n > 0 ? n : 0;
+
+    // Row offsets and visibility bits of the chunk's keys.
+    int64_t* offs = reinterpret_cast<int64_t*>(lds);
+    uint32_t* seen = reinterpret_cast<uint32_t*>(lds + (PAGED ? (size_t)a.chunk * 8 : 0));
+    const int padded = (n + 63) & ~63;
+    for (int i = tid; i < padded; i += kThreads) {
+        bool ok = i < n;
+        const int t = first + start + i;
+        if constexpr (PAGED) {
+            int64_t o = ok ? slot_offset(a.pages, b, t) : -1;
+            ok = o >= 0;
+            offs[i] = ok ? o : 0;  // page 0 exists: a readable row
+        } else {
+            if (ok && a.mask) ok = a.mask[b * a.mask_stride + t] != 0;
+        }
+        const uint64_t w = __ballot(ok);
+        if (lane == 0) *reinterpret_cast<uint64_t*>(seen + (i >> 5)) = w;
+    }
+
+    // Queries of this tile: lane (col, g) holds pieces 4f + g of row col.
+    u32x4 qf[NF];
+    {
+        const int r = row0 + col;
+        const bool live = col < rows;
+        const int lq = live ? (int)fdiv((uint32_t)r, a.fd_G) : 0;
+        const S* qr = static_cast<const S*>(a.q) + b * a.q_b + lq * a.q_row +
+                      (int64_t)(h * a.G + (live ? r - lq * a.G : 0)) * a.q_head;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int d = (4 * f + g) * VEC;
+            qf[f] = u32x4{0, 0, 0, 0};
+            if (live && (EXACT || d < a.D)) {
+                qf[f] = *reinterpret_cast<const u32x4*>(qr + d);
+                const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[f][i] ^= flip;
+            }
+        }
+    }
+    const S* kbase = static_cast<const S*>(a.k) +
+                     (PAGED ? h * a.pages.head_stride : b * a.k_b + h * a.k_head);
+    const S* vbase = static_cast<const S*>(a.v) +
+                     (PAGED ? h * a.pages.head_stride : b * a.v_b + h * a.v_head);
+    __syncthreads();
+
+    f32x4 acc[VPL];
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -__builtin_huge_valf(), l = 0.f;
+    const int t0 = first + start;
+
+    for (int kb = wave * KB; kb < n; kb += kWaves * KB) {
+        uint32_t bits = seen[kb >> 5];
+        if (KB == 16) bits = (bits >> (kb & 16)) & 0xFFFFu;
+        const uint32_t all = KB == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+        if (bits == 0 && !a.scores) continue;
+        u32x4 kf[NT][NF];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int i = kb + 16 * t + col;
+            int64_t o;
+            if constexpr (PAGED) o = offs[i];
+            else o = (bits >> (16 * t + col)) & 1 ? (int64_t)(t0 + i) * a.k_row : 0;
+            const S* kr = kbase + o;
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const int d = (4 * f + g) * VEC;
+                kf[t][f] = *reinterpret_cast<const u32x4*>(kr + (EXACT || d < a.D ? d : 0));
+            }
+        }
+        // Values: key slot j of this lane group is key 4g + j % 4 of score
+        // tile j / 4.
+        uint32_t vr[VK][VW];
+#pragma unroll
+        for (int j = 0; j < VK; ++j) {
+            const int i = kb + 16 * (j >> 2) + 4 * g + (j & 3);
+            int64_t o;
+            if constexpr (PAGED) o = offs[i];
+            else o = (bits >> (i - kb)) & 1 ? (int64_t)(t0 + i) * a.v_row : 0;
+            const int d = col * VPL;
+            const S* vrow = vbase + o;
+            if constexpr (VW == 2) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(vrow + (EXACT || d < a.D ? d : 0));
+                vr[j][0] = w[0];
+                vr[j][1] = w[1];
+            } else {
+#pragma unroll
+                for (int p = 0; p < VW / 4; ++p) {
+                    const int dp = d + p * VEC;
+                    const u32x4 w =
+                        *reinterpret_cast<const u32x4*>(vrow + (EXACT || dp < a.D ? dp : 0));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) vr[j][4 * p + q] = w[q];
+                }
+            }
+        }
+        f32x4 s[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                u32x4 k = kf[t][f];
+                // the piece past the row was read from its start: not a product
+                if (!EXACT && (4 * f + g) * VEC >= a.D) k = u32x4{0, 0, 0, 0};
+                Mma<TR>::step(s[t], k, qf[f]);
+            }
+        }
+        float top = -__builtin_huge_valf();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = s[t][i] * a.c;
+                if (bits != all && !((bits >> (16 * t + 4 * g + i)) & 1)) v = -__builtin_huge_valf();
+                s[t][i] = v;
+                top = fmaxf(top, v);
+            }
+        if (a.scores && col < rows) {
+            float* sr = a.scores + ((int64_t)bh * a.R + row0 + col) * a.score_stride + start + kb;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                *reinterpret_cast<f32x4*>(sr + 16 * t + 4 * g) = s[t];
+        }
+        if (bits != all) {
+            // what a slot without a visible key holds may be NaN: zero, not 0 * NaN
+#pragma unroll
+            for (int j = 0; j < VK; ++j)
+                if (!((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1))
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) vr[j][w] = 0;
+        }
+        if (__any(top > m + kRaise)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float up = fmaxf(m, top);
+            const float f = m == up ? 1.f : exp2_fast(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < VPL; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[e][i] *= f;
+        }
+        const float ref = m == -__builtin_huge_valf() ? 0.f : m;
+        float p[VK];
+#pragma unroll
+        for (int j = 0; j < VK; ++j) {
+            p[j] = exp2_fast(s[j >> 2][j & 3] - ref);
+            l += p[j];
+        }
+        if constexpr (ES == 2) {
+            u32x4 pf;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) pf[w] = mfma::pack2<TR>(p[2 * w], p[2 * w + 1]);
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) {
+                const unsigned sel = (e & 1) ? 0x07060302u : 0x05040100u;
+                u32x4 vf;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][e >> 1], vr[2 * w][e >> 1], sel);
+                Mma<TR>::step(acc[e], vf, pf);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VK; ++j)
+#pragma unroll
+                for (int e = 0; e < VPL; ++e)
+                    acc[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vr[j][e]), p[j],
+                                                                  acc[e], 0, 0, 0);
+        }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // Merge the waves: [wave][row][DS] outputs, then [wave][row] maxima and
+    // sums, then [row] merged ones.
+    __syncthreads();  // offs and seen are no longer read
+    float* mo = reinterpret_cast<float*>(lds);
+    float* mm = mo + kWaves * rows * DS;
+    float* ml = mm + kWaves * 16;
+    float* jm = ml + kWaves * 16;  // [16] maximum, [16] sum
+    if (col < rows) {
+        float* o = mo + (wave * rows + col) * DS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < VPL; e += 4)
+                *reinterpret_cast<f32x4*>(o + (4 * g + i) * VPL + e) =
+                    f32x4{acc[e][i], acc[e + 1][i], acc[e + 2][i], acc[e + 3][i]};
+        if (g == 0) {
+            mm[wave * 16 + col] = m;
+            ml[wave * 16 + col] = l;
+        }
+    }
+    __syncthreads();
+    if (tid < rows) {
+        float top = mm[tid];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, mm[w * 16 + tid]);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float mw = mm[w * 16 + tid];
+            const float f = mw == -__builtin_huge_valf() ? 0.f : exp2_fast(mw - top);
+            sum += f * ml[w * 16 + tid];
+            mm[w * 16 + tid] = f;
+        }
+        jm[tid] = top;
+        jm[16 + tid] = sum;
+        if (a.direct && a.lse) {
+            const int r = row0 + tid, lq = (int)fdiv((uint32_t)r, a.fd_G);
+            a.lse[((int64_t)b * a.Hq + h * a.G + (r - lq * a.G)) * a.Lq + lq] =
+                top * kLn2 + logf(sum);
+        }
+    }
+    __syncthreads();
+    const int pieces = a.D / 4;
+    for (int i = tid; i < rows * pieces; i += kThreads) {
+        const int r = i / pieces, d = (i - r * pieces) * 4;
+        f32x4 o{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = mm[w * 16 + r];
+            const f32x4 x = *reinterpret_cast<const f32x4*>(mo + (w * rows + r) * DS + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[e], o[e]);
+        }
+        if (a.direct) {
+            const float sum = jm[16 + r];
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int rr = row0 + r, lq = (int)fdiv((uint32_t)rr, a.fd_G);
+            S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row +
+                    (int64_t)(h * a.G + (rr - lq * a.G)) * a.o_head + d;
+            if constexpr (ES == 2) {
+                u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv),
+                        mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
+                *reinterpret_cast<u32x2*>(to) = w;
+            } else {
+                *reinterpret_cast<f32x4*>(to) = o * inv;
+            }
+        } else {
+            const int64_t part = ((int64_t)bh * a.splits + split) * a.R + row0 + r;
+            *reinterpret_cast<f32x4*>(a.part_o + part * a.D + d) = o;
+            if (d == 0) {
+                a.part_ml[2 * part] = jm[r];
+                a.part_ml[2 * part + 1] = jm[16 + r];
+            }
+        }
+    }
+}
+
+// Join: one workgroup per query row adds the splits' outputs in ascending
+// order within each of its lane groups, and the groups in ascending order.
+// The workgroups past those add the weights to weight_sum: 1024 slots each.
+constexpr int kWeightSlots = 4 * kThreads;
+constexpr int kLseRows = 256;
+
+// Maximum and sum (relative to it) of a row over its splits; every lane of
+// the wave calls it and gets both.
+__device__ inline void join_stats(const float* ml, int64_t stride, int n, float& top, float& sum) {
+    const int lane = threadIdx.x & 63;
+    top = -__builtin_huge_valf();
+    for (int s = lane; s < n; s += 64) top = fmaxf(top, ml[2 * s * stride]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    sum = 0.f;
+    for (int s = lane; s < n; s += 64) {
+        const float m = ml[2 * s * stride];
+        if (m != -__builtin_huge_valf()) sum += exp2_fast(m - top) * ml[2 * s * stride + 1];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+}
+
+template <class TR, bool PAGED>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_blocks,
+                                                        int weight_blocks) {
+    using S = typename TR::storage;
+    __shared__ float part[kThreads * 4];
+    const int tid = threadIdx.x, wave = tid >> 6;
+    if ((int)blockIdx.x < out_blocks) {
+        const int bh = blockIdx.x / a.R, r = blockIdx.x - bh * a.R;
+        const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+        int first, span;
+        visible<PAGED>(a, b, first, span);
+        const int n = (span + a.chunk - 1) / a.chunk;
+        const int64_t p0 = (int64_t)bh * a.splits * a.R + r;
+        const float* ml = a.part_ml + 2 * p0;
+        float top, sum;
+        join_stats(ml, a.R, n, top, sum);
+        const int pieces = a.D / 4, groups = kThreads / pieces;
+        const int grp = tid / pieces, d = (tid - grp * pieces) * 4;
+        if (grp < groups) {
+            f32x4 o{0.f, 0.f, 0.f, 0.f};
+            for (int s = grp; s < n; s += groups) {
+                const float m = ml[2 * (int64_t)s * a.R];
+                if (m == -__builtin_huge_valf()) continue;
+                const float f = exp2_fast(m - top);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(
+                    a.part_o + (p0 + (int64_t)s * a.R) * a.D + d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[e], o[e]);
+            }
+            *reinterpret_cast<f32x4*>(part + 4 * tid) = o;
+        }
+        __syncthreads();
+        const int lq = (int)fdiv((uint32_t)r, a.fd_G);
+        const int hq = h * a.G + (r - lq * a.G);
+        if (tid < pieces) {
+            f32x4 o{0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < groups; ++q)
+                o += *reinterpret_cast<const f32x4*>(part + 4 * (q * pieces + tid));
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row + (int64_t)hq * a.o_head + d;
+            if constexpr (sizeof(S) == 2) {
+                u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv),
+                        mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
+                *reinterpret_cast<u32x2*>(to) = w;
+            } else {
+                *reinterpret_cast<f32x4*>(to) = o * inv;
+            }
+        }
+        if (tid == 0 && a.lse)
+            a.lse[((int64_t)b * a.Hq + hq) * a.Lq + lq] = top * kLn2 + logf(sum);
+        return;
+    }
+    // weights of paged calls (Lq = 1, R = G)
+    const int item = blockIdx.x - out_blocks;
+    const int bh = item / weight_blocks, blk = item - bh * weight_blocks;
+    const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+    int first, span;
+    visible<PAGED>(a, b, first, span);
+    if (blk * kWeightSlots >= span) return;
+    const int n = (span + a.chunk - 1) / a.chunk;
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    const int i0 = blk * kWeightSlots + 4 * tid;
+    float* lse2 = part;
+    for (int r0 = 0; r0 < a.R; r0 += kLseRows) {
+        const int rn = a.R - r0 < kLseRows ? a.R - r0 : kLseRows;
+        __syncthreads();
+        for (int r = wave; r < rn; r += kWaves) {
+            float top, sum;
+            join_stats(a.part_ml + 2 * ((int64_t)bh * a.splits * a.R + r0 + r), a.R, n, top, sum);
+            if ((tid & 63) == 0)
+                lse2[r] = top == -__builtin_huge_valf() ? __builtin_huge_valf()
+                                                        : top + __builtin_amdgcn_logf(sum);
+        }
+        __syncthreads();
+        if (i0 < span)
+            for (int r = 0; r < rn; ++r) {
+                const f32x4 s = *reinterpret_cast<const f32x4*>(
+                    a.scores + ((int64_t)bh * a.R + r0 + r) * a.score_stride + i0);
+                const float z = lse2[r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add[e] += exp2_fast(s[e] - z);
+            }
+    }
+    float* w = a.weight_sum + b * a.slot_b + h * a.slot_h + first + i0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (i0 + e < span) w[e] += add[e];
+}
+
+template <class TR, int DP, bool PAGED>
+hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
+    const int rows = a.R < 16 ? a.R : 16;
+    const size_t stage = (PAGED ? (size_t)a.chunk * 8 : 0) + (size_t)(a.chunk / 32 + 2) * 4;
+    const size_t merge = (size_t)(kWaves * rows * (DP + 4) + 2 * kWaves * 16 + 32) * 4;
+    const size_t lds = stage > merge ? stage : merge;
+    const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * a.row_tiles * a.splits));
+    const void* fn = a.D == DP ? reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, true>)
+                               : reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, false>);
+    if (lds > 64u << 10) {
+        const hipError_t e =
+            hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    AttnArgs args = a;
+    void* params[] = {&args};
+    return hipLaunchKernel(fn, grid, dim3(kThreads), params, lds, s);
+}
+
+template <class TR, bool PAGED>
+hipError_t stream_t(const AttnArgs& a, hipStream_t s) {
+    if (a.D <= 64) return stream_d<TR, 64, PAGED>(a, s);
+    if (a.D <= 128) return stream_d<TR, 128, PAGED>(a, s);
+    return stream_d<TR, 256, PAGED>(a, s);
+}
+
+template <class TR, bool PAGED>
+hipError_t join_t(const AttnArgs& a, hipStream_t s) {
+    const int out_blocks = a.B * a.Hkv * a.R;
+    const int64_t longest = a.score_stride;
+    const int weight_blocks =
+        a.weight_sum ? (int)((longest + kWeightSlots - 1) / kWeightSlots) : 0;
+    const int64_t grid = out_blocks + (int64_t)a.B * a.Hkv * weight_blocks;
+    join_kernel<TR, PAGED>
+        <<<dim3((unsigned)grid), dim3(kThreads), 0, s>>>(a, out_blocks, weight_blocks);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_stream(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s) {
+    switch (dt) {
+        case CTCONV_F32: return paged ? stream_t<TF32, true>(a, s) : stream_t<TF32, false>(a, s);
+        case CTCONV_BF16: return paged ? stream_t<TBF16, true>(a, s) : stream_t<TBF16, false>(a, s);
+        case CTCONV_F16: return paged ? stream_t<TF16, true>(a, s) : stream_t<TF16, false>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s) {
+    switch (dt) {
+        case CTCONV_F32: return paged ? join_t<TF32, true>(a, s) : join_t<TF32, false>(a, s);
+        case CTCONV_BF16: return paged ? join_t<TBF16, true>(a, s) : join_t<TBF16, false>(a, s);
+        case CTCONV_F16: return paged ? join_t<TF16, true>(a, s) : join_t<TF16, false>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace block
+}  // namespace ctconv

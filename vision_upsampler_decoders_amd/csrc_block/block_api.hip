@@ -1,0 +1,564 @@
+// C ABI of the decoder-block operators: argument validation, planning and
+// launches.  No allocation, no synchronisation, no global state.
+
+#include <math.h>
+#include <string.h>
+
+#include "block_internal.h"
+
+using namespace ctconv;
+using namespace ctconv::block;
+
+namespace {
+
+constexpr int64_t kMaxInt = INT32_MAX;
+constexpr int64_t kMaxEvictSlots = 524288;  // select_kernel's bits and sums fit LDS
+constexpr int64_t kMaxRowValues = 16384;    // norm_kernel keeps a row in registers
+
+size_t esize(ctconv_dtype dt) { return dt == CTCONV_F32 ? 4 : 2; }
+
+bool dtype_ok(int dt) { return dt == CTCONV_F32 || dt == CTCONV_BF16 || dt == CTCONV_F16; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+ctconv_status to_status(hipError_t e) { return e == hipSuccess ? CTCONV_OK : CTCONV_ERR_HIP; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Strides of a tensor whose last dimension holds D values: not negative, the
+// last element addressable.
+ctconv_status strides_ok(const int64_t* strides, const int64_t* sizes, int n, int64_t D,
+                         ctconv_dtype dt) {
+    __int128 last = D;
+    for (int i = 0; i < n; ++i) {
+        if (strides[i] < 0) return CTCONV_ERR_SHAPE;
+        if (sizes[i] > 0) last += (__int128)(sizes[i] - 1) * strides[i];
+    }
+    if (last * (int64_t)esize(dt) > INT64_MAX) return CTCONV_ERR_SHAPE;
+    return CTCONV_OK;
+}
+
+// Every row starts on 16 bytes (strides of a dimension of one are not stepped).
+bool rows_aligned(const int64_t* strides, const int64_t* sizes, int n, ctconv_dtype dt) {
+    const int64_t step = 16 / (int64_t)esize(dt);
+    for (int i = 0; i < n; ++i)
+        if (sizes[i] > 1 && strides[i] % step != 0) return false;
+    return true;
+}
+
+struct Check {
+    ctconv_status st = CTCONV_OK;
+    bool align = true;
+    void tensor(const void* p, const int64_t* strides, std::initializer_list<int64_t> sizes,
+                int64_t D, ctconv_dtype dt) {
+        const ctconv_status s = strides_ok(strides, sizes.begin(), (int)sizes.size(), D, dt);
+        if (st == CTCONV_OK) st = s;
+        if (p && !aligned16(p)) align = false;
+        if (!rows_aligned(strides, sizes.begin(), (int)sizes.size(), dt)) align = false;
+    }
+    void pointer(const void* p) {
+        if (p && !aligned16(p)) align = false;
+    }
+    ctconv_status status() const {
+        return st != CTCONV_OK ? st : align ? CTCONV_OK : CTCONV_ERR_ALIGN;
+    }
+};
+
+// Heads and row width of the attention and cache calls.
+ctconv_status head_sizes(int64_t B, int64_t Hkv, int64_t D, ctconv_dtype dt) {
+    if (!dtype_ok(dt)) return CTCONV_ERR_DTYPE;
+    if (B < 0 || B > kMaxInt || Hkv < 1 || Hkv > 65535) return CTCONV_ERR_SHAPE;
+    if (D < 8 || D > 256 || D % 8 != 0) return CTCONV_ERR_SHAPE;
+    return CTCONV_OK;
+}
+
+ctconv_status page_sizes(int64_t num_pages, int64_t page_size, int64_t max_pages) {
+    if (num_pages < 1 || num_pages > kMaxInt || page_size < 1 || page_size > kMaxInt ||
+        max_pages < 1 || max_pages > kMaxInt)
+        return CTCONV_ERR_SHAPE;
+    // slot numbers, and what rounding up to whole workgroups adds, fit int32
+    if ((__int128)page_size * max_pages > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
+    return CTCONV_OK;
+}
+
+Pages make_pages(const int32_t* table, int64_t table_stride, const int64_t* kv_strides,
+                 int64_t num_pages, int64_t page_size, int64_t max_pages, int64_t max_length) {
+    Pages p;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.page_stride = kv_strides[0];
+    p.slot_stride = kv_strides[1];
+    p.head_stride = kv_strides[2];
+    p.num_pages = (int)num_pages;
+    p.page_size = (int)page_size;
+    const int64_t slots = page_size * max_pages;
+    p.slots = (int)(slots < max_length ? slots : max_length);
+    p.fd_page = make_fastdiv((uint32_t)page_size);
+    return p;
+}
+
+// Slot arrays (positions, weights): one value per slot.
+ctconv_status slot_strides_ok(const int64_t* strides, int64_t B, int64_t Hkv, int64_t slots) {
+    const int64_t sizes[2] = {B, Hkv};
+    return strides_ok(strides, sizes, 2, slots, CTCONV_F32);
+}
+
+// The split of one attention call: R query rows per (sequence, cache head),
+// at most `span` visible keys.
+struct Plan {
+    int64_t row_tiles, chunk, splits;
+    bool direct;
+    int64_t score_stride;  // floats per query row (weights), else 0
+    int64_t parts;         // partial rows
+    int64_t score_bytes, part_o_bytes, part_ml_bytes, bytes;
+};
+
+constexpr int64_t kTargetGroups = 2048;  // 8 workgroups per compute unit
+constexpr int64_t kMinChunk = 256, kMaxChunk = 2048;
+
+int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
+
+ctconv_status plan_stream(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span, bool weights,
+                          Plan* p) {
+    memset(p, 0, sizeof(*p));
+    p->row_tiles = ceil_div(R, 16);
+    const __int128 tiles = (__int128)B * Hkv * p->row_tiles;
+    if (tiles > kMaxInt || (__int128)B * Hkv * R > kMaxInt) return CTCONV_ERR_SHAPE;
+    const int64_t want = tiles > 0 ? ceil_div(kTargetGroups, (int64_t)tiles) : 1;
+    int64_t chunk = round_up(ceil_div(span > 0 ? span : 1, want), 128);
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    if (chunk > kMaxChunk) chunk = kMaxChunk;
+    p->chunk = chunk;
+    p->splits = span > 0 ? ceil_div(span, chunk) : 1;
+    p->direct = p->splits == 1 && !weights;
+    __int128 score = 0, parts = 0;
+    if (weights) {
+        p->score_stride = round_up(span > 0 ? span : 1, 128);
+        score = (__int128)B * Hkv * R * p->score_stride * 4;
+    }
+    if (!p->direct) parts = (__int128)B * Hkv * R * p->splits;
+    const __int128 total = score + parts * (D + 2) * 4 + 64;
+    if (tiles * p->splits > kMaxInt || parts * D > ((__int128)1 << 61) ||
+        total > ((__int128)1 << 62))
+        return CTCONV_ERR_SHAPE;
+    if (weights && (__int128)B * Hkv * R + (__int128)B * Hkv * ceil_div(p->score_stride, 1024) >
+                       kMaxInt)
+        return CTCONV_ERR_SHAPE;
+    p->parts = (int64_t)parts;
+    p->score_bytes = (int64_t)score;
+    p->part_o_bytes = (int64_t)parts * D * 4;
+    p->part_ml_bytes = round_up((int64_t)parts * 8, 16);
+    p->bytes = p->score_bytes + p->part_o_bytes + p->part_ml_bytes;
+    return CTCONV_OK;
+}
+
+void apply_plan(const Plan& p, void* ws, AttnArgs* a) {
+    a->row_tiles = (int)p.row_tiles;
+    a->chunk = (int)p.chunk;
+    a->splits = (int)p.splits;
+    a->direct = p.direct;
+    a->score_stride = p.score_stride;
+    char* at = static_cast<char*>(ws);
+    a->scores = p.score_bytes ? reinterpret_cast<float*>(at) : nullptr;
+    a->part_o = reinterpret_cast<float*>(at + p.score_bytes);
+    a->part_ml = reinterpret_cast<float*>(at + p.score_bytes + p.part_o_bytes);
+}
+
+ctconv_status paged_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_length,
+                         int64_t window, bool weights, ctconv_dtype dt, Plan* p) {
+    const ctconv_status st = head_sizes(B, Hkv, D, dt);
+    if (st != CTCONV_OK) return st;
+    if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
+    if (max_length < 0 || max_length > kMaxInt - (1 << 20) || window < 0) return CTCONV_ERR_SHAPE;
+    const int64_t span = window > 0 && window < max_length ? window : max_length;
+    return plan_stream(B, Hkv, Hq / Hkv, D, span, weights, p);
+}
+
+ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
+                         ctconv_dtype dt, Plan* p) {
+    const ctconv_status st = head_sizes(B, Hkv, D, dt);
+    if (st != CTCONV_OK) return st;
+    if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
+    if (Lq < 0 || Lq > kMaxInt || Lk < 0 || Lk > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
+    if ((__int128)Lq * (Hq / Hkv) > kMaxInt) return CTCONV_ERR_SHAPE;
+    return plan_stream(B, Hkv, Lq * (Hq / Hkv), D, Lk, false, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+ctconv_status ctconv_cache_append(const void* k_new, const void* v_new, void* k_cache,
+                                  void* v_cache, const int32_t* page_table,
+                                  const int32_t* lengths, const int32_t* counts,
+                                  const int32_t* now, int32_t* positions, float* weight_sum,
+                                  int64_t B, int64_t n, int64_t Hkv, int64_t D,
+                                  int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                  const int64_t* new_strides, const int64_t* kv_strides,
+                                  int64_t table_stride, const int64_t* slot_strides,
+                                  ctconv_dtype dtype, void* stream) {
+    ctconv_status st = head_sizes(B, Hkv, D, dtype);
+    if (st != CTCONV_OK) return st;
+    if (n < 0 || n > kMaxInt - (1 << 20) || table_stride < 0) return CTCONV_ERR_SHAPE;
+    st = page_sizes(num_pages, page_size, max_pages);
+    if (st != CTCONV_OK) return st;
+    if (B == 0 || n == 0) return CTCONV_OK;
+    const bool slots = positions || weight_sum;
+    if (!k_new || !v_new || !k_cache || !v_cache || !page_table || !lengths || !new_strides ||
+        !kv_strides || (slots && !slot_strides))
+        return CTCONV_ERR_NULL;
+    Check c;
+    c.tensor(k_new, new_strides, {B, n, Hkv}, D, dtype);
+    c.tensor(k_cache, kv_strides, {num_pages, page_size, Hkv}, D, dtype);
+    c.pointer(v_new);
+    c.pointer(v_cache);
+    if (slots && c.st == CTCONV_OK)
+        c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
+    st = c.status();
+    if (st != CTCONV_OK) return st;
+    AppendArgs a;
+    memset(&a, 0, sizeof(a));
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.lengths = lengths;
+    a.counts = counts;
+    a.now = now;
+    a.positions = positions;
+    a.weight_sum = weight_sum;
+    a.pages = make_pages(page_table, table_stride, kv_strides, num_pages, page_size, max_pages,
+                         kMaxInt);
+    a.new_b = new_strides[0];
+    a.new_row = new_strides[1];
+    a.new_head = new_strides[2];
+    if (slots) {
+        a.slot_b = slot_strides[0];
+        a.slot_h = slot_strides[1];
+    }
+    a.B = (int)B;
+    a.n = (int)n;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.chunks = (int)(D * (int64_t)esize(dtype) / 16);
+    // about 2048 pieces of K and of V per workgroup
+    int64_t rows = 2048 / (Hkv * a.chunks);
+    rows = rows < 1 ? 1 : rows > n ? n : rows;
+    a.rows_per_group = (int)rows;
+    const int64_t groups = ceil_div(n, rows);
+    if ((__int128)groups * B > kMaxInt) return CTCONV_ERR_SHAPE;
+    a.groups = (int)groups;
+    a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
+    a.fd_heads = make_fastdiv((uint32_t)Hkv);
+    a.fd_groups = make_fastdiv((uint32_t)groups);
+    return to_status(launch_append(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+ctconv_status ctconv_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                                     int64_t max_length, int64_t window,
+                                                     int weights, ctconv_dtype dtype,
+                                                     size_t* bytes) {
+    if (!bytes) return CTCONV_ERR_NULL;
+    Plan p;
+    const ctconv_status st =
+        paged_plan(B, Hq, Hkv, D, max_length, window, weights != 0, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    *bytes = (size_t)p.bytes;
+    return CTCONV_OK;
+}
+
+ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* page_table, const int32_t* lengths, void* out,
+                                     float* lse, float* weight_sum, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                                     int64_t max_pages, int64_t max_length, int64_t window,
+                                     const int64_t* q_strides, const int64_t* kv_strides,
+                                     const int64_t* out_strides, int64_t table_stride,
+                                     const int64_t* slot_strides, float scale, ctconv_dtype dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    Plan p;
+    ctconv_status st =
+        paged_plan(B, Hq, Hkv, D, max_length, window, weight_sum != nullptr, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    st = page_sizes(num_pages, page_size, max_pages);
+    if (st != CTCONV_OK) return st;
+    if (max_length > page_size * max_pages || table_stride < 0) return CTCONV_ERR_SHAPE;
+    if (!isfinite(scale)) return CTCONV_ERR_PARAM;
+    if (B == 0) return CTCONV_OK;
+    if (!q || !k_cache || !v_cache || !page_table || !lengths || !out || !q_strides ||
+        !kv_strides || !out_strides || (weight_sum && !slot_strides))
+        return CTCONV_ERR_NULL;
+    Check c;
+    c.tensor(q, q_strides, {B, Hq}, D, dtype);
+    c.tensor(out, out_strides, {B, Hq}, D, dtype);
+    c.tensor(k_cache, kv_strides, {num_pages, page_size, Hkv}, D, dtype);
+    c.pointer(v_cache);
+    c.pointer(workspace);
+    if (weight_sum && c.st == CTCONV_OK)
+        c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
+    st = c.status();
+    if (st != CTCONV_OK) return st;
+    if (p.bytes > 0 && (!workspace || workspace_bytes < (size_t)p.bytes))
+        return CTCONV_ERR_WORKSPACE;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.out = out;
+    a.lse = lse;
+    a.lengths = lengths;
+    a.weight_sum = weight_sum;
+    a.pages = make_pages(page_table, table_stride, kv_strides, num_pages, page_size, max_pages,
+                         max_length);
+    a.q_b = q_strides[0];
+    a.q_head = q_strides[1];
+    a.o_b = out_strides[0];
+    a.o_head = out_strides[1];
+    if (weight_sum) {
+        a.slot_b = slot_strides[0];
+        a.slot_h = slot_strides[1];
+    }
+    a.B = (int)B;
+    a.Lq = 1;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.G = a.R = (int)(Hq / Hkv);
+    a.D = (int)D;
+    a.window = (int)(window < max_length ? window : 0);
+    a.fd_G = make_fastdiv((uint32_t)a.G);
+    a.c = fabsf(scale) * kLog2e;
+    a.negate = scale < 0;
+    apply_plan(p, workspace, &a);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    st = to_status(launch_attn_stream(a, dtype, true, s));
+    if (st != CTCONV_OK || a.direct) return st;
+    return to_status(launch_attn_join(a, dtype, true, s));
+}
+
+ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* page_table,
+                                 const int32_t* lengths, const int32_t* now,
+                                 const float* weight_sum, const int32_t* positions,
+                                 float* weight_out, int32_t* positions_out, int32_t* lengths_out,
+                                 int32_t* source, int64_t B, int64_t Hkv, int64_t D,
+                                 int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                 int64_t max_length, int64_t keep, int64_t sink, int64_t recent,
+                                 const int64_t* kv_strides, int64_t table_stride,
+                                 const int64_t* slot_strides, const int64_t* out_slot_strides,
+                                 ctconv_dtype dtype, void* stream) {
+    ctconv_status st = head_sizes(B, Hkv, D, dtype);
+    if (st != CTCONV_OK) return st;
+    st = page_sizes(num_pages, page_size, max_pages);
+    if (st != CTCONV_OK) return st;
+    if (max_length < 0 || max_length > page_size * max_pages || max_length > kMaxEvictSlots ||
+        table_stride < 0)
+        return CTCONV_ERR_SHAPE;
+    if (keep < 1 || sink < 0 || recent < 0) return CTCONV_ERR_PARAM;
+    if (keep > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
+    if (B == 0) return CTCONV_OK;
+    if (!k_cache || !v_cache || !page_table || !lengths || !weight_sum || !weight_out || !source ||
+        !kv_strides || !slot_strides || !out_slot_strides || (positions && !positions_out))
+        return CTCONV_ERR_NULL;
+    Check c;
+    c.tensor(k_cache, kv_strides, {num_pages, page_size, Hkv}, D, dtype);
+    c.pointer(v_cache);
+    if (c.st == CTCONV_OK) c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
+    if (c.st == CTCONV_OK) c.st = slot_strides_ok(out_slot_strides, B, Hkv, keep);
+    st = c.status();
+    if (st != CTCONV_OK) return st;
+    // in place: the same slots
+    if ((weight_out == weight_sum || (positions && positions_out == positions)) &&
+        (slot_strides[0] != out_slot_strides[0] || slot_strides[1] != out_slot_strides[1]))
+        return CTCONV_ERR_PARAM;
+    EvictArgs a;
+    memset(&a, 0, sizeof(a));
+    a.k = k_cache;
+    a.v = v_cache;
+    a.lengths = lengths;
+    a.now = now;
+    a.weight_sum = weight_sum;
+    a.positions = positions;
+    a.weight_out = weight_out;
+    a.positions_out = positions_out;
+    a.lengths_out = lengths_out;
+    a.source = source;
+    a.pages = make_pages(page_table, table_stride, kv_strides, num_pages, page_size, max_pages,
+                         max_length);
+    a.slot_b = slot_strides[0];
+    a.slot_h = slot_strides[1];
+    a.out_b = out_slot_strides[0];
+    a.out_h = out_slot_strides[1];
+    a.B = (int)B;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.keep = (int)keep;
+    a.sink = (int)(sink < kMaxInt ? sink : kMaxInt);
+    a.recent = (int)(recent < kMaxInt ? recent : kMaxInt);
+    a.words = (int)(round_up(max_length > 0 ? max_length : 1, 1024) / 64);
+    a.chunks = (int)(D * (int64_t)esize(dtype) / 16);
+    a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
+    if ((__int128)B * Hkv * ceil_div(keep, 64) > kMaxInt) return CTCONV_ERR_SHAPE;
+    return to_status(launch_evict(a, dtype, static_cast<hipStream_t>(stream)));
+}
+
+ctconv_status ctconv_cross_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
+                                                     int64_t Hkv, int64_t D, ctconv_dtype dtype,
+                                                     size_t* bytes) {
+    if (!bytes) return CTCONV_ERR_NULL;
+    Plan p;
+    const ctconv_status st = cross_plan(B, Lq, Lk, Hq, Hkv, D, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    *bytes = (size_t)p.bytes;
+    return CTCONV_OK;
+}
+
+ctconv_status ctconv_cross_attention(const void* q, const void* k, const void* v,
+                                     const int32_t* lengths, const uint8_t* mask, void* out,
+                                     float* lse, int64_t B, int64_t Lq, int64_t Lk, int64_t Hq,
+                                     int64_t Hkv, int64_t D, const int64_t* q_strides,
+                                     const int64_t* k_strides, const int64_t* v_strides,
+                                     const int64_t* out_strides, int64_t mask_stride, float scale,
+                                     ctconv_dtype dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    Plan p;
+    ctconv_status st = cross_plan(B, Lq, Lk, Hq, Hkv, D, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    if (!isfinite(scale)) return CTCONV_ERR_PARAM;
+    if (mask && mask_stride < 0) return CTCONV_ERR_SHAPE;
+    if (B == 0 || Lq == 0) return CTCONV_OK;
+    if (!q || !out || ((!k || !v) && Lk > 0) || !q_strides || !k_strides || !v_strides ||
+        !out_strides)
+        return CTCONV_ERR_NULL;
+    Check c;
+    c.tensor(q, q_strides, {B, Lq, Hq}, D, dtype);
+    c.tensor(out, out_strides, {B, Lq, Hq}, D, dtype);
+    c.tensor(k, k_strides, {B, Lk, Hkv}, D, dtype);
+    c.tensor(v, v_strides, {B, Lk, Hkv}, D, dtype);
+    c.pointer(workspace);
+    st = c.status();
+    if (st != CTCONV_OK) return st;
+    if (p.bytes > 0 && (!workspace || workspace_bytes < (size_t)p.bytes))
+        return CTCONV_ERR_WORKSPACE;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.lse = lse;
+    a.lengths = lengths;
+    a.mask = mask;
+    a.q_b = q_strides[0];
+    a.q_row = q_strides[1];
+    a.q_head = q_strides[2];
+    a.k_b = k_strides[0];
+    a.k_row = k_strides[1];
+    a.k_head = k_strides[2];
+    a.v_b = v_strides[0];
+    a.v_row = v_strides[1];
+    a.v_head = v_strides[2];
+    a.o_b = out_strides[0];
+    a.o_row = out_strides[1];
+    a.o_head = out_strides[2];
+    a.mask_stride = mask_stride;
+    a.B = (int)B;
+    a.Lq = (int)Lq;
+    a.Lk = (int)Lk;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.G = (int)(Hq / Hkv);
+    a.R = (int)(Lq * a.G);
+    a.D = (int)D;
+    a.fd_G = make_fastdiv((uint32_t)a.G);
+    a.c = fabsf(scale) * kLog2e;
+    a.negate = scale < 0;
+    apply_plan(p, workspace, &a);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    st = to_status(launch_attn_stream(a, dtype, false, s));
+    if (st != CTCONV_OK || a.direct) return st;
+    return to_status(launch_attn_join(a, dtype, false, s));
+}
+
+ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* post_weight,
+                                   const void* post_bias, const void* scale, const void* gate,
+                                   const void* pre_weight, const void* pre_bias, void* x_out,
+                                   void* y, int64_t rows, int64_t C, const int64_t* strides,
+                                   int64_t rows_per_gate, ctconv_norm post, ctconv_norm pre,
+                                   ctconv_gate gate_fn, float eps, ctconv_dtype dtype,
+                                   void* stream) {
+    int kinds[3];
+    // a C caller may pass any int: read them as ints
+    memcpy(&kinds[0], &post, sizeof(int));
+    memcpy(&kinds[1], &pre, sizeof(int));
+    memcpy(&kinds[2], &gate_fn, sizeof(int));
+    if (!dtype_ok(dtype)) return CTCONV_ERR_DTYPE;
+    if (kinds[0] < 0 || kinds[0] > CTCONV_NORM_LAYER || kinds[1] < 0 ||
+        kinds[1] > CTCONV_NORM_LAYER || kinds[2] < 0 || kinds[2] > CTCONV_GATE_TANH)
+        return CTCONV_ERR_PARAM;
+    if (!isfinite(eps) || eps < 0) return CTCONV_ERR_PARAM;
+    if (rows < 0 || rows > kMaxInt || C < 1 || C > kMaxRowValues) return CTCONV_ERR_SHAPE;
+    const bool gated = kinds[2] != CTCONV_GATE_NONE, normed = kinds[1] != CTCONV_NORM_NONE;
+    if (gated && rows_per_gate < 1) return CTCONV_ERR_SHAPE;
+    if (rows == 0) return CTCONV_OK;
+    if (!x || !h || !x_out || !strides || (gated && !gate) || (normed && !y))
+        return CTCONV_ERR_NULL;
+    const int64_t gate_rows = gated ? ceil_div(rows, rows_per_gate) : 1;
+    Check c;
+    bool vec = C % (16 / (int64_t)esize(dtype)) == 0;
+    const struct {
+        const void* p;
+        int64_t stride, n;
+        bool used, written;
+    } row[5] = {{x, strides[0], rows, true, false},
+                {h, strides[1], rows, true, false},
+                {gate, strides[2], gate_rows, gated, false},
+                {x_out, strides[3], rows, true, true},
+                {y, strides[4], rows, normed, true}};
+    for (const auto& r : row) {
+        if (!r.used) continue;
+        const ctconv_status s = strides_ok(&r.stride, &r.n, 1, C, dtype);
+        if (s != CTCONV_OK) return s;
+        if (r.written && r.n > 1 && r.stride < C) return CTCONV_ERR_SHAPE;
+        if (!rows_aligned(&r.stride, &r.n, 1, dtype)) vec = false;
+        c.pointer(r.p);
+    }
+    const bool posted = kinds[0] != CTCONV_NORM_NONE;
+    if (posted) {
+        c.pointer(post_weight);
+        c.pointer(post_bias);
+    }
+    if (normed) {
+        c.pointer(pre_weight);
+        c.pointer(pre_bias);
+    }
+    c.pointer(scale);
+    if (c.status() != CTCONV_OK) return c.status();
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.h = h;
+    a.post_w = post_weight;
+    a.post_b = post_bias;
+    a.scale = scale;
+    a.gate = gate;
+    a.pre_w = pre_weight;
+    a.pre_b = pre_bias;
+    a.x_out = x_out;
+    a.y = y;
+    a.xs = strides[0];
+    a.hs = strides[1];
+    a.gs = strides[2];
+    a.os = strides[3];
+    a.ys = strides[4];
+    a.rows = rows;
+    a.rows_per_gate = gated ? rows_per_gate : 1;
+    a.C = (int)C;
+    a.post = kinds[0];
+    a.pre = kinds[1];
+    a.gate_fn = kinds[2];
+    a.eps = eps;
+    a.inv_C = (float)(1.0 / (double)C);
+    return to_status(launch_norm(a, dtype, vec, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -29,11 +29,17 @@ EXPORTED = (
     "ctconv_depthwise_forward_kernel", "ctconv_depthwise_query_kernel",
     "ctconv_workspace_bytes", "ctconv_forward_ws", "ctconv_forward_noalloc",
     "ctconv_scratch_bytes", "ctconv_clock_probe_bytes", "ctconv_clock_probe",
+    "ctconv_cache_append", "ctconv_paged_attention_workspace_bytes", "ctconv_paged_attention",
+    "ctconv_cache_evict", "ctconv_cross_attention_workspace_bytes", "ctconv_cross_attention",
+    "ctconv_norm_residual",
 )
 
 DW_AUTO, DW_ROW, DW_ELEMENT = 0, 1, 2
 
 ACT_NONE, ACT_ELU = 0, 1
+
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+GATE_NONE, GATE_LINEAR, GATE_SIGMOID, GATE_TANH = 0, 1, 2, 3
 
 
 class CtconvError(RuntimeError):
@@ -112,6 +118,28 @@ def load(path: str = LIB_PATH):
     lib.ctconv_istft_normalize.argtypes = [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_int,
                                            c_vp]
     lib.ctconv_istft_normalize.restype = c_int
+    c_sz, c_f = ctypes.c_size_t, ctypes.c_float
+    lib.ctconv_cache_append.argtypes = [c_vp] * 10 + [c_i64] * 7 + [_i64p, _i64p, c_i64, _i64p,
+                                                                    c_int, c_vp]
+    lib.ctconv_cache_append.restype = c_int
+    lib.ctconv_paged_attention_workspace_bytes.argtypes = [c_i64] * 6 + [
+        c_int, c_int, ctypes.POINTER(c_sz)]
+    lib.ctconv_paged_attention_workspace_bytes.restype = c_int
+    lib.ctconv_paged_attention.argtypes = [c_vp] * 8 + [c_i64] * 9 + [
+        _i64p, _i64p, _i64p, c_i64, _i64p, c_f, c_int, c_vp, c_sz, c_vp]
+    lib.ctconv_paged_attention.restype = c_int
+    lib.ctconv_cache_evict.argtypes = [c_vp] * 11 + [c_i64] * 10 + [_i64p, c_i64, _i64p, _i64p,
+                                                                    c_int, c_vp]
+    lib.ctconv_cache_evict.restype = c_int
+    lib.ctconv_cross_attention_workspace_bytes.argtypes = [c_i64] * 6 + [c_int,
+                                                                         ctypes.POINTER(c_sz)]
+    lib.ctconv_cross_attention_workspace_bytes.restype = c_int
+    lib.ctconv_cross_attention.argtypes = [c_vp] * 7 + [c_i64] * 6 + [_i64p] * 4 + [
+        c_i64, c_f, c_int, c_vp, c_sz, c_vp]
+    lib.ctconv_cross_attention.restype = c_int
+    lib.ctconv_norm_residual.argtypes = [c_vp] * 10 + [c_i64, c_i64, _i64p, c_i64, c_int, c_int,
+                                                       c_int, c_f, c_int, c_vp]
+    lib.ctconv_norm_residual.restype = c_int
     _lib = lib
     return lib
 
@@ -653,3 +681,431 @@ class ConvWS(Conv):
                       self.ndim, *self._args, self.dtype, self.act, ws_ptr, ws_bytes, stream)
         if st != 0:
             raise CtconvError("ctconv_forward_ws", st)
+
+
+# ---------------------------------------------------------------------------
+# The transformer block of a streaming decoder: plans (arguments marshalled
+# once, called with raw pointers, like Conv) and torch helpers.
+# ---------------------------------------------------------------------------
+
+
+def _strides(given, default):
+    return _arr(default if given is None else given)
+
+
+def _scale(scale, D: int) -> float:
+    return float(D) ** -0.5 if scale is None else float(scale)
+
+
+class _Paged:
+    """Sizes and strides of a paged cache.  Without strides: pages of
+    [Hkv, page_size, D], a dense table, dense [B, Hkv, slots] slot arrays."""
+
+    def _cache(self, B, Hkv, D, num_pages, page_size, max_pages, kv_strides, table_stride,
+               slot_strides):
+        self.B, self.Hkv, self.D = int(B), int(Hkv), int(D)
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.max_pages = int(max_pages)
+        self.slots = self.page_size * self.max_pages
+        self._kv = _strides(kv_strides, (self.Hkv * self.page_size * self.D, self.D,
+                                         self.page_size * self.D))
+        self._table = self.max_pages if table_stride is None else int(table_stride)
+        self._slot = _strides(slot_strides, (self.Hkv * self.slots, self.slots))
+
+
+class CacheAppend(_Paged):
+    """ctconv_cache_append for one shape: n new rows [B, n, Hkv, D] per sequence at most."""
+
+    def __init__(self, B: int, n: int, Hkv: int, D: int, num_pages: int, page_size: int,
+                 max_pages: int, dtype: int = CTCONV_F32, new_strides=None, kv_strides=None,
+                 table_stride=None, slot_strides=None):
+        self._cache(B, Hkv, D, num_pages, page_size, max_pages, kv_strides, table_stride,
+                    slot_strides)
+        self.n, self.dtype = int(n), dtype
+        new = _strides(new_strides, (self.n * self.Hkv * self.D, self.Hkv * self.D, self.D))
+        self._args = (self.B, self.n, self.Hkv, self.D, self.num_pages, self.page_size,
+                      self.max_pages, new, self._kv, self._table, self._slot, dtype)
+        self._fn = load().ctconv_cache_append
+
+    def __call__(self, k_new_ptr, v_new_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, counts_ptr,
+                 now_ptr, positions_ptr, weight_ptr, stream: int) -> None:
+        st = self._fn(k_new_ptr, v_new_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, counts_ptr,
+                      now_ptr, positions_ptr, weight_ptr, *self._args, stream)
+        if st != 0:
+            raise CtconvError("ctconv_cache_append", st)
+
+
+def ctconv_paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_length: int,
+                                           window: int, weights: bool, dtype: int) -> int:
+    nb = ctypes.c_size_t(0)
+    _check("ctconv_paged_attention_workspace_bytes",
+           load().ctconv_paged_attention_workspace_bytes(B, Hq, Hkv, D, max_length, window,
+                                                         int(bool(weights)), dtype,
+                                                         ctypes.byref(nb)))
+    return int(nb.value)
+
+
+class PagedAttention(_Paged):
+    """ctconv_paged_attention for one shape.  weights: whether calls pass a
+    weight_sum (the workspace then holds the scores).  scale: D ** -0.5."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, D: int, num_pages: int, page_size: int,
+                 max_pages: int, max_length=None, window: int = 0, scale=None,
+                 weights: bool = False, dtype: int = CTCONV_F32, q_strides=None,
+                 kv_strides=None, out_strides=None, table_stride=None, slot_strides=None):
+        self._cache(B, Hkv, D, num_pages, page_size, max_pages, kv_strides, table_stride,
+                    slot_strides)
+        self.Hq, self.window, self.dtype = int(Hq), int(window), dtype
+        self.max_length = self.slots if max_length is None else int(max_length)
+        self.weights = bool(weights)
+        dense = (self.Hq * self.D, self.D)
+        self.workspace_bytes = ctconv_paged_attention_workspace_bytes(
+            self.B, self.Hq, self.Hkv, self.D, self.max_length, self.window, self.weights, dtype)
+        self._args = (self.B, self.Hq, self.Hkv, self.D, self.num_pages, self.page_size,
+                      self.max_pages, self.max_length, self.window, _strides(q_strides, dense),
+                      self._kv, _strides(out_strides, dense), self._table, self._slot,
+                      _scale(scale, self.D), dtype)
+        self._fn = load().ctconv_paged_attention
+
+    def __call__(self, q_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, out_ptr, lse_ptr, weight_ptr,
+                 ws_ptr, ws_bytes: int, stream: int) -> None:
+        st = self._fn(q_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, out_ptr, lse_ptr, weight_ptr,
+                      *self._args, ws_ptr, ws_bytes, stream)
+        if st != 0:
+            raise CtconvError("ctconv_paged_attention", st)
+
+
+class CacheEvict(_Paged):
+    """ctconv_cache_evict for one shape.  Without out_slot_strides the results
+    are dense [B, Hkv, keep]; in place, pass slot_strides for both."""
+
+    def __init__(self, B: int, Hkv: int, D: int, num_pages: int, page_size: int, max_pages: int,
+                 keep: int, max_length=None, sink: int = 0, recent: int = 0,
+                 dtype: int = CTCONV_F32, kv_strides=None, table_stride=None, slot_strides=None,
+                 out_slot_strides=None):
+        self._cache(B, Hkv, D, num_pages, page_size, max_pages, kv_strides, table_stride,
+                    slot_strides)
+        self.keep, self.sink, self.recent, self.dtype = int(keep), int(sink), int(recent), dtype
+        self.max_length = self.slots if max_length is None else int(max_length)
+        out = _strides(out_slot_strides, (self.Hkv * self.keep, self.keep))
+        self._args = (self.B, self.Hkv, self.D, self.num_pages, self.page_size, self.max_pages,
+                      self.max_length, self.keep, self.sink, self.recent, self._kv, self._table,
+                      self._slot, out, dtype)
+        self._fn = load().ctconv_cache_evict
+
+    def __call__(self, k_ptr, v_ptr, table_ptr, lengths_ptr, now_ptr, weight_ptr, positions_ptr,
+                 weight_out_ptr, positions_out_ptr, lengths_out_ptr, source_ptr,
+                 stream: int) -> None:
+        st = self._fn(k_ptr, v_ptr, table_ptr, lengths_ptr, now_ptr, weight_ptr, positions_ptr,
+                      weight_out_ptr, positions_out_ptr, lengths_out_ptr, source_ptr, *self._args,
+                      stream)
+        if st != 0:
+            raise CtconvError("ctconv_cache_evict", st)
+
+
+def ctconv_cross_attention_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: int,
+                                           dtype: int) -> int:
+    nb = ctypes.c_size_t(0)
+    _check("ctconv_cross_attention_workspace_bytes",
+           load().ctconv_cross_attention_workspace_bytes(B, Lq, Lk, Hq, Hkv, D, dtype,
+                                                         ctypes.byref(nb)))
+    return int(nb.value)
+
+
+class CrossAttention:
+    """ctconv_cross_attention for one shape; dense [B, L, H, D] tensors without strides."""
+
+    def __init__(self, B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: int, scale=None,
+                 dtype: int = CTCONV_F32, q_strides=None, k_strides=None, v_strides=None,
+                 out_strides=None, mask_stride=None):
+        self.B, self.Lq, self.Lk, self.Hq = int(B), int(Lq), int(Lk), int(Hq)
+        self.Hkv, self.D, self.dtype = int(Hkv), int(D), dtype
+        q = (self.Lq * self.Hq * self.D, self.Hq * self.D, self.D)
+        k = (self.Lk * self.Hkv * self.D, self.Hkv * self.D, self.D)
+        self.workspace_bytes = ctconv_cross_attention_workspace_bytes(
+            self.B, self.Lq, self.Lk, self.Hq, self.Hkv, self.D, dtype)
+        self._args = (self.B, self.Lq, self.Lk, self.Hq, self.Hkv, self.D,
+                      _strides(q_strides, q), _strides(k_strides, k), _strides(v_strides, k),
+                      _strides(out_strides, q),
+                      self.Lk if mask_stride is None else int(mask_stride),
+                      _scale(scale, self.D), dtype)
+        self._fn = load().ctconv_cross_attention
+
+    def __call__(self, q_ptr, k_ptr, v_ptr, lengths_ptr, mask_ptr, out_ptr, lse_ptr, ws_ptr,
+                 ws_bytes: int, stream: int) -> None:
+        st = self._fn(q_ptr, k_ptr, v_ptr, lengths_ptr, mask_ptr, out_ptr, lse_ptr, *self._args,
+                      ws_ptr, ws_bytes, stream)
+        if st != 0:
+            raise CtconvError("ctconv_cross_attention", st)
+
+
+class NormResidual:
+    """ctconv_norm_residual for one shape; dense rows without strides
+    (strides: of x, h, gate, x_out, y)."""
+
+    def __init__(self, rows: int, C: int, post: int = NORM_NONE, pre: int = NORM_LAYER,
+                 gate: int = GATE_NONE, rows_per_gate: int = 1, eps: float = 1e-5,
+                 dtype: int = CTCONV_F32, strides=None):
+        self.rows, self.C, self.dtype = int(rows), int(C), dtype
+        self.post, self.pre, self.gate = post, pre, gate
+        self._args = (self.rows, self.C, _strides(strides, (self.C,) * 5), int(rows_per_gate),
+                      post, pre, gate, float(eps), dtype)
+        self._fn = load().ctconv_norm_residual
+
+    def __call__(self, x_ptr, h_ptr, post_weight_ptr, post_bias_ptr, scale_ptr, gate_ptr,
+                 pre_weight_ptr, pre_bias_ptr, x_out_ptr, y_ptr, stream: int) -> None:
+        st = self._fn(x_ptr, h_ptr, post_weight_ptr, post_bias_ptr, scale_ptr, gate_ptr,
+                      pre_weight_ptr, pre_bias_ptr, x_out_ptr, y_ptr, *self._args, stream)
+        if st != 0:
+            raise CtconvError("ctconv_norm_residual", st)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_ready(name, t, dtype, device, dims: int):
+    """t with a contiguous last dimension, unchanged otherwise (its strides are passed on)."""
+    _check_tensor(name, t, dtype, device)
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _index(name, t, device, shape, dtype=None):
+    """An int32 (or `dtype`) array of `shape` whose last dimension is contiguous, or None."""
+    if t is None:
+        return None
+    torch = _torch()
+    _check_tensor(name, t, torch.int32 if dtype is None else dtype, device, shape=shape)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _cache_tensors(k_cache, v_cache, page_table, dtype, device):
+    """(num_pages, page_size, max_pages, Hkv, D, kv_strides) of a cache held as two
+    [num_pages, Hkv, page_size, D] tensors of the same strides."""
+    torch = _torch()
+    _rows_ready("k_cache", k_cache, dtype, device, 4)
+    _rows_ready("v_cache", v_cache, dtype, device, 4)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    _rows_ready("page_table", page_table, torch.int32, device, 2)
+    num_pages, Hkv, page_size, D = k_cache.shape
+    st = k_cache.stride()
+    return num_pages, page_size, page_table.shape[1], Hkv, D, (st[0], st[2], st[1])
+
+
+def _slot_arrays(arrays, B, Hkv, slots, device):
+    """Strides shared by the given [B, Hkv, slots] arrays (name, tensor, dtype)."""
+    strides = None
+    for name, t, dtype in arrays:
+        if t is None:
+            continue
+        _index(name, t, device, (B, Hkv, slots), dtype)
+        if strides is not None and t.stride()[:2] != strides:
+            raise ValueError(f"{name} must have the strides of the other slot arrays")
+        strides = t.stride()[:2]
+    return strides
+
+
+def _workspace(workspace, need: int, device):
+    torch = _torch()
+    if need == 0:
+        return None
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes; "
+                         f"the call needs {need}")
+    return workspace
+
+
+def _result(out, shape, dtype, device, name="out"):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_tensor(name, out, dtype, device, shape=shape)
+    return _rows_ready(name, out, dtype, device, len(shape))
+
+
+def cache_append(k_new, v_new, k_cache, v_cache, page_table, lengths, counts=None, now=None,
+                 positions=None, weight_sum=None, stream=None) -> None:
+    """Append k_new, v_new [B, n, Hkv, D] to the cache (see ctconv_cache_append).
+
+    k_cache, v_cache [num_pages, Hkv, page_size, D] (any strides with a
+    contiguous last dimension), page_table int32 [B, max_pages], lengths,
+    counts, now int32 [B]; positions int32 and weight_sum fp32
+    [B, Hkv, max_pages * page_size].  lengths already counts the new rows."""
+    torch = _torch()
+    dev, dt = k_new.device, k_new.dtype
+    if not k_new.is_cuda:
+        raise ValueError("k_new must be a device tensor")
+    _rows_ready("k_new", k_new, dt, dev, 4)
+    _rows_ready("v_new", v_new, dt, dev, 4)
+    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
+        k_new, v_new = k_new.contiguous(), v_new.contiguous()
+        if v_new.shape != k_new.shape:
+            raise ValueError("k_new and v_new must have the same shape")
+    B, n, Hkv, D = k_new.shape
+    pages, size, cols, H, Dc, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
+    if (H, Dc) != (Hkv, D) or page_table.shape[0] != B:
+        raise ValueError("the cache's heads, width or table rows do not match k_new")
+    for name, t in (("lengths", lengths), ("counts", counts), ("now", now)):
+        _index(name, t, dev, (B,))
+    slots = _slot_arrays((("positions", positions, torch.int32),
+                          ("weight_sum", weight_sum, torch.float32)), B, Hkv, cols * size, dev)
+    plan = CacheAppend(B, n, Hkv, D, pages, size, cols, dtype_code(k_new), k_new.stride()[:3], kv,
+                       page_table.stride(0), slots)
+    side = _side_stream(stream, dev)
+    plan(k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         page_table.data_ptr(), lengths.data_ptr(), _ptr(counts), _ptr(now), _ptr(positions),
+         _ptr(weight_sum), _stream(stream))
+    _claim(side, k_new, v_new, k_cache, v_cache, page_table, lengths, counts, now, positions,
+           weight_sum)
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lengths, max_length=None, window: int = 0,
+                    scale=None, weight_sum=None, out=None, workspace=None, stream=None):
+    """(out [B, Hq, D], lse fp32 [B, Hq]) of one new row per sequence over the
+    paged cache (see ctconv_paged_attention); weight_sum fp32 [B, Hkv, slots]
+    or None is added to.  max_length: a bound on lengths, default the table's
+    capacity.  workspace: None (allocated here) or a device tensor."""
+    torch = _torch()
+    dev, dt = q.device, q.dtype
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    _rows_ready("q", q, dt, dev, 3)
+    B, Hq, D = q.shape
+    pages, size, cols, Hkv, Dc, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
+    if Dc != D or page_table.shape[0] != B:
+        raise ValueError("the cache's width or table rows do not match q")
+    _index("lengths", lengths, dev, (B,))
+    slots = _slot_arrays((("weight_sum", weight_sum, torch.float32),), B, Hkv, cols * size, dev)
+    y = _result(out, (B, Hq, D), dt, dev)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    plan = PagedAttention(B, Hq, Hkv, D, pages, size, cols, max_length, window, scale,
+                          weight_sum is not None, dtype_code(q), q.stride()[:2], kv,
+                          y.stride()[:2], page_table.stride(0), slots)
+    ws = _workspace(workspace, plan.workspace_bytes, dev)
+    side = _side_stream(stream, dev)
+    plan(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+         lengths.data_ptr(), y.data_ptr(), lse.data_ptr(), _ptr(weight_sum), _ptr(ws),
+         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _claim(side, q, k_cache, v_cache, page_table, lengths, y, lse, weight_sum, ws)
+    return y, lse
+
+
+def cache_evict(k_cache, v_cache, page_table, lengths, weight_sum, keep: int, positions=None,
+                now=None, sink: int = 0, recent: int = 0, max_length=None, stream=None):
+    """Cut the cache back to `keep` slots per head, in place (see
+    ctconv_cache_evict): the rows move in k_cache and v_cache, and weight_sum,
+    positions and lengths are updated.  Returns source int32 [B, Hkv, keep].
+    weight_sum fp32 and positions int32 (or None) [B, Hkv, slots]."""
+    torch = _torch()
+    dev, dt = k_cache.device, k_cache.dtype
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a device tensor")
+    pages, size, cols, Hkv, D, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
+    B, slots = page_table.shape[0], cols * size
+    if weight_sum is None:
+        raise ValueError("weight_sum is required")
+    if not 1 <= keep <= slots:
+        raise ValueError(f"keep must be between 1 and the table's {slots} slots")
+    for name, t in (("lengths", lengths), ("now", now)):
+        _index(name, t, dev, (B,))
+    st = _slot_arrays((("weight_sum", weight_sum, torch.float32),
+                       ("positions", positions, torch.int32)), B, Hkv, slots, dev)
+    source = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+    plan = CacheEvict(B, Hkv, D, pages, size, cols, keep, max_length, sink, recent,
+                      dtype_code(k_cache), kv, page_table.stride(0), st, st)
+    side = _side_stream(stream, dev)
+    plan(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
+         _ptr(now), weight_sum.data_ptr(), _ptr(positions), weight_sum.data_ptr(),
+         _ptr(positions), lengths.data_ptr(), source.data_ptr(), _stream(stream))
+    _claim(side, k_cache, v_cache, page_table, lengths, now, weight_sum, positions, source)
+    return source
+
+
+def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, workspace=None,
+                    stream=None):
+    """(out [B, Lq, Hq, D], lse fp32 [B, Hq, Lq]) of q [B, Lq, Hq, D] over
+    k, v [B, Lk, Hkv, D] (see ctconv_cross_attention); lengths int32 [B] or
+    None; mask bool or uint8 [B, Lk] or None (True: seen)."""
+    torch = _torch()
+    dev, dt = q.device, q.dtype
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _rows_ready(name, t, dt, dev, 4)
+    B, Lq, Hq, D = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    if tuple(k.shape) != (B, Lk, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, Lk, Hkv, D] with q's batch and width")
+    _index("lengths", lengths, dev, (B,))
+    if mask is not None:
+        if mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _index("mask", mask, dev, (B, Lk), torch.uint8)
+    y = _result(out, (B, Lq, Hq, D), dt, dev)
+    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=dev)
+    plan = CrossAttention(B, Lq, Lk, Hq, Hkv, D, scale, dtype_code(q), q.stride()[:3],
+                          k.stride()[:3], v.stride()[:3], y.stride()[:3],
+                          None if mask is None else mask.stride(0))
+    ws = _workspace(workspace, plan.workspace_bytes, dev)
+    side = _side_stream(stream, dev)
+    plan(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(lengths), _ptr(mask), y.data_ptr(),
+         lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+         _stream(stream))
+    _claim(side, q, k, v, lengths, mask, y, lse, ws)
+    return y, lse
+
+
+def norm_residual(x, h, post: int = NORM_NONE, post_weight=None, post_bias=None, scale=None,
+                  gate=None, gate_fn: int = GATE_NONE, rows_per_gate: int = 1,
+                  pre: int = NORM_LAYER, pre_weight=None, pre_bias=None, eps: float = 1e-5,
+                  x_out=None, y=None, stream=None):
+    """(x + scale * g(gate) * post(h), pre of that) row by row (see
+    ctconv_norm_residual); x, h [..., C], gate [ceil(rows / rows_per_gate), C],
+    the rest [C].  The second result is None when pre is NORM_NONE.  x_out may
+    be x and y may be h."""
+    torch = _torch()
+    dev, dt = x.device, x.dtype
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    _check_tensor("h", h, dt, dev, shape=tuple(x.shape))
+    C = x.shape[-1]
+    rows = x.numel() // C if C else 0
+    for name, t in (("x_out", x_out), ("y", y)):
+        if t is not None:
+            _check_tensor(name, t, dt, dev, shape=tuple(x.shape))
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    x, h = x.contiguous(), h.contiguous()
+    if (gate is None) != (gate_fn == GATE_NONE):
+        raise ValueError("gate and gate_fn go together")
+    if gate is not None:
+        groups = -(-rows // rows_per_gate) if rows_per_gate > 0 else 0
+        _check_tensor("gate", gate, dt, dev, numel=groups * C)
+        gate = gate.contiguous()
+    params = []
+    for name, t in (("post_weight", post_weight), ("post_bias", post_bias), ("scale", scale),
+                    ("pre_weight", pre_weight), ("pre_bias", pre_bias)):
+        if t is not None:
+            _check_tensor(name, t, dt, dev, numel=C)
+            t = t.contiguous()
+        params.append(t)
+    pw, pb, sc, nw, nb = params
+    xo = torch.empty_like(x) if x_out is None else x_out
+    yo = None if pre == NORM_NONE else torch.empty_like(x) if y is None else y
+    plan = NormResidual(rows, C, post, pre, gate_fn, rows_per_gate, eps, dtype_code(x))
+    side = _side_stream(stream, dev)
+    plan(x.data_ptr(), h.data_ptr(), _ptr(pw), _ptr(pb), _ptr(sc), _ptr(gate), _ptr(nw), _ptr(nb),
+         xo.data_ptr(), _ptr(yo), _stream(stream))
+    _claim(side, x, h, gate, pw, pb, sc, nw, nb, xo, yo)
+    return xo, yo
