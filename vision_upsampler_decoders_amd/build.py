@@ -33,7 +33,7 @@ FLAGS = [
 
 SOURCES = ["ctconv_api.hip", "prepack.hip", "gather.hip", "pointwise.hip", "stream.hip",
            "depthwise.hip", "polyphase.hip", "polyrw.hip", "noalloc.hip", "clock.hip"]
-BLOCK_SOURCES = ["block_api.hip", "norm.hip", "cache.hip", "attn_stream.hip"]
+BLOCK_SOURCES = ["block_api.hip", "norm.hip", "cache.hip", "attn_stream.hip", "attn_tile.hip"]
 HEADERS = [os.path.join(CSRC, "ctconv_internal.h"), os.path.join(CSRC, "mfma_common.h"),
            os.path.join(INCLUDE, "ctconv.h")]
 

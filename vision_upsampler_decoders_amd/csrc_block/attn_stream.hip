@@ -34,7 +34,7 @@ using mfma::Mma;
 using mfma::u32x2;
 using mfma::u32x4;
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;  // of the join kernels
 constexpr int kThreads = 64 * kWaves;
 constexpr float kRaise = 8.f;
 
@@ -49,8 +49,8 @@ __device__ inline void visible(const AttnArgs& a, int b, int& first, int& span) 
     span = n - first;
 }
 
-template <class TR, int DP, bool PAGED, bool EXACT>
-__global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
+template <class TR, int DP, bool PAGED, bool EXACT, int NW>
+__global__ __launch_bounds__(64 * NW) void stream_kernel(AttnArgs a) {
     using S = typename TR::storage;
     constexpr int ES = sizeof(S), VEC = 16 / ES;
     constexpr int KB = ES == 2 ? 32 : 16;  // keys per block
@@ -64,9 +64,14 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 15, g = lane >> 4;
+    // Splits slowest: workgroups go to the XCDs in turn, and the late splits
+    // of ragged sequences, which are empty, must not all fall to the same
+    // ones (splits fastest, 16 of them: 212 us instead of 157 for 48 ragged
+    // sequences up to 8192).
     int item = blockIdx.x;
-    const int split = item % a.splits;
-    item /= a.splits;
+    const int tiles = a.B * a.Hkv * a.row_tiles;
+    const int split = item / tiles;
+    item -= split * tiles;
     const int tile = item % a.row_tiles;
     const int bh = item / a.row_tiles;
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
@@ -85,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     int64_t* offs = reinterpret_cast<int64_t*>(lds);
     uint32_t* seen = reinterpret_cast<uint32_t*>(lds + (PAGED ? (size_t)a.chunk * 8 : 0));
     const int padded = (n + 63) & ~63;
-    for (int i = tid; i < padded; i += kThreads) {
+    for (int i = tid; i < padded; i += (64 * NW)) {
         bool ok = i < n;
         const int t = first + start + i;
         if constexpr (PAGED) {
@@ -131,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     float m = -__builtin_huge_valf(), l = 0.f;
     const int t0 = first + start;
 
-    for (int kb = wave * KB; kb < n; kb += kWaves * KB) {
+    for (int kb = wave * KB; kb < n; kb += NW * KB) {
         uint32_t bits = seen[kb >> 5];
         if (KB == 16) bits = (bits >> (kb & 16)) & 0xFFFFu;
         const uint32_t all = KB == 32 ? 0xFFFFFFFFu : 0xFFFFu;
@@ -260,9 +265,9 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     // sums, then [row] merged ones.
     __syncthreads();  // offs and seen are no longer read
     float* mo = reinterpret_cast<float*>(lds);
-    float* mm = mo + kWaves * rows * DS;
-    float* ml = mm + kWaves * 16;
-    float* jm = ml + kWaves * 16;  // [16] maximum, [16] sum
+    float* mm = mo + NW * rows * DS;
+    float* ml = mm + NW * 16;
+    float* jm = ml + NW * 16;  // [16] maximum, [16] sum
     if (col < rows) {
         float* o = mo + (wave * rows + col) * DS;
 #pragma unroll
@@ -280,10 +285,10 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     if (tid < rows) {
         float top = mm[tid];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, mm[w * 16 + tid]);
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w * 16 + tid]);
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float mw = mm[w * 16 + tid];
             const float f = mw == -__builtin_huge_valf() ? 0.f : exp2_fast(mw - top);
             sum += f * ml[w * 16 + tid];
@@ -299,11 +304,11 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     }
     __syncthreads();
     const int pieces = a.D / 4;
-    for (int i = tid; i < rows * pieces; i += kThreads) {
+    for (int i = tid; i < rows * pieces; i += (64 * NW)) {
         const int r = i / pieces, d = (i - r * pieces) * 4;
         f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = mm[w * 16 + r];
             const f32x4 x = *reinterpret_cast<const f32x4*>(mo + (w * rows + r) * DS + d);
 #pragma unroll
@@ -333,33 +338,135 @@ __global__ __launch_bounds__(kThreads) void stream_kernel(AttnArgs a) {
     }
 }
 
-// Join: one workgroup per query row adds the splits' outputs in ascending
-// order within each of its lane groups, and the groups in ascending order.
+// Join.  A row's outputs are its splits' outputs weighted by 2^(m - maximum),
+// over the sum of their sums weighted the same.
+//  - Few splits of many rows: D / 4 lanes add a row's splits in ascending
+//    order, 256 / (D / 4) rows per workgroup.
+//  - Else: a workgroup per row; each of its lane groups takes every
+//    groups-th split in ascending order, then the groups are added in order.
 // The workgroups past those add the weights to weight_sum: 1024 slots each.
+constexpr int kFewSplits = 16, kManyRows = 4096;
+constexpr int kAtOnce = 4;  // splits of a row whose loads are in flight together
 constexpr int kWeightSlots = 4 * kThreads;
 constexpr int kLseRows = 256;
+constexpr int kAhead = 8;  // score rows that a weight workgroup loads ahead
 
-// Maximum and sum (relative to it) of a row over its splits; every lane of
-// the wave calls it and gets both.
-__device__ inline void join_stats(const float* ml, int64_t stride, int n, float& top, float& sum) {
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Maximum and sum (relative to it) of each of N rows over its splits; every
+// lane of the wave calls it and gets both.  Up to 128 splits, of all N rows,
+// are read in one go.
+template <int N>
+__device__ inline void join_stats(const float* const (&ml)[N], int64_t stride, int n,
+                                  float (&top)[N], float (&sum)[N]) {
     const int lane = threadIdx.x & 63;
-    top = -__builtin_huge_valf();
-    for (int s = lane; s < n; s += 64) top = fmaxf(top, ml[2 * s * stride]);
+    f32x2 v[N][2];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    sum = 0.f;
-    for (int s = lane; s < n; s += 64) {
-        const float m = ml[2 * s * stride];
-        if (m != -__builtin_huge_valf()) sum += exp2_fast(m - top) * ml[2 * s * stride + 1];
+    for (int r = 0; r < N; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t s = lane + 64 * i < n ? lane + 64 * i : 0;
+            v[r][i] = *reinterpret_cast<const f32x2*>(ml[r] + 2 * s * stride);
+        }
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane + 64 * i >= n) v[r][i] = f32x2{-__builtin_huge_valf(), 0.f};
+        top[r] = fmaxf(v[r][0][0], v[r][1][0]);
+        for (int s = lane + 128; s < n; s += 64) top[r] = fmaxf(top[r], ml[r][2 * s * stride]);
     }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < N; ++r) top[r] = fmaxf(top[r], __shfl_xor(top[r], o));
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        sum[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (v[r][i][0] != -__builtin_huge_valf())
+                sum[r] += exp2_fast(v[r][i][0] - top[r]) * v[r][i][1];
+        for (int s = lane + 128; s < n; s += 64) {
+            const float m = ml[r][2 * s * stride];
+            if (m != -__builtin_huge_valf()) sum[r] += exp2_fast(m - top[r]) * ml[r][2 * s * stride + 1];
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < N; ++r) sum[r] += __shfl_xor(sum[r], o);
+}
+
+// One row's joined values of 4 value columns, and its log-sum-exp.
+template <class TR>
+__device__ inline void join_write(const AttnArgs& a, int b, int h, int r, int d, f32x4 o, float top,
+                                  float sum) {
+    using S = typename TR::storage;
+    const int lq = (int)fdiv((uint32_t)r, a.fd_G);
+    const int hq = h * a.G + (r - lq * a.G);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row + (int64_t)hq * a.o_head + d;
+    if constexpr (sizeof(S) == 2) {
+        u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv), mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
+        *reinterpret_cast<u32x2*>(to) = w;
+    } else {
+        *reinterpret_cast<f32x4*>(to) = o * inv;
+    }
+    if (d == 0 && a.lse)
+        a.lse[((int64_t)b * a.Hq + hq) * a.Lq + lq] = top * kLn2 + logf(sum);
+}
+
+template <class TR, bool PAGED>
+__global__ __launch_bounds__(kThreads) void join_few_kernel(AttnArgs a) {
+    const int pieces = a.D / 4, rows = kThreads / pieces;
+    const int grp = threadIdx.x / pieces, d = (threadIdx.x - grp * pieces) * 4;
+    const int64_t i = (int64_t)blockIdx.x * rows + grp;
+    if (grp >= rows || i >= (int64_t)a.B * a.Hkv * a.R) return;
+    const int bh = (int)(i / a.R), r = (int)(i - (int64_t)bh * a.R);
+    const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+    int first, span;
+    visible<PAGED>(a, b, first, span);
+    const int n = (span + a.chunk - 1) / a.chunk;
+    const int64_t p0 = (int64_t)bh * a.splits * a.R + r;
+    // every load clamped to a split that exists, none behind a branch
+    const float* ml = a.part_ml + 2 * p0;
+    const float* po = a.part_o + p0 * a.D + d;
+    const int64_t step = (int64_t)a.R;
+    float top = -__builtin_huge_valf(), sum = 0.f;
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < n; s0 += kAtOnce) {
+        f32x2 v[kAtOnce];
+        f32x4 x[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t s = s0 + i < n ? s0 + i : n - 1;
+            v[i] = *reinterpret_cast<const f32x2*>(ml + 2 * s * step);
+            x[i] = *reinterpret_cast<const f32x4*>(po + s * step * a.D);
+        }
+        float up = top;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) up = fmaxf(up, v[i][0]);
+        if (up == -__builtin_huge_valf()) continue;
+        const float old = exp2_fast(top - up);
+        top = up;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= old;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float f = s0 + i < n ? exp2_fast(v[i][0] - top) : 0.f;
+            sum = fmaf(f, v[i][1], sum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[i][e], o[e]);
+        }
+    }
+    join_write<TR>(a, b, h, r, d, o, top, sum);
 }
 
 template <class TR, bool PAGED>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_blocks,
                                                         int weight_blocks) {
-    using S = typename TR::storage;
     __shared__ float part[kThreads * 4];
     const int tid = threadIdx.x, wave = tid >> 6;
     if ((int)blockIdx.x < out_blocks) {
@@ -370,8 +477,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
         const int n = (span + a.chunk - 1) / a.chunk;
         const int64_t p0 = (int64_t)bh * a.splits * a.R + r;
         const float* ml = a.part_ml + 2 * p0;
-        float top, sum;
-        join_stats(ml, a.R, n, top, sum);
+        const float* const rows[1] = {ml};
+        float tops[1], sums[1];
+        join_stats(rows, a.R, n, tops, sums);
+        const float top = tops[0], sum = sums[0];
         const int pieces = a.D / 4, groups = kThreads / pieces;
         const int grp = tid / pieces, d = (tid - grp * pieces) * 4;
         if (grp < groups) {
@@ -388,24 +497,12 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
             *reinterpret_cast<f32x4*>(part + 4 * tid) = o;
         }
         __syncthreads();
-        const int lq = (int)fdiv((uint32_t)r, a.fd_G);
-        const int hq = h * a.G + (r - lq * a.G);
         if (tid < pieces) {
             f32x4 o{0.f, 0.f, 0.f, 0.f};
             for (int q = 0; q < groups; ++q)
                 o += *reinterpret_cast<const f32x4*>(part + 4 * (q * pieces + tid));
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row + (int64_t)hq * a.o_head + d;
-            if constexpr (sizeof(S) == 2) {
-                u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv),
-                        mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
-                *reinterpret_cast<u32x2*>(to) = w;
-            } else {
-                *reinterpret_cast<f32x4*>(to) = o * inv;
-            }
+            join_write<TR>(a, b, h, r, d, o, top, sum);
         }
-        if (tid == 0 && a.lse)
-            a.lse[((int64_t)b * a.Hq + hq) * a.Lq + lq] = top * kLn2 + logf(sum);
         return;
     }
     // weights of paged calls (Lq = 1, R = G)
@@ -418,42 +515,65 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
     const int n = (span + a.chunk - 1) / a.chunk;
     float add[4] = {0.f, 0.f, 0.f, 0.f};
     const int i0 = blk * kWeightSlots + 4 * tid;
+    const bool mine = i0 < span;
+    float* w = a.weight_sum + b * a.slot_b + h * a.slot_h + first + i0;
+    float old[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[e] = i0 + e < span ? w[e] : 0.f;
+    const float* sr = a.scores + (int64_t)bh * a.R * a.score_stride + i0;
     float* lse2 = part;
     for (int r0 = 0; r0 < a.R; r0 += kLseRows) {
         const int rn = a.R - r0 < kLseRows ? a.R - r0 : kLseRows;
+        // the first rows' scores are on their way while the sums are joined
+        f32x4 s[kAhead];
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r)
+            if (mine && r < rn)
+                s[r] = *reinterpret_cast<const f32x4*>(sr + (int64_t)(r0 + r) * a.score_stride);
         __syncthreads();
-        for (int r = wave; r < rn; r += kWaves) {
-            float top, sum;
-            join_stats(a.part_ml + 2 * ((int64_t)bh * a.splits * a.R + r0 + r), a.R, n, top, sum);
-            if ((tid & 63) == 0)
-                lse2[r] = top == -__builtin_huge_valf() ? __builtin_huge_valf()
-                                                        : top + __builtin_amdgcn_logf(sum);
+        const float* ml = a.part_ml + 2 * ((int64_t)bh * a.splits * a.R + r0);
+        for (int r = wave; r < rn; r += 2 * kWaves) {
+            const int r2 = r + kWaves < rn ? r + kWaves : r;
+            const float* const rows[2] = {ml + 2 * r, ml + 2 * r2};
+            float top[2], sum[2];
+            join_stats(rows, a.R, n, top, sum);
+            // a row without a visible slot adds nothing: exp2(s - infinity)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if ((tid & 63) == 0)
+                    lse2[i ? r2 : r] = top[i] == -__builtin_huge_valf()
+                                           ? __builtin_huge_valf()
+                                           : top[i] + __builtin_amdgcn_logf(sum[i]);
         }
         __syncthreads();
-        if (i0 < span)
-            for (int r = 0; r < rn; ++r) {
-                const f32x4 s = *reinterpret_cast<const f32x4*>(
-                    a.scores + ((int64_t)bh * a.R + r0 + r) * a.score_stride + i0);
+        if (mine) {
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r)
+                if (r < rn) {
+                    const float z = lse2[r];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) add[e] += exp2_fast(s[r][e] - z);
+                }
+            for (int r = kAhead; r < rn; ++r) {
+                const f32x4 t =
+                    *reinterpret_cast<const f32x4*>(sr + (int64_t)(r0 + r) * a.score_stride);
                 const float z = lse2[r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) add[e] += exp2_fast(s[e] - z);
+                for (int e = 0; e < 4; ++e) add[e] += exp2_fast(t[e] - z);
             }
+        }
     }
-    float* w = a.weight_sum + b * a.slot_b + h * a.slot_h + first + i0;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (i0 + e < span) w[e] += add[e];
+        if (i0 + e < span) w[e] = old[e] + add[e];
 }
 
-template <class TR, int DP, bool PAGED>
-hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
-    const int rows = a.R < 16 ? a.R : 16;
-    const size_t stage = (PAGED ? (size_t)a.chunk * 8 : 0) + (size_t)(a.chunk / 32 + 2) * 4;
-    const size_t merge = (size_t)(kWaves * rows * (DP + 4) + 2 * kWaves * 16 + 32) * 4;
-    const size_t lds = stage > merge ? stage : merge;
+template <class TR, int DP, bool PAGED, int NW>
+hipError_t stream_w(const AttnArgs& a, size_t lds, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * a.row_tiles * a.splits));
-    const void* fn = a.D == DP ? reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, true>)
-                               : reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, false>);
+    const void* fn = a.D == DP
+                         ? reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, true, NW>)
+                         : reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, false, NW>);
     if (lds > 64u << 10) {
         const hipError_t e =
             hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -461,7 +581,22 @@ hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
     }
     AttnArgs args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, grid, dim3(kThreads), params, lds, s);
+    return hipLaunchKernel(fn, grid, dim3(64 * NW), params, lds, s);
+}
+
+template <class TR, int DP, bool PAGED>
+hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
+    const int rows = a.R < 16 ? a.R : 16;
+    const size_t stage = (PAGED ? (size_t)a.chunk * 8 : 0) + (size_t)(a.chunk / 32 + 2) * 4;
+    const auto lds = [&](int nw) {
+        const size_t merge = (size_t)(nw * rows * (DP + 4) + 2 * nw * 16 + 32) * 4;
+        return stage > merge ? stage : merge;
+    };
+    // as many waves as the registers allow (512 per lane and SIMD)
+    constexpr int WIDE = DP <= 64 ? 16 : DP <= 128 ? 8 : 4;
+    if constexpr (WIDE > 4)
+        if (a.wide) return stream_w<TR, DP, PAGED, WIDE>(a, lds(WIDE), s);
+    return stream_w<TR, DP, PAGED, 4>(a, lds(4), s);
 }
 
 template <class TR, bool PAGED>
@@ -474,6 +609,12 @@ hipError_t stream_t(const AttnArgs& a, hipStream_t s) {
 template <class TR, bool PAGED>
 hipError_t join_t(const AttnArgs& a, hipStream_t s) {
     const int out_blocks = a.B * a.Hkv * a.R;
+    if (a.splits <= kFewSplits && out_blocks >= kManyRows && !a.weight_sum) {
+        const int rows = kThreads / (a.D / 4);
+        join_few_kernel<TR, PAGED><<<dim3((unsigned)((out_blocks + rows - 1) / rows)),
+                                     dim3(kThreads), 0, s>>>(a);
+        return hipGetLastError();
+    }
     const int64_t longest = a.score_stride;
     const int weight_blocks =
         a.weight_sum ? (int)((longest + kWeightSlots - 1) / kWeightSlots) : 0;

@@ -13,6 +13,8 @@ namespace {
 
 constexpr int64_t kMaxInt = INT32_MAX;
 constexpr int64_t kMaxEvictSlots = 524288;  // select_kernel's bits and sums fit LDS
+constexpr int64_t kEvictLds = 128 << 10;     // of the 160 KB, with what it declares itself
+constexpr int64_t kFusedKeep = 2048;
 constexpr int64_t kMaxRowValues = 16384;    // norm_kernel keeps a row in registers
 
 size_t esize(ctconv_dtype dt) { return dt == CTCONV_F32 ? 4 : 2; }
@@ -106,6 +108,8 @@ ctconv_status slot_strides_ok(const int64_t* strides, int64_t B, int64_t Hkv, in
 // The split of one attention call: R query rows per (sequence, cache head),
 // at most `span` visible keys.
 struct Plan {
+    bool tile;  // tile_kernel (many rows), else stream_kernel
+    bool wide;
     int64_t row_tiles, chunk, splits;
     bool direct;
     int64_t score_stride;  // floats per query row (weights), else 0
@@ -113,21 +117,64 @@ struct Plan {
     int64_t score_bytes, part_o_bytes, part_ml_bytes, bytes;
 };
 
-constexpr int64_t kTargetGroups = 2048;  // 8 workgroups per compute unit
-constexpr int64_t kMinChunk = 256, kMaxChunk = 2048;
+constexpr int64_t kTileRows = 128;  // query rows per workgroup of tile_kernel
+constexpr int64_t kTileFrom = 64;   // more rows per cache head than this: tile_kernel
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
-ctconv_status plan_stream(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span, bool weights,
-                          Plan* p) {
+// Keys per workgroup of tile_kernel.  A workgroup costs about one tile on top
+// of its own (its first loads, its last stores), and the compute units take
+// the workgroups in rounds; splitting pays a join.
+int64_t tile_chunk(int64_t tiles, int64_t keys) {
+    const int64_t cus = 256, steps = ceil_div(keys, 64);
+    int64_t best = 1, cost = INT64_MAX;
+    for (int64_t s = 1; s <= 16 && s <= ceil_div(steps, 4); ++s) {
+        const int64_t c =
+            ceil_div(tiles * s, cus) * (ceil_div(steps, s) + 1) + (s > 1 ? 4 + s : 0);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    return round_up(ceil_div(keys, best), 128);
+}
+
+// Keys per workgroup of stream_kernel.
+//  - One workgroup of as many waves as it can have per row tile and no join,
+//    where few keys or many row tiles allow it: 500 keys on 8 tiles 9.8 us
+//    against 12.1 split, 1000 keys on 256 tiles 28 against 32; but 2000 keys on
+//    64 tiles 25 against 20 (bf16, D = 128).
+//  - Else chunks that give every compute unit one round of the workgroups its
+//    registers hold (4, 2 or 1 of 4 waves for D up to 64, 128, 256): 30000
+//    keys on 8 tiles take 33 us in 469 workgroups, 40 in 938.  At least 256
+//    keys (a workgroup's start costs about as much as 128), at most 1024, so
+//    that ragged sequences still spread.
+void stream_split(int64_t tiles, int64_t keys, int64_t D, int64_t* chunk, bool* wide) {
+    *wide = (keys <= 512 && tiles <= 256) || (keys <= 1024 && tiles >= 128) ||
+            (keys <= 2048 && tiles >= 256);
+    if (*wide) {
+        *chunk = round_up(keys, 128);
+        return;
+    }
+    const int64_t room = D <= 64 ? 1024 : D <= 128 ? 512 : 256;
+    const int64_t c = round_up(ceil_div(keys * tiles, room), 128);
+    *chunk = c < 256 ? 256 : c > 1024 ? 1024 : c;
+}
+
+ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span,
+                             bool weights, bool tile, Plan* p) {
     memset(p, 0, sizeof(*p));
-    p->row_tiles = ceil_div(R, 16);
+    p->tile = tile;
+    p->row_tiles = ceil_div(R, tile ? kTileRows : 16);
     const __int128 tiles = (__int128)B * Hkv * p->row_tiles;
     if (tiles > kMaxInt || (__int128)B * Hkv * R > kMaxInt) return CTCONV_ERR_SHAPE;
-    const int64_t want = tiles > 0 ? ceil_div(kTargetGroups, (int64_t)tiles) : 1;
-    int64_t chunk = round_up(ceil_div(span > 0 ? span : 1, want), 128);
-    if (chunk < kMinChunk) chunk = kMinChunk;
-    if (chunk > kMaxChunk) chunk = kMaxChunk;
+    const int64_t keys = span > 0 ? span : 1;
+    int64_t chunk;
+    if (tile) {
+        chunk = tile_chunk((int64_t)tiles, keys);
+    } else {
+        stream_split((int64_t)tiles, keys, D, &chunk, &p->wide);
+    }
     p->chunk = chunk;
     p->splits = span > 0 ? ceil_div(span, chunk) : 1;
     p->direct = p->splits == 1 && !weights;
@@ -138,7 +185,7 @@ ctconv_status plan_stream(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t 
     }
     if (!p->direct) parts = (__int128)B * Hkv * R * p->splits;
     const __int128 total = score + parts * (D + 2) * 4 + 64;
-    if (tiles * p->splits > kMaxInt || parts * D > ((__int128)1 << 61) ||
+    if (tiles * p->splits > kMaxInt - 8 || parts * D > ((__int128)1 << 61) ||
         total > ((__int128)1 << 62))
         return CTCONV_ERR_SHAPE;
     if (weights && (__int128)B * Hkv * R + (__int128)B * Hkv * ceil_div(p->score_stride, 1024) >
@@ -157,6 +204,7 @@ void apply_plan(const Plan& p, void* ws, AttnArgs* a) {
     a->chunk = (int)p.chunk;
     a->splits = (int)p.splits;
     a->direct = p.direct;
+    a->wide = p.wide;
     a->score_stride = p.score_stride;
     char* at = static_cast<char*>(ws);
     a->scores = p.score_bytes ? reinterpret_cast<float*>(at) : nullptr;
@@ -171,7 +219,7 @@ ctconv_status paged_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
     if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
     if (max_length < 0 || max_length > kMaxInt - (1 << 20) || window < 0) return CTCONV_ERR_SHAPE;
     const int64_t span = window > 0 && window < max_length ? window : max_length;
-    return plan_stream(B, Hkv, Hq / Hkv, D, span, weights, p);
+    return plan_attention(B, Hkv, Hq / Hkv, D, span, weights, false, p);
 }
 
 ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
@@ -181,7 +229,8 @@ ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t 
     if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
     if (Lq < 0 || Lq > kMaxInt || Lk < 0 || Lk > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
     if ((__int128)Lq * (Hq / Hkv) > kMaxInt) return CTCONV_ERR_SHAPE;
-    return plan_stream(B, Hkv, Lq * (Hq / Hkv), D, Lk, false, p);
+    const int64_t R = Lq * (Hq / Hkv);
+    return plan_attention(B, Hkv, R, D, Lk, false, R > kTileFrom, p);
 }
 
 }  // namespace
@@ -395,6 +444,11 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
     a.sink = (int)(sink < kMaxInt ? sink : kMaxInt);
     a.recent = (int)(recent < kMaxInt ? recent : kMaxInt);
     a.words = (int)(round_up(max_length > 0 ? max_length : 1, 1024) / 64);
+    const int64_t excess = max_length > keep ? max_length - keep : 0;
+    const int64_t moves = excess < keep ? excess : keep;
+    const int64_t room = (kEvictLds - a.words * 12) / 4;
+    a.list = (int)(moves < room ? moves : room);
+    a.fused = keep <= kFusedKeep && lengths_out != lengths;
     a.chunks = (int)(D * (int64_t)esize(dtype) / 16);
     a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
     if ((__int128)B * Hkv * ceil_div(keep, 64) > kMaxInt) return CTCONV_ERR_SHAPE;
@@ -474,7 +528,8 @@ ctconv_status ctconv_cross_attention(const void* q, const void* k, const void* v
     a.negate = scale < 0;
     apply_plan(p, workspace, &a);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    st = to_status(launch_attn_stream(a, dtype, false, s));
+    st = to_status(p.tile ? launch_attn_tile(a, dtype, s)
+                          : launch_attn_stream(a, dtype, false, s));
     if (st != CTCONV_OK || a.direct) return st;
     return to_status(launch_attn_join(a, dtype, false, s));
 }

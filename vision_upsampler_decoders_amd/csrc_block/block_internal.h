@@ -59,7 +59,9 @@ struct EvictArgs {
     Pages pages;
     int64_t slot_b, slot_h, out_b, out_h;
     int B, Hkv, D, keep, sink, recent;
-    int words;  // 64-slot words of the longest sequence
+    int words;  // 64-slot words of the longest sequence, a multiple of 16
+    int list;   // kept slots past keep that select_kernel has room to list
+    int fused;  // few slots: select_kernel fills them itself
     int chunks;
     FastDiv fd_chunks;
 };
@@ -84,9 +86,9 @@ struct AttnArgs {
     int B, Lq, Lk, Hq, Hkv, G, D, R;
     int window;
     int chunk, splits;           // keys per workgroup, workgroups per row tile
+    int wide;                    // stream kernel: a workgroup of as many waves as it can have
     int direct;                  // one workgroup per row tile, and no weights: no join
     int row_tiles;
-    int xcd;                     // sequences x heads in runs per XCD (tile kernel)
     FastDiv fd_G;
     float c;                     // |scale| * log2(e)
     int negate;                  // scale < 0: the queries change sign
@@ -106,6 +108,8 @@ hipError_t launch_evict(const EvictArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, ctconv_dtype dt, bool vec, hipStream_t s);
 // Few query rows (paged calls, single tokens): keys streamed from memory.
 hipError_t launch_attn_stream(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s);
+// Many query rows: keys and values through LDS tiles.
+hipError_t launch_attn_tile(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 // The partial results of `splits` workgroups joined, and the slots' weights.
 hipError_t launch_attn_join(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s);
 

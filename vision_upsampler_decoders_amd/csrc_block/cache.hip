@@ -78,6 +78,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kDigits = 256, kColumns = 32;
+constexpr int kBatch = 8;
+constexpr int kNear = 4096;  // keys gathered in LDS
 
 __device__ inline uint32_t rank_key(float w, bool safe) {
     if (safe) return 0xFFFFFFFFu;
@@ -134,15 +136,91 @@ __device__ inline int nth_bit(uint64_t w, int n) {
     return at;
 }
 
+// What slots j (one per lane of a wave) become, once it is known that they
+// take `src` (-1: empty): weight and position, and the rows of the holes.
+// Sources are kept slots from m on and targets lie below m, so no copy reads
+// what another one writes, in place or not.
+struct MovedRow {
+    int64_t from, to;
+};
+
+template <class S, int U>
+__device__ inline void fill_slots(const EvictArgs& a, int b, int h, const int (&j)[U],
+                                  const int (&src)[U], MovedRow* rows) {
+    constexpr int VEC = 16 / sizeof(S);
+    const int lane = threadIdx.x & 63;
+    const int64_t in = b * a.slot_b + h * a.slot_h, out = b * a.out_b + h * a.out_h;
+    float wt[U];
+    int pos[U];
+    int64_t from[U], to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = src[u] < 0 ? 0 : src[u];
+        wt[u] = a.weight_sum[in + i];
+        pos[u] = a.positions ? a.positions[in + i] : i;
+        const bool hole = src[u] >= 0 && src[u] != j[u];
+        from[u] = to[u] = -1;
+        if (hole) {
+            from[u] = slot_offset(a.pages, b, src[u]);
+            to[u] = slot_offset(a.pages, b, j[u]);
+        }
+    }
+    int count = 0;  // rows to move, listed in LDS
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (j[u] < a.keep) {
+            a.weight_out[out + j[u]] = src[u] < 0 ? 0.f : wt[u];
+            if (a.positions_out) a.positions_out[out + j[u]] = src[u] < 0 ? -1 : pos[u];
+        }
+        const bool moves = from[u] >= 0 && to[u] >= 0;
+        const uint64_t mask = __ballot(moves);
+        if (moves)
+            rows[count + __popcll(mask & ((1ull << lane) - 1))] = MovedRow{from[u], to[u]};
+        count += __popcll(mask);
+    }
+    if (count == 0) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // one wave's LDS, in order
+    const int at_once = 64 / a.chunks;
+    const int mine = (int)fdiv((uint32_t)lane, a.fd_chunks), c = lane - mine * a.chunks;
+    S* k = static_cast<S*>(a.k) + h * a.pages.head_stride + c * VEC;
+    S* v = static_cast<S*>(a.v) + h * a.pages.head_stride + c * VEC;
+    if (mine < at_once) {
+        constexpr int UNROLL = 4;
+        for (int r0 = mine; r0 < count; r0 += UNROLL * at_once) {
+            u32x4 rk[UNROLL], rv[UNROLL];
+            int64_t dst[UNROLL];
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                const int r = r0 + i * at_once;
+                const MovedRow row = rows[r < count ? r : r0];
+                dst[i] = row.to;
+                rk[i] = *reinterpret_cast<const u32x4*>(k + row.from);
+                rv[i] = *reinterpret_cast<const u32x4*>(v + row.from);
+            }
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                if (r0 + i * at_once >= count) continue;
+                *reinterpret_cast<u32x4*>(k + dst[i]) = rk[i];
+                *reinterpret_cast<u32x4*>(v + dst[i]) = rv[i];
+            }
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // KEYS > 0: the keys of up to KEYS * kSelThreads slots stay in registers;
-// KEYS = 0: computed again from memory for each pass.
-template <int KEYS>
+// KEYS = 0: computed again from memory for each pass, in a loop.  (All 40 keys
+// of 40001 slots in registers took 37 us: every pass is then straight-line
+// code that runs once, at the rate at which instructions are fetched.)
+template <class S, int KEYS>
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     extern __shared__ __align__(16) uint32_t lds[];
-    __shared__ int wave_sums[kSelWaves], found[4];
-    uint32_t* hist = lds;                                // kDigits x kColumns, first
+    __shared__ int wave_sums[kSelWaves], found[4], digits[kDigits];
+    __shared__ MovedRow rows[kSelWaves][64];
+    uint32_t* hist = lds;  // kDigits x kColumns, then kNear keys, first
     uint64_t* bits = reinterpret_cast<uint64_t*>(lds);   // then a.words, and
-    int* pre = reinterpret_cast<int*>(bits + a.words);   // a.words prefix sums
+    int* pre = reinterpret_cast<int*>(bits + a.words);   // a.words prefix sums, and
+    int* spare = pre + a.words;                          // a.list kept slots from m on
     const int bh = blockIdx.x, b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = clamped(a.lengths[b], a.pages.slots);
@@ -151,48 +229,68 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const int32_t* position = a.positions ? a.positions + b * a.slot_b + h * a.slot_h : nullptr;
     const int64_t seen = a.now ? a.now[b] : a.lengths[b];
     int32_t* source = a.source + (int64_t)bh * a.keep;
-    float* weight_out = a.weight_out + b * a.out_b + h * a.out_h;
-    int32_t* position_out = a.positions_out ? a.positions_out + b * a.out_b + h * a.out_h : nullptr;
     const bool all = n == m;
+    int moves = 0;
 
-    const auto key_of = [&](int t) {
-        const int64_t pos = position ? position[t] : t;
-        return rank_key(weight[t], pos < a.sink || pos >= seen - a.recent);
-    };
-    uint32_t keys[KEYS > 0 ? KEYS : 1];
     const int rounds = (n + kSelThreads - 1) / kSelThreads;
     if (!all) {
-        if constexpr (KEYS > 0) {
+        const auto key_of = [&](float w, int pos) {
+            return rank_key(w, pos < a.sink || (int64_t)pos >= seen - a.recent);
+        };
+        // a batch's loads in flight, none behind a branch
+        const auto load = [&](auto& keys, int i0) {
+            constexpr int N = sizeof(keys) / sizeof(keys[0]);
+            float w[N];
+            int pos[N];
 #pragma unroll
-            for (int i = 0; i < KEYS; ++i) {
-                const int t = i * kSelThreads + tid;
-                keys[i] = t < n ? key_of(t) : 0;
+            for (int i = 0; i < N; ++i) {
+                int t = (i0 + i) * kSelThreads + tid;
+                t = t < n ? t : n - 1;
+                w[i] = weight[t];
+                pos[i] = position ? position[t] : t;
             }
-        }
-        // f(slot, key, i) for every slot of this thread, whole waves at a time
+#pragma unroll
+            for (int i = 0; i < N; ++i) keys[i] = key_of(w[i], pos[i]);
+        };
+        uint32_t held[KEYS > 0 ? KEYS : kBatch];
+        if constexpr (KEYS > 0) load(held, 0);
+        // f(slot, key) for every slot of this thread, whole waves at a time
         const auto each = [&](auto f) {
             if constexpr (KEYS > 0) {
 #pragma unroll
                 for (int i = 0; i < KEYS; ++i)
-                    if (i < rounds) f(i * kSelThreads + tid, keys[i]);
+                    if (i < rounds) f(i * kSelThreads + tid, held[i]);
             } else {
-                for (int i = 0; i < rounds; ++i) {
-                    const int t = i * kSelThreads + tid;
-                    f(t, t < n ? key_of(t) : 0u);
+                for (int i0 = 0; i0 < rounds; i0 += kBatch) {
+                    load(held, i0);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        if (i0 + i < rounds) f((i0 + i) * kSelThreads + tid, held[i]);
                 }
             }
         };
-        // the m-th largest key
+        // The m-th largest key.  Once few enough keys share its digits, those
+        // are gathered in LDS and only they are counted on.
         uint32_t prefix = 0, mask = 0;
         int want = m;
         bool exact = false;  // every key with this prefix stays
+        uint32_t* near = hist + kDigits * kColumns;
+        int near_n = -1;
+        if (tid == 0) found[3] = 0;
         for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
             for (int i = tid; i < kDigits * kColumns; i += kSelThreads) hist[i] = 0;
             __syncthreads();
-            each([&](int t, uint32_t key) {
-                if (t < n && (key & mask) == prefix)
-                    atomicAdd(&hist[((key >> shift) & 255) * kColumns + (tid & (kColumns - 1))], 1u);
-            });
+            const auto count = [&](uint32_t key) {
+                atomicAdd(&hist[((key >> shift) & 255) * kColumns + (tid & (kColumns - 1))], 1u);
+            };
+            if (near_n >= 0) {
+                for (int i = tid; i < near_n; i += kSelThreads)
+                    if ((near[i] & mask) == prefix) count(near[i]);
+            } else {
+                each([&](int t, uint32_t key) {
+                    if (t < n && (key & mask) == prefix) count(key);
+                });
+            }
             __syncthreads();
             // four threads add up a digit's columns
             int c = 0;
@@ -200,15 +298,14 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 c += hist[(tid >> 2) * kColumns + (((tid & 3) + 4 * (i + (tid >> 2))) & (kColumns - 1))];
             c += __shfl_xor(c, 1);
             c += __shfl_xor(c, 2);
-            __syncthreads();
-            if ((tid & 3) == 0) hist[tid >> 2] = c;
+            if ((tid & 3) == 0) digits[tid >> 2] = c;
             __syncthreads();
             if (wave == 0) {
                 // lane l: digits 255 - 4l .. 252 - 4l, from the top
                 int d[4], sum = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    d[i] = hist[255 - 4 * lane - i];
+                    d[i] = digits[255 - 4 * lane - i];
                     sum += d[i];
                 }
                 int inc = sum;
@@ -233,6 +330,18 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             mask |= 255u << shift;
             want = found[1];
             exact = found[1] == found[2];
+            if (near_n < 0 && !exact && shift > 0 && found[2] <= kNear) {
+                near_n = found[2];
+                each([&](int t, uint32_t key) {
+                    const bool is = t < n && (key & mask) == prefix;
+                    const uint64_t w = __ballot(is);
+                    if (w == 0) return;
+                    int at = 0;  // any order: the keys are only counted
+                    if (lane == 0) at = atomicAdd(&found[3], __popcll(w));
+                    at = __builtin_amdgcn_readfirstlane(at);
+                    if (is) near[at + __popcll(w & ((1ull << lane) - 1))] = key;
+                });
+            }
             __syncthreads();
         }
         // keys from `prefix` on stay; where not `exact`, only the first
@@ -266,67 +375,101 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             pre[w] = w < edge ? __popcll(~bits[w])
                               : __popcll(w == edge ? bits[w] & ~below : bits[w]);
         __syncthreads();
-        scan_words(pre, words, wave_sums);
+        moves = scan_words(pre, words, wave_sums) - pre[edge];
     }
+    // the kept slots from m on, in order, where they fit
     const int words = (n + 63) >> 6, edge = m >> 6;
-    for (int j = tid; j < a.keep; j += kSelThreads) {
+    const int base = all ? 0 : pre[edge];
+    const uint64_t below = (1ull << (m & 63)) - 1;
+    const bool listed = moves <= a.list;
+    if (!all && listed) {
+        for (int t = m + tid; t < n; t += kSelThreads) {
+            const uint64_t w = (t >> 6) == edge ? bits[edge] & ~below : bits[t >> 6];
+            const int at = t & 63;
+            if ((w >> at) & 1)
+                spare[pre[t >> 6] - base + __popcll(w & ((1ull << at) - 1))] = t;
+        }
+        __syncthreads();
+    }
+    for (int j0 = 0; j0 < a.keep; j0 += kSelThreads) {
+        const int j = j0 + tid;
         int src = -1;
         if (j < m) {
             src = j;
             if (!all && !((bits[j >> 6] >> (j & 63)) & 1)) {
                 const int r = pre[j >> 6] + __popcll(~bits[j >> 6] & ((1ull << (j & 63)) - 1));
-                // the last word from `edge` on whose kept slots start at or before rank r
-                const int base = pre[edge];
-                int lo = edge, hi = words - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (pre[mid] - base <= r) lo = mid;
-                    else hi = mid - 1;
+                if (listed) {
+                    src = spare[r];
+                } else {
+                    // the last word from `edge` on whose kept slots start at or before rank r
+                    int lo = edge, hi = words - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (pre[mid] - base <= r) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    uint64_t w = bits[lo];
+                    if (lo == edge) w &= ~below;
+                    src = lo * 64 + nth_bit(w, r - (pre[lo] - base));
                 }
-                uint64_t w = bits[lo];
-                if (lo == edge) w &= ~((1ull << (m & 63)) - 1);
-                src = lo * 64 + nth_bit(w, r - (pre[lo] - base));
             }
         }
-        source[j] = src;
-        const float wt = src >= 0 ? weight[src] : 0.f;
-        const int pos = src < 0 ? -1 : position ? position[src] : src;
-        weight_out[j] = wt;
-        if (position_out) position_out[j] = pos;
+        if (j < a.keep) source[j] = src;
+        if (a.fused) {
+            const int js[1] = {j}, srcs[1] = {src};
+            fill_slots<S, 1>(a, b, h, js, srcs, rows[wave]);
+        }
     }
+    if (a.fused && a.lengths_out && h == 0 && tid == 0) a.lengths_out[b] = m;
 }
 
-// Second kernel: the rows of the filled holes.  Sources are kept slots from m
-// on and targets lie below m, so no copy reads what another one writes.
-constexpr int kMoveSlots = 64;
+// Second kernel: every wave fills 64 slots kFill times.
+constexpr int kFillThreads = 256, kFill = 4, kFillSlots = kFillThreads * kFill;
 
 template <class S>
-__global__ __launch_bounds__(256) void move_kernel(EvictArgs a) {
-    constexpr int VEC = 16 / sizeof(S);
-    const int tiles = (a.keep + kMoveSlots - 1) / kMoveSlots;
-    const int bh = blockIdx.x / tiles, first = (int)(blockIdx.x - (uint32_t)bh * tiles) * kMoveSlots;
+__global__ __launch_bounds__(kFillThreads) void fill_kernel(EvictArgs a) {
+    __shared__ MovedRow rows[kFillThreads / 64][64 * kFill];
+    const int tiles = (a.keep + kFillSlots - 1) / kFillSlots;
+    const int bh = blockIdx.x / tiles, tile = blockIdx.x - (uint32_t)bh * tiles;
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
-    if (a.lengths_out && h == 0 && first == 0 && threadIdx.x == 0) {
+    if (a.lengths_out && h == 0 && tile == 0 && threadIdx.x == 0) {
         // the one place that reads lengths here: lengths_out may be lengths
         const int n = clamped(a.lengths[b], a.pages.slots);
         a.lengths_out[b] = n < a.keep ? n : a.keep;
     }
     const int32_t* source = a.source + (int64_t)bh * a.keep;
-    const int slots = a.keep - first < kMoveSlots ? a.keep - first : kMoveSlots;
-    S* k = static_cast<S*>(a.k) + h * a.pages.head_stride;
-    S* v = static_cast<S*>(a.v) + h * a.pages.head_stride;
-    for (int i = threadIdx.x; i < slots * a.chunks; i += 256) {
-        const int row = (int)fdiv((uint32_t)i, a.fd_chunks);
-        const int c = i - row * a.chunks;
-        const int to = first + row, from = source[to];
-        if (from < 0 || from == to) continue;
-        const int64_t o1 = slot_offset(a.pages, b, to), o0 = slot_offset(a.pages, b, from);
-        if (o0 < 0 || o1 < 0) continue;
-        const u32x4 rk = *reinterpret_cast<const u32x4*>(k + o0 + c * VEC);
-        const u32x4 rv = *reinterpret_cast<const u32x4*>(v + o0 + c * VEC);
-        *reinterpret_cast<u32x4*>(k + o1 + c * VEC) = rk;
-        *reinterpret_cast<u32x4*>(v + o1 + c * VEC) = rv;
+    int j[kFill], src[kFill];
+#pragma unroll
+    for (int u = 0; u < kFill; ++u) {
+        j[u] = tile * kFillSlots + u * kFillThreads + threadIdx.x;
+        src[u] = source[j[u] < a.keep ? j[u] : a.keep - 1];
+        if (j[u] >= a.keep) src[u] = -1;
     }
+    fill_slots<S, kFill>(a, b, h, j, src, rows[threadIdx.x >> 6]);
+}
+
+template <class S>
+hipError_t evict_t(const EvictArgs& a, hipStream_t s) {
+    size_t lds = (size_t)a.words * 12 + (size_t)a.list * 4;
+    const size_t count = (kDigits * kColumns + kNear) * 4;
+    if (lds < count) lds = count;
+    const int slots = a.words * 64;
+    const void* fn = slots <= kSelThreads     ? reinterpret_cast<const void*>(&select_kernel<S, 1>)
+                     : slots <= 4 * kSelThreads ? reinterpret_cast<const void*>(&select_kernel<S, 4>)
+                                                : reinterpret_cast<const void*>(&select_kernel<S, 0>);
+    if (lds > 48u << 10) {
+        const hipError_t e =
+            hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    EvictArgs args = a;
+    void* params[] = {&args};
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(a.B * a.Hkv)), dim3(kSelThreads),
+                                         params, lds, s);
+    if (e != hipSuccess || a.fused) return e;
+    const int64_t tiles = ((int64_t)a.keep + kFillSlots - 1) / kFillSlots;
+    fill_kernel<S><<<dim3((unsigned)(a.B * a.Hkv * tiles)), dim3(kFillThreads), 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -341,29 +484,7 @@ hipError_t launch_append(const AppendArgs& a, ctconv_dtype dt, hipStream_t s) {
 }
 
 hipError_t launch_evict(const EvictArgs& a, ctconv_dtype dt, hipStream_t s) {
-    const dim3 grid((unsigned)(a.B * a.Hkv));
-    size_t lds = (size_t)a.words * 12;
-    if (lds < kDigits * kColumns * 4) lds = kDigits * kColumns * 4;
-    const int slots = a.words * 64;
-    const void* fn = slots <= 8 * kSelThreads    ? reinterpret_cast<const void*>(&select_kernel<8>)
-                     : slots <= 40 * kSelThreads ? reinterpret_cast<const void*>(&select_kernel<40>)
-                                                 : reinterpret_cast<const void*>(&select_kernel<0>);
-    if (lds > 64u << 10) {
-        const hipError_t e =
-            hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
-    EvictArgs args = a;
-    void* params[] = {&args};
-    hipError_t e = hipLaunchKernel(fn, grid, dim3(kSelThreads), params, lds, s);
-    if (e != hipSuccess) return e;
-    const int64_t tiles = ((int64_t)a.keep + kMoveSlots - 1) / kMoveSlots;
-    const dim3 mgrid((unsigned)(a.B * a.Hkv * tiles));
-    if (dt == CTCONV_F32)
-        move_kernel<float><<<mgrid, dim3(256), 0, s>>>(a);
-    else
-        move_kernel<uint16_t><<<mgrid, dim3(256), 0, s>>>(a);
-    return hipGetLastError();
+    return dt == CTCONV_F32 ? evict_t<float>(a, s) : evict_t<uint16_t>(a, s);
 }
 
 }  // namespace block
