@@ -199,6 +199,13 @@ ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64
     return CTCONV_OK;
 }
 
+// |scale| log2(e), not zero: hidden scores are minus infinity times it.
+// (Scores times 1e-30 weigh the same as scores times 0.)
+float score_factor(float scale) {
+    const float c = fabsf(scale) * kLog2e;
+    return c > 1e-30f ? c : 1e-30f;
+}
+
 void apply_plan(const Plan& p, void* ws, AttnArgs* a) {
     a->row_tiles = (int)p.row_tiles;
     a->chunk = (int)p.chunk;
@@ -230,7 +237,9 @@ ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t 
     if (Lq < 0 || Lq > kMaxInt || Lk < 0 || Lk > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
     if ((__int128)Lq * (Hq / Hkv) > kMaxInt) return CTCONV_ERR_SHAPE;
     const int64_t R = Lq * (Hq / Hkv);
-    return plan_attention(B, Hkv, R, D, Lk, false, R > kTileFrom, p);
+    // (fp32 rows past 512 bytes are too long for its LDS tiles)
+    const bool tile = R > kTileFrom && D * (int64_t)esize(dt) <= 512;
+    return plan_attention(B, Hkv, R, D, Lk, false, tile, p);
 }
 
 }  // namespace
@@ -376,7 +385,7 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
     a.D = (int)D;
     a.window = (int)(window < max_length ? window : 0);
     a.fd_G = make_fastdiv((uint32_t)a.G);
-    a.c = fabsf(scale) * kLog2e;
+    a.c = score_factor(scale);
     a.negate = scale < 0;
     apply_plan(p, workspace, &a);
     const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -524,12 +533,21 @@ ctconv_status ctconv_cross_attention(const void* q, const void* k, const void* v
     a.R = (int)(Lq * a.G);
     a.D = (int)D;
     a.fd_G = make_fastdiv((uint32_t)a.G);
-    a.c = fabsf(scale) * kLog2e;
+    a.c = score_factor(scale);
     a.negate = scale < 0;
     apply_plan(p, workspace, &a);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    st = to_status(p.tile ? launch_attn_tile(a, dtype, s)
-                          : launch_attn_stream(a, dtype, false, s));
+    // tile_kernel holds offsets within a tile of 64 keys in 32 bits
+    const int64_t reach = a.k_row > a.v_row ? a.k_row : a.v_row;
+    const bool far = reach > (((int64_t)1 << 32) / (int64_t)esize(dtype) - D) / 64;
+    if (p.tile && far) {
+        // the same split by the other kernel, whose row tiles are smaller
+        const int64_t tiles = ceil_div(a.R, 16);
+        if ((__int128)B * Hkv * tiles * a.splits > kMaxInt) return CTCONV_ERR_SHAPE;
+        a.row_tiles = (int)tiles;
+    }
+    st = to_status(p.tile && !far ? launch_attn_tile(a, dtype, s)
+                                  : launch_attn_stream(a, dtype, false, s));
     if (st != CTCONV_OK || a.direct) return st;
     return to_status(launch_attn_join(a, dtype, false, s));
 }
