@@ -564,7 +564,7 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
  * K and V rows move in place; no page of the sequences may be shared with
  * another sequence.  A row whose old or new slot has no page is not moved.
  * keep >= 1, sink >= 0, recent >= 0 (CTCONV_ERR_PARAM); max_length (a bound
- * on lengths) at most max_pages * page_size and 524288 (CTCONV_ERR_SHAPE).
+ * on lengths) at most max_pages * page_size and 262144 (CTCONV_ERR_SHAPE).
  * keep may exceed the lengths: then nothing is given up.
  */
 ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* page_table,

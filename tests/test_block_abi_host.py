@@ -118,7 +118,7 @@ def test_evict_validation(lib):
                dict(wo=P[4]), dict(po=P[5])):  # in place needs the same strides
         assert _evict(lib, **kw) == PARAM, kw
     for kw in (dict(B=-2), dict(H=0), dict(D=20), dict(maxlen=81),
-               dict(page=1 << 10, cols=1 << 10, maxlen=524289, slot=(1 << 22, 1 << 20),
+               dict(page=1 << 10, cols=1 << 10, maxlen=262145, slot=(1 << 22, 1 << 20),
                     kv=(1 << 18, 64, 1 << 16)), dict(slot=(-1, 80)),
                dict(out=(256, -1)), dict(kv=(4096, 64, -1)), dict(keep=1 << 31),
                dict(B=1 << 16, H=1 << 15)):

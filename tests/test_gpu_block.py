@@ -282,6 +282,10 @@ EVICT = [
     (1, 1, 8, 1024, [70001], 69000, 0, 7, "random"),
     (2, 2, 32, 16, [100, 90], 160, 0, 0, "random"),
     (2, 2, 64, 16, [513, 600], 1, 0, 0, "level"),
+    (1, 1, 8, 512, [9500], 4100, 0, 0, "close"),
+    (1, 1, 8, 512, [9500], 4100, 0, 0, "level"),
+    (2, 1, 8, 512, [30000, 29000], 9000, 4, 9, "close"),
+    (1, 1, 8, 1024, [200001], 100000, 4, 9, "ties"),
 ]
 
 
@@ -301,6 +305,8 @@ def test_cache_evict(cc, case, dt):
         w[w == 0] = np.where(rng.random(int((w == 0).sum())) < 0.5, 0.0, -0.0)
     elif kind == "level":
         w = np.full((B, H, cap), 0.125, np.float32)
+    elif kind == "close":  # the same upper three digits, many equal
+        w = (0x3F123400 + rng.integers(0, 256, (B, H, cap))).astype(np.int32).view(np.float32)
     else:
         w = (rng.random((B, H, cap)) ** 8 * 50).astype(np.float32)
     if kind == "nan":

@@ -50,7 +50,8 @@ __device__ inline void visible(const AttnArgs& a, int b, int& first, int& span) 
 }
 
 template <class TR, int DP, bool PAGED, bool EXACT, int NW>
-__global__ __launch_bounds__(64 * NW) void stream_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, NW > 4 ? 1 : DP <= 64 ? 4 : DP <= 128 ? 3 : 1) void
+stream_kernel(AttnArgs a) {
     using S = typename TR::storage;
     constexpr int ES = sizeof(S), VEC = 16 / ES;
     constexpr int KB = ES == 2 ? 32 : 16;  // keys per block

@@ -12,7 +12,7 @@ using namespace ctconv::block;
 namespace {
 
 constexpr int64_t kMaxInt = INT32_MAX;
-constexpr int64_t kMaxEvictSlots = 524288;  // select_kernel's bits and sums fit LDS
+constexpr int64_t kMaxEvictSlots = 262144;  // select_kernel keeps a few bits per slot in LDS
 constexpr int64_t kEvictLds = 128 << 10;     // of the 160 KB, with what it declares itself
 constexpr int64_t kFusedKeep = 2048;
 constexpr int64_t kMaxRowValues = 16384;    // norm_kernel keeps a row in registers
@@ -145,7 +145,7 @@ int64_t tile_chunk(int64_t tiles, int64_t keys) {
 //    against 12.1 split, 1000 keys on 256 tiles 28 against 32; but 2000 keys on
 //    64 tiles 25 against 20 (bf16, D = 128).
 //  - Else chunks that give every compute unit one round of the workgroups its
-//    registers hold (4, 2 or 1 of 4 waves for D up to 64, 128, 256): 30000
+//    registers hold (4, 3 or 1 of 4 waves for D up to 64, 128, 256): 30000
 //    keys on 8 tiles take 33 us in 469 workgroups, 40 in 938.  At least 256
 //    keys (a workgroup's start costs about as much as 128), at most 1024, so
 //    that ragged sequences still spread.
@@ -156,7 +156,7 @@ void stream_split(int64_t tiles, int64_t keys, int64_t D, int64_t* chunk, bool* 
         *chunk = round_up(keys, 128);
         return;
     }
-    const int64_t room = D <= 64 ? 1024 : D <= 128 ? 512 : 256;
+    const int64_t room = D <= 64 ? 1024 : D <= 128 ? 768 : 256;
     const int64_t c = round_up(ceil_div(keys * tiles, room), 128);
     *chunk = c < 256 ? 256 : c > 1024 ? 1024 : c;
 }
@@ -455,7 +455,7 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
     a.words = (int)(round_up(max_length > 0 ? max_length : 1, 1024) / 64);
     const int64_t excess = max_length > keep ? max_length - keep : 0;
     const int64_t moves = excess < keep ? excess : keep;
-    const int64_t room = (kEvictLds - a.words * 12) / 4;
+    const int64_t room = (kEvictLds - a.words * 12) / 4;  // (a few slots: all of them)
     a.list = (int)(moves < room ? moves : room);
     a.fused = keep <= kFusedKeep && lengths_out != lengths;
     a.chunks = (int)(D * (int64_t)esize(dtype) / 16);

@@ -79,7 +79,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kDigits = 256, kColumns = 32;
 constexpr int kBatch = 8;
-constexpr int kNear = 4096;  // keys gathered in LDS
+constexpr int kNear = 2048;  // keys gathered in LDS
 
 __device__ inline uint32_t rank_key(float w, bool safe) {
     if (safe) return 0xFFFFFFFFu;
@@ -216,11 +216,14 @@ template <class S, int KEYS>
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     extern __shared__ __align__(16) uint32_t lds[];
     __shared__ int wave_sums[kSelWaves], found[4], digits[kDigits];
-    __shared__ MovedRow rows[kSelWaves][64];
-    uint32_t* hist = lds;  // kDigits x kColumns, then kNear keys, first
-    uint64_t* bits = reinterpret_cast<uint64_t*>(lds);   // then a.words, and
-    int* pre = reinterpret_cast<int*>(bits + a.words);   // a.words prefix sums, and
-    int* spare = pre + a.words;                          // a.list kept slots from m on
+    uint64_t* bits = reinterpret_cast<uint64_t*>(lds);   // a.words: who stays
+    int* pre = reinterpret_cast<int*>(bits + a.words);   // a.words prefix sums
+    uint32_t* work = reinterpret_cast<uint32_t*>(pre + a.words);
+    uint32_t* hist = work;                               // kDigits x kColumns
+    uint32_t* near = hist + kDigits * kColumns;          // kNear keys and slots
+    int* near_slot = reinterpret_cast<int*>(near + kNear);
+    uint64_t* ties = reinterpret_cast<uint64_t*>(work);  // later: a.words
+    int* spare = reinterpret_cast<int*>(work);           // last: a.list kept slots from m on
     const int bh = blockIdx.x, b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = clamped(a.lengths[b], a.pages.slots);
@@ -270,11 +273,11 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             }
         };
         // The m-th largest key.  Once few enough keys share its digits, those
-        // are gathered in LDS and only they are counted on.
+        // are gathered in LDS with their slots and only they are looked at;
+        // the larger ones are marked as staying in the same pass.
         uint32_t prefix = 0, mask = 0;
         int want = m;
         bool exact = false;  // every key with this prefix stays
-        uint32_t* near = hist + kDigits * kColumns;
         int near_n = -1;
         if (tid == 0) found[3] = 0;
         for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
@@ -330,42 +333,62 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             mask |= 255u << shift;
             want = found[1];
             exact = found[1] == found[2];
-            if (near_n < 0 && !exact && shift > 0 && found[2] <= kNear) {
+            if (near_n < 0 && !exact && found[2] <= kNear) {
                 near_n = found[2];
                 each([&](int t, uint32_t key) {
+                    const uint64_t above = __ballot(t < n && (key & mask) > prefix);
+                    if (lane == 0) bits[t >> 6] = above;
                     const bool is = t < n && (key & mask) == prefix;
                     const uint64_t w = __ballot(is);
                     if (w == 0) return;
-                    int at = 0;  // any order: the keys are only counted
+                    int at = 0;  // in any order: what follows does not depend on it
                     if (lane == 0) at = atomicAdd(&found[3], __popcll(w));
-                    at = __builtin_amdgcn_readfirstlane(at);
-                    if (is) near[at + __popcll(w & ((1ull << lane) - 1))] = key;
+                    at = __builtin_amdgcn_readfirstlane(at) + __popcll(w & ((1ull << lane) - 1));
+                    if (is) {
+                        near[at] = key;
+                        near_slot[at] = t;
+                    }
                 });
             }
             __syncthreads();
         }
-        // keys from `prefix` on stay; where not `exact`, only the first
-        // `want` of those equal to it
-        each([&](int t, uint32_t key) {
-            const uint64_t w = __ballot(t < n && key >= prefix);
-            if (lane == 0) bits[t >> 6] = w;
-            if (!exact) {
-                const uint64_t e = __ballot(t < n && key == prefix);
-                if (lane == 0) pre[t >> 6] = __popcll(e);
-            }
-        });
-        __syncthreads();
         const int words = (n + 63) >> 6;
-        if (!exact) {
-            scan_words(pre, words, wave_sums);
+        // Keys from `prefix` on stay; where not `exact`, only the first `want`
+        // of those equal to it, by their rank among the slots of `ties`.
+        if (!exact)
+            for (int w = tid; w < words; w += kSelThreads) ties[w] = 0;
+        __syncthreads();
+        const auto mark = [&](uint64_t* to, int t) {
+            atomicOr(reinterpret_cast<unsigned long long*>(&to[t >> 6]), 1ull << (t & 63));
+        };
+        if (near_n >= 0) {
+            for (int i = tid; i < near_n; i += kSelThreads) {
+                const uint32_t key = near[i];
+                if (key > prefix || (exact && key == prefix)) mark(bits, near_slot[i]);
+                else if (key == prefix) mark(ties, near_slot[i]);
+            }
+        } else {
             each([&](int t, uint32_t key) {
-                const bool level = t < n && key == prefix;
-                const uint64_t e = __ballot(level);
-                const int before = __popcll(e & ((1ull << lane) - 1));
-                const uint64_t gone = __ballot(level && (t >> 6) < words &&
-                                               pre[(t >> 6) < words ? t >> 6 : 0] + before >= want);
-                if (lane == 0 && (t >> 6) < words) bits[t >> 6] &= ~gone;
+                const uint64_t w = __ballot(t < n && (exact ? key >= prefix : key > prefix));
+                const uint64_t e = __ballot(t < n && key == prefix);
+                if (lane == 0) {
+                    bits[t >> 6] = w;
+                    if (!exact && (t >> 6) < words) ties[t >> 6] = e;
+                }
             });
+        }
+        __syncthreads();
+        if (!exact) {
+            for (int w = tid; w < words; w += kSelThreads) pre[w] = __popcll(ties[w]);
+            __syncthreads();
+            scan_words(pre, words, wave_sums);
+            for (int w = tid; w < words; w += kSelThreads) {
+                // the first want - pre[w] ties of the word
+                const int left = want - pre[w], all_of = __popcll(ties[w]);
+                if (left <= 0 || all_of == 0) continue;
+                bits[w] |= left >= all_of ? ties[w]
+                                          : ties[w] & ((1ull << nth_bit(ties[w], left)) - 1);
+            }
             __syncthreads();
         }
         // holes per word below m, kept slots per word from m on
@@ -391,36 +414,35 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         }
         __syncthreads();
     }
-    for (int j0 = 0; j0 < a.keep; j0 += kSelThreads) {
-        const int j = j0 + tid;
-        int src = -1;
-        if (j < m) {
-            src = j;
-            if (!all && !((bits[j >> 6] >> (j & 63)) & 1)) {
-                const int r = pre[j >> 6] + __popcll(~bits[j >> 6] & ((1ull << (j & 63)) - 1));
-                if (listed) {
-                    src = spare[r];
-                } else {
-                    // the last word from `edge` on whose kept slots start at or before rank r
-                    int lo = edge, hi = words - 1;
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (pre[mid] - base <= r) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    uint64_t w = bits[lo];
-                    if (lo == edge) w &= ~below;
-                    src = lo * 64 + nth_bit(w, r - (pre[lo] - base));
-                }
-            }
+    const auto source_of = [&](int j) {
+        if (j >= m) return -1;
+        const uint64_t word = all ? ~0ull : bits[j >> 6];
+        if ((word >> (j & 63)) & 1) return j;
+        const int r = pre[j >> 6] + __popcll(~word & ((1ull << (j & 63)) - 1));
+        if (listed) return spare[r];
+        // the last word from `edge` on whose kept slots start at or before rank r
+        int lo = edge, hi = words - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] - base <= r) lo = mid;
+            else hi = mid - 1;
         }
-        if (j < a.keep) source[j] = src;
-        if (a.fused) {
-            const int js[1] = {j}, srcs[1] = {src};
-            fill_slots<S, 1>(a, b, h, js, srcs, rows[wave]);
-        }
+        const uint64_t w = lo == edge ? bits[lo] & ~below : bits[lo];
+        return lo * 64 + nth_bit(w, r - (pre[lo] - base));
+    };
+    if (!a.fused) {
+#pragma unroll 4
+        for (int j = tid; j < a.keep; j += kSelThreads) source[j] = source_of(j);
+        return;
     }
-    if (a.fused && a.lengths_out && h == 0 && tid == 0) a.lengths_out[b] = m;
+    MovedRow* rows = reinterpret_cast<MovedRow*>(work + ((a.list + 3) & ~3)) + wave * 64;
+    for (int j0 = 0; j0 < a.keep; j0 += kSelThreads) {
+        const int js[1] = {j0 + tid};
+        const int srcs[1] = {source_of(js[0])};
+        if (js[0] < a.keep) source[js[0]] = srcs[0];
+        fill_slots<S, 1>(a, b, h, js, srcs, rows);
+    }
+    if (a.lengths_out && h == 0 && tid == 0) a.lengths_out[b] = m;
 }
 
 // Second kernel: every wave fills 64 slots kFill times.
@@ -450,9 +472,11 @@ __global__ __launch_bounds__(kFillThreads) void fill_kernel(EvictArgs a) {
 
 template <class S>
 hipError_t evict_t(const EvictArgs& a, hipStream_t s) {
-    size_t lds = (size_t)a.words * 12 + (size_t)a.list * 4;
-    const size_t count = (kDigits * kColumns + kNear) * 4;
-    if (lds < count) lds = count;
+    const size_t count = (kDigits * kColumns + 2 * kNear) * 4;
+    size_t work = (size_t)((a.list + 3) & ~3) * 4 + (a.fused ? kSelThreads * sizeof(MovedRow) : 0);
+    if (work < count) work = count;
+    if (work < (size_t)a.words * 8) work = (size_t)a.words * 8;
+    const size_t lds = (size_t)a.words * 12 + work;
     const int slots = a.words * 64;
     const void* fn = slots <= kSelThreads     ? reinterpret_cast<const void*>(&select_kernel<S, 1>)
                      : slots <= 4 * kSelThreads ? reinterpret_cast<const void*>(&select_kernel<S, 4>)
