@@ -502,6 +502,55 @@ def test_norm_residual(cc, case, dt):
     assert torch.equal(xi, xo) and (not pre or torch.equal(hi, y))
 
 
+def test_large_rows_past_the_caches(cc):
+    """Enough rows that norms and appended rows are written past the L2 caches."""
+    import torch
+
+    say("large norm")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows, C = 4200, 4104
+    x, h, gate = (torch.randn(rows, C, generator=g, device="cuda").bfloat16() for _ in range(3))
+    xo, y = cc.norm_residual(x, h, cc.NORM_RMS, gate=gate, gate_fn=cc.GATE_SIGMOID, pre=cc.NORM_RMS)
+    pick = torch.tensor([0, 1, 63, 64, 2047, 4199], device="cuda")
+    rx, ry = R.norm_residual(to_host(x[pick]), to_host(h[pick]), 1, None, None, None,
+                             to_host(gate[pick]), 2, 1, 1, None, None, 1e-5)
+    R.check(to_host(xo[pick]), rx, _norm_bound("bf16", C, rx, np.abs(rx) + 20), "x_out")
+    R.check(to_host(y[pick]), ry, _norm_bound("bf16", C, ry, np.abs(ry) + 40), "y")
+    small = cc.norm_residual(x[:64], h[:64], cc.NORM_RMS, gate=gate[:64], gate_fn=cc.GATE_SIGMOID,
+                             pre=cc.NORM_RMS)
+    assert torch.equal(small[0], xo[:64]) and torch.equal(small[1], y[:64])
+    say("large append")
+    B, n, H, D, page = 2, 2100, 8, 256, 64
+    kn, vn = (torch.randn(B, n, H, D, generator=g, device="cuda") for _ in range(2))
+    cols = -(-n // page)
+    table = torch.randperm(B * cols).int().view(B, cols).cuda()
+    k, v = (torch.zeros(B * cols, H, page, D, device="cuda") for _ in range(2))
+    cc.cache_append(kn, vn, k, v, table, ints([n, n]))
+    for new, cache in ((kn, k), (vn, v)):
+        rows = cache[table.long()].transpose(2, 3).reshape(B, cols * page, H, D)
+        assert torch.equal(rows[:, :n], new) and not bool(rows[:, n:].any())
+
+
+def test_cross_attention_far_rows(cc):
+    """Key and value rows so far apart that a tile of them spans over 4 GiB."""
+    import torch
+
+    B, Lq, Lk, H, D = 1, 130, 70, 1, 64
+    say("cross far rows")
+    rng = np.random.default_rng(53)
+    stride = (1 << 26) + 64  # bf16: 64 rows span 8 GiB
+    pool = torch.empty((Lk - 1) * stride + D, dtype=torch.bfloat16, device="cuda")
+    kd = pool.as_strided((B, Lk, H, D), (0, stride, D, 1))
+    k, k64 = dev(rng.standard_normal((B, Lk, H, D)), "bf16")
+    kd.copy_(k)
+    q, q64 = dev(rng.standard_normal((B, Lq, H, D)), "bf16")
+    out, lse = cc.cross_attention(q, kd, kd)
+    torch.cuda.synchronize()
+    (o, l), (bo, bl) = R.cross(q64, k64, k64, None, None, D ** -0.5, "bf16")
+    R.check(to_host(out), o, bo, "out")
+    R.check(to_host(lse), l, bl, "lse")
+
+
 def test_norm_residual_row_strides(cc):
     """Rows apart from each other, by strides that keep and that break the
     16-byte starts: the same bits as dense rows, nothing written between."""
