@@ -649,6 +649,29 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
                                    ctconv_gate gate_fn, float eps, ctconv_dtype dtype,
                                    void* stream);
 
+/*
+ * The five calls above with their arguments in two tables, for callers that
+ * prepare the sizes once and pay per argument afterwards (a foreign-function
+ * binding; the Python plans use it): the function is called with
+ *   buffers   its buffer pointers, in the order of its signature
+ *   sizes     every other argument up to the dtype, in the order of its
+ *             signature: integers and enumerators as they are, the values of
+ *             a stride array one after the other (all arrays are needed
+ *             here), scale and eps as the bits of a double
+ *   workspace, workspace_bytes   of the attention calls; otherwise ignored
+ * Checks, errors and results are the function's own.  CTCONV_ERR_PARAM for an
+ * unknown op, CTCONV_ERR_NULL for a missing table.
+ */
+typedef enum {
+    CTCONV_OP_CACHE_APPEND = 0,    /* 10 buffers, 17 sizes */
+    CTCONV_OP_PAGED_ATTENTION = 1, /*  8 buffers, 21 sizes */
+    CTCONV_OP_CACHE_EVICT = 2,     /* 11 buffers, 19 sizes */
+    CTCONV_OP_CROSS_ATTENTION = 3, /*  7 buffers, 21 sizes */
+    CTCONV_OP_NORM_RESIDUAL = 4    /* 10 buffers, 13 sizes */
+} ctconv_block_op;
+ctconv_status ctconv_block_run(ctconv_block_op op, const int64_t* sizes, void* const* buffers,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -197,3 +197,55 @@ def test_python_helpers_refuse_host_tensors():
         C.cache_append(t, t, t, t, t, t)
     with pytest.raises(ValueError, match="device"):
         C.cache_evict(t, t, t, t, t, 1)
+
+
+def test_block_run_reaches_each_function(lib):
+    """The table form refuses what the functions refuse, with their statuses."""
+    run = lib.ctconv_block_run
+    bufs = (ctypes.c_void_p * 12)(*P)
+
+    def sizes(*v):
+        return (ctypes.c_int64 * 24)(*v)
+
+    one = ctypes.c_int64.from_buffer_copy(ctypes.c_double(0.1)).value
+    nan = ctypes.c_int64.from_buffer_copy(ctypes.c_double(float("nan"))).value
+    append = [2, 3, 4, 64, 10, 16, 5, 768, 256, 64, 4096, 64, 1024, 5, 320, 80, 1]
+    paged = [2, 8, 4, 64, 10, 16, 5, 80, 0, 512, 64, 4096, 64, 1024, 512, 64, 5, 320, 80, one, 1]
+    evict = [2, 4, 64, 10, 16, 5, 80, 64, 4, 8, 4096, 64, 1024, 5, 320, 80, 320, 80, 1]
+    cross = [2, 5, 7, 8, 4, 64, 2560, 512, 64, 1792, 256, 64, 1792, 256, 64, 2560, 512, 64, 7, one, 1]
+    norm = [4, 64, 64, 64, 64, 64, 64, 1, 1, 2, 2, one, 0]
+
+    def call(op, z, **kw):
+        z = list(z)
+        for i, v in kw.items():
+            z[int(i[1:])] = v
+        return run(op, sizes(*z), bufs, None, 0, None)
+
+    assert run(5, sizes(), bufs, None, 0, None) == PARAM
+    assert run(-1, sizes(), bufs, None, 0, None) == PARAM
+    assert run(0, None, bufs, None, 0, None) == NULL
+    assert run(0, sizes(*append), None, None, 0, None) == NULL
+    for op, z in enumerate((append, paged, evict, cross, norm)):
+        last = len(z) - 1
+        for bad in (3, -1, 1 << 40):
+            assert call(op, z, **{f"_{last}": bad}) == DTYPE, (op, bad)
+    assert call(0, append, _3=12) == SHAPE
+    assert call(0, append, _11=66) == ALIGN
+    assert call(1, paged, _19=nan) == PARAM
+    assert call(1, paged) == WORKSPACE  # a weight_sum is among the buffers
+    assert call(2, evict, _7=0) == PARAM
+    assert call(3, cross, _19=nan) == PARAM
+    assert call(3, cross, _10=257) == ALIGN
+    assert call(4, norm, _8=7) == PARAM
+    assert call(4, norm, _10=-3) == PARAM
+    assert call(4, norm, _11=nan) == PARAM
+    assert call(4, norm, _0=0) == 0
+
+
+def test_plans_raise_the_function_s_error():
+    with pytest.raises(C.CtconvError, match="ctconv_norm_residual") as e:
+        C.NormResidual(4, 64)(None, P[1], None, None, None, None, None, None, P[2], P[3], 0)
+    assert e.value.status == NULL
+    with pytest.raises(C.CtconvError, match="ctconv_cache_evict") as e:
+        C.CacheEvict(1, 1, 8, 4, 4, 4, keep=0)(*P[:11], 0)
+    assert e.value.status == PARAM

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,7 +32,7 @@ EXPORTED = (
     "ctconv_scratch_bytes", "ctconv_clock_probe_bytes", "ctconv_clock_probe",
     "ctconv_cache_append", "ctconv_paged_attention_workspace_bytes", "ctconv_paged_attention",
     "ctconv_cache_evict", "ctconv_cross_attention_workspace_bytes", "ctconv_cross_attention",
-    "ctconv_norm_residual",
+    "ctconv_norm_residual", "ctconv_block_run",
 )
 
 DW_AUTO, DW_ROW, DW_ELEMENT = 0, 1, 2
@@ -140,6 +141,8 @@ def load(path: str = LIB_PATH):
     lib.ctconv_norm_residual.argtypes = [c_vp] * 10 + [c_i64, c_i64, _i64p, c_i64, c_int, c_int,
                                                        c_int, c_f, c_int, c_vp]
     lib.ctconv_norm_residual.restype = c_int
+    lib.ctconv_block_run.argtypes = [c_int, c_vp, c_vp, c_vp, c_sz, c_vp]
+    lib.ctconv_block_run.restype = c_int
     _lib = lib
     return lib
 
@@ -689,15 +692,38 @@ class ConvWS(Conv):
 # ---------------------------------------------------------------------------
 
 
+OP_CACHE_APPEND, OP_PAGED_ATTENTION, OP_CACHE_EVICT = 0, 1, 2
+OP_CROSS_ATTENTION, OP_NORM_RESIDUAL = 3, 4
+
+
 def _strides(given, default):
-    return _arr(default if given is None else given)
+    return tuple(int(v) for v in (default if given is None else given))
+
+
+class _Plan:
+    """A prepared ctconv_block_run: the sizes in one array, the call's pointers
+    packed into another (a fresh one per call, so that threads can share a
+    plan).  Against the functions themselves, whose arguments ctypes converts
+    one by one, this takes about 1 us off a call of 5."""
+
+    def _prepare(self, name: str, op: int, buffers: int, sizes):
+        flat = []
+        for v in sizes:
+            flat.extend(v if isinstance(v, tuple) else (v,))
+        as_int = [struct.unpack("q", struct.pack("d", v))[0] if isinstance(v, float) else int(v)
+                  for v in flat]
+        self._name, self._op = name, op
+        self._sizes = _arr(as_int)
+        self._sizes_ptr = ctypes.c_void_p(ctypes.addressof(self._sizes))
+        self._pack = struct.Struct(f"{buffers}P").pack
+        self._fn = load().ctconv_block_run
 
 
 def _scale(scale, D: int) -> float:
     return float(D) ** -0.5 if scale is None else float(scale)
 
 
-class _Paged:
+class _Paged(_Plan):
     """Sizes and strides of a paged cache.  Without strides: pages of
     [Hkv, page_size, D], a dense table, dense [B, Hkv, slots] slot arrays."""
 
@@ -723,16 +749,20 @@ class CacheAppend(_Paged):
                     slot_strides)
         self.n, self.dtype = int(n), dtype
         new = _strides(new_strides, (self.n * self.Hkv * self.D, self.Hkv * self.D, self.D))
-        self._args = (self.B, self.n, self.Hkv, self.D, self.num_pages, self.page_size,
-                      self.max_pages, new, self._kv, self._table, self._slot, dtype)
-        self._fn = load().ctconv_cache_append
+        self._prepare("ctconv_cache_append", OP_CACHE_APPEND, 10,
+                      (self.B, self.n, self.Hkv, self.D, self.num_pages, self.page_size,
+                       self.max_pages, new, self._kv, self._table, self._slot, dtype))
 
     def __call__(self, k_new_ptr, v_new_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, counts_ptr,
                  now_ptr, positions_ptr, weight_ptr, stream: int) -> None:
-        st = self._fn(k_new_ptr, v_new_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, counts_ptr,
-                      now_ptr, positions_ptr, weight_ptr, *self._args, stream)
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(k_new_ptr or 0, v_new_ptr or 0, k_ptr or 0, v_ptr or 0, table_ptr or 0,
+                       lengths_ptr or 0, counts_ptr or 0, now_ptr or 0, positions_ptr or 0,
+                       weight_ptr or 0),
+            None, 0, stream)
         if st != 0:
-            raise CtconvError("ctconv_cache_append", st)
+            raise CtconvError(self._name, st)
 
 
 def ctconv_paged_attention_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_length: int,
@@ -761,18 +791,21 @@ class PagedAttention(_Paged):
         dense = (self.Hq * self.D, self.D)
         self.workspace_bytes = ctconv_paged_attention_workspace_bytes(
             self.B, self.Hq, self.Hkv, self.D, self.max_length, self.window, self.weights, dtype)
-        self._args = (self.B, self.Hq, self.Hkv, self.D, self.num_pages, self.page_size,
-                      self.max_pages, self.max_length, self.window, _strides(q_strides, dense),
-                      self._kv, _strides(out_strides, dense), self._table, self._slot,
-                      _scale(scale, self.D), dtype)
-        self._fn = load().ctconv_paged_attention
+        self._prepare("ctconv_paged_attention", OP_PAGED_ATTENTION, 8,
+                      (self.B, self.Hq, self.Hkv, self.D, self.num_pages, self.page_size,
+                       self.max_pages, self.max_length, self.window, _strides(q_strides, dense),
+                       self._kv, _strides(out_strides, dense), self._table, self._slot,
+                       _scale(scale, self.D), dtype))
 
     def __call__(self, q_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, out_ptr, lse_ptr, weight_ptr,
                  ws_ptr, ws_bytes: int, stream: int) -> None:
-        st = self._fn(q_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, out_ptr, lse_ptr, weight_ptr,
-                      *self._args, ws_ptr, ws_bytes, stream)
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(q_ptr or 0, k_ptr or 0, v_ptr or 0, table_ptr or 0, lengths_ptr or 0,
+                       out_ptr or 0, lse_ptr or 0, weight_ptr or 0),
+            ws_ptr, ws_bytes, stream)
         if st != 0:
-            raise CtconvError("ctconv_paged_attention", st)
+            raise CtconvError(self._name, st)
 
 
 class CacheEvict(_Paged):
@@ -788,19 +821,22 @@ class CacheEvict(_Paged):
         self.keep, self.sink, self.recent, self.dtype = int(keep), int(sink), int(recent), dtype
         self.max_length = self.slots if max_length is None else int(max_length)
         out = _strides(out_slot_strides, (self.Hkv * self.keep, self.keep))
-        self._args = (self.B, self.Hkv, self.D, self.num_pages, self.page_size, self.max_pages,
-                      self.max_length, self.keep, self.sink, self.recent, self._kv, self._table,
-                      self._slot, out, dtype)
-        self._fn = load().ctconv_cache_evict
+        self._prepare("ctconv_cache_evict", OP_CACHE_EVICT, 11,
+                      (self.B, self.Hkv, self.D, self.num_pages, self.page_size, self.max_pages,
+                       self.max_length, self.keep, self.sink, self.recent, self._kv, self._table,
+                       self._slot, out, dtype))
 
     def __call__(self, k_ptr, v_ptr, table_ptr, lengths_ptr, now_ptr, weight_ptr, positions_ptr,
                  weight_out_ptr, positions_out_ptr, lengths_out_ptr, source_ptr,
                  stream: int) -> None:
-        st = self._fn(k_ptr, v_ptr, table_ptr, lengths_ptr, now_ptr, weight_ptr, positions_ptr,
-                      weight_out_ptr, positions_out_ptr, lengths_out_ptr, source_ptr, *self._args,
-                      stream)
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(k_ptr or 0, v_ptr or 0, table_ptr or 0, lengths_ptr or 0, now_ptr or 0,
+                       weight_ptr or 0, positions_ptr or 0, weight_out_ptr or 0,
+                       positions_out_ptr or 0, lengths_out_ptr or 0, source_ptr or 0),
+            None, 0, stream)
         if st != 0:
-            raise CtconvError("ctconv_cache_evict", st)
+            raise CtconvError(self._name, st)
 
 
 def ctconv_cross_attention_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: int,
@@ -812,7 +848,7 @@ def ctconv_cross_attention_workspace_bytes(B: int, Lq: int, Lk: int, Hq: int, Hk
     return int(nb.value)
 
 
-class CrossAttention:
+class CrossAttention(_Plan):
     """ctconv_cross_attention for one shape; dense [B, L, H, D] tensors without strides."""
 
     def __init__(self, B: int, Lq: int, Lk: int, Hq: int, Hkv: int, D: int, scale=None,
@@ -824,22 +860,25 @@ class CrossAttention:
         k = (self.Lk * self.Hkv * self.D, self.Hkv * self.D, self.D)
         self.workspace_bytes = ctconv_cross_attention_workspace_bytes(
             self.B, self.Lq, self.Lk, self.Hq, self.Hkv, self.D, dtype)
-        self._args = (self.B, self.Lq, self.Lk, self.Hq, self.Hkv, self.D,
-                      _strides(q_strides, q), _strides(k_strides, k), _strides(v_strides, k),
-                      _strides(out_strides, q),
-                      self.Lk if mask_stride is None else int(mask_stride),
-                      _scale(scale, self.D), dtype)
-        self._fn = load().ctconv_cross_attention
+        self._prepare("ctconv_cross_attention", OP_CROSS_ATTENTION, 7,
+                      (self.B, self.Lq, self.Lk, self.Hq, self.Hkv, self.D,
+                       _strides(q_strides, q), _strides(k_strides, k), _strides(v_strides, k),
+                       _strides(out_strides, q),
+                       self.Lk if mask_stride is None else int(mask_stride),
+                       _scale(scale, self.D), dtype))
 
     def __call__(self, q_ptr, k_ptr, v_ptr, lengths_ptr, mask_ptr, out_ptr, lse_ptr, ws_ptr,
                  ws_bytes: int, stream: int) -> None:
-        st = self._fn(q_ptr, k_ptr, v_ptr, lengths_ptr, mask_ptr, out_ptr, lse_ptr, *self._args,
-                      ws_ptr, ws_bytes, stream)
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(q_ptr or 0, k_ptr or 0, v_ptr or 0, lengths_ptr or 0, mask_ptr or 0,
+                       out_ptr or 0, lse_ptr or 0),
+            ws_ptr, ws_bytes, stream)
         if st != 0:
-            raise CtconvError("ctconv_cross_attention", st)
+            raise CtconvError(self._name, st)
 
 
-class NormResidual:
+class NormResidual(_Plan):
     """ctconv_norm_residual for one shape; dense rows without strides
     (strides: of x, h, gate, x_out, y)."""
 
@@ -848,16 +887,20 @@ class NormResidual:
                  dtype: int = CTCONV_F32, strides=None):
         self.rows, self.C, self.dtype = int(rows), int(C), dtype
         self.post, self.pre, self.gate = post, pre, gate
-        self._args = (self.rows, self.C, _strides(strides, (self.C,) * 5), int(rows_per_gate),
-                      post, pre, gate, float(eps), dtype)
-        self._fn = load().ctconv_norm_residual
+        self._prepare("ctconv_norm_residual", OP_NORM_RESIDUAL, 10,
+                      (self.rows, self.C, _strides(strides, (self.C,) * 5), int(rows_per_gate),
+                       post, pre, gate, float(eps), dtype))
 
     def __call__(self, x_ptr, h_ptr, post_weight_ptr, post_bias_ptr, scale_ptr, gate_ptr,
                  pre_weight_ptr, pre_bias_ptr, x_out_ptr, y_ptr, stream: int) -> None:
-        st = self._fn(x_ptr, h_ptr, post_weight_ptr, post_bias_ptr, scale_ptr, gate_ptr,
-                      pre_weight_ptr, pre_bias_ptr, x_out_ptr, y_ptr, *self._args, stream)
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(x_ptr or 0, h_ptr or 0, post_weight_ptr or 0, post_bias_ptr or 0,
+                       scale_ptr or 0, gate_ptr or 0, pre_weight_ptr or 0, pre_bias_ptr or 0,
+                       x_out_ptr or 0, y_ptr or 0),
+            None, 0, stream)
         if st != 0:
-            raise CtconvError("ctconv_norm_residual", st)
+            raise CtconvError(self._name, st)
 
 
 def _ptr(t):
