@@ -79,9 +79,31 @@ stream_kernel(AttnArgs a) {
     const int row0 = tile * 16;
     const int rows = a.R - row0 < 16 ? a.R - row0 : 16;
 
+    // Queries of this tile: lane (col, g) holds pieces 4f + g of row col.  They
+    // and, where no length moves the first slot, this thread's page are asked
+    // for before the length has arrived: a short call is a chain of latencies.
+    u32x4 qf[NF];
+    {
+        const int r = row0 + col;
+        const bool live = col < rows;
+        const int lq = live ? (int)fdiv((uint32_t)r, a.fd_G) : 0;
+        const S* qr = static_cast<const S*>(a.q) + b * a.q_b + lq * a.q_row +
+                      (int64_t)(h * a.G + (live ? r - lq * a.G : 0)) * a.q_head;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int d = (4 * f + g) * VEC;
+            qf[f] = u32x4{0, 0, 0, 0};
+            if (live && (EXACT || d < a.D)) qf[f] = *reinterpret_cast<const u32x4*>(qr + d);
+        }
+    }
+    const int start = split * a.chunk;  // relative to the first slot
+    int page0 = -1;
+    if (PAGED && a.window == 0 && start + tid < a.pages.slots)
+        page0 = a.pages.table[b * a.pages.table_stride +
+                              (int)fdiv((uint32_t)(start + tid), a.pages.fd_page)];
+
     int first, span;
     visible<PAGED>(a, b, first, span);
-    const int start = split * a.chunk;  // relative to first
     if (a.splits > 1 && start >= span) return;
     int n = span - start;
     n = n < a.chunk ? n : a.chunk;
@@ -95,7 +117,10 @@ stream_kernel(AttnArgs a) {
         bool ok = i < n;
         const int t = first + start + i;
         if constexpr (PAGED) {
-            int64_t o = ok ? slot_offset(a.pages, b, t) : -1;
+            int64_t o = -1;
+            if (ok)
+                o = a.window == 0 && i == tid ? offset_in_page(a.pages, t, page0)
+                                              : slot_offset(a.pages, b, t);
             ok = o >= 0;
             offs[i] = ok ? o : 0;  // page 0 exists: a readable row
         } else {
@@ -105,31 +130,16 @@ stream_kernel(AttnArgs a) {
         if (lane == 0) *reinterpret_cast<uint64_t*>(seen + (i >> 5)) = w;
     }
 
-    // Queries of this tile: lane (col, g) holds pieces 4f + g of row col.
-    u32x4 qf[NF];
-    {
-        const int r = row0 + col;
-        const bool live = col < rows;
-        const int lq = live ? (int)fdiv((uint32_t)r, a.fd_G) : 0;
-        const S* qr = static_cast<const S*>(a.q) + b * a.q_b + lq * a.q_row +
-                      (int64_t)(h * a.G + (live ? r - lq * a.G : 0)) * a.q_head;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int d = (4 * f + g) * VEC;
-            qf[f] = u32x4{0, 0, 0, 0};
-            if (live && (EXACT || d < a.D)) {
-                qf[f] = *reinterpret_cast<const u32x4*>(qr + d);
-                const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qf[f][i] ^= flip;
-            }
-        }
-    }
     const S* kbase = static_cast<const S*>(a.k) +
                      (PAGED ? h * a.pages.head_stride : b * a.k_b + h * a.k_head);
     const S* vbase = static_cast<const S*>(a.v) +
                      (PAGED ? h * a.pages.head_stride : b * a.v_b + h * a.v_head);
     __syncthreads();
+    if (a.negate)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[f][i] ^= ES == 2 ? 0x80008000u : 0x80000000u;
 
     f32x4 acc[VPL];
 #pragma unroll
@@ -263,12 +273,12 @@ stream_kernel(AttnArgs a) {
     l += __shfl_xor(l, 32);
 
     // Merge the waves: [wave][row][DS] outputs, then [wave][row] maxima and
-    // sums, then [row] merged ones.
+    // sums.  Who writes a piece of a row weighs the waves by itself: NW
+    // exponentials cost less than one more barrier.
     __syncthreads();  // offs and seen are no longer read
     float* mo = reinterpret_cast<float*>(lds);
     float* mm = mo + NW * rows * DS;
     float* ml = mm + NW * 16;
-    float* jm = ml + NW * 16;  // [16] maximum, [16] sum
     if (col < rows) {
         float* o = mo + (wave * rows + col) * DS;
 #pragma unroll
@@ -283,44 +293,30 @@ stream_kernel(AttnArgs a) {
         }
     }
     __syncthreads();
-    if (tid < rows) {
-        float top = mm[tid];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w * 16 + tid]);
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float mw = mm[w * 16 + tid];
-            const float f = mw == -__builtin_huge_valf() ? 0.f : exp2_fast(mw - top);
-            sum += f * ml[w * 16 + tid];
-            mm[w * 16 + tid] = f;
-        }
-        jm[tid] = top;
-        jm[16 + tid] = sum;
-        if (a.direct && a.lse) {
-            const int r = row0 + tid, lq = (int)fdiv((uint32_t)r, a.fd_G);
-            a.lse[((int64_t)b * a.Hq + h * a.G + (r - lq * a.G)) * a.Lq + lq] =
-                top * kLn2 + logf(sum);
-        }
-    }
-    __syncthreads();
     const int pieces = a.D / 4;
     for (int i = tid; i < rows * pieces; i += (64 * NW)) {
         const int r = i / pieces, d = (i - r * pieces) * 4;
+        float top = mm[r];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w * 16 + r]);
+        const float low = top == -__builtin_huge_valf() ? 0.f : top;  // no key: factors 0
+        float sum = 0.f;
         f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = mm[w * 16 + r];
+            const float f = exp2_fast(mm[w * 16 + r] - low);
+            sum = fmaf(f, ml[w * 16 + r], sum);
             const f32x4 x = *reinterpret_cast<const f32x4*>(mo + (w * rows + r) * DS + d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[e], o[e]);
         }
         if (a.direct) {
-            const float sum = jm[16 + r];
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int rr = row0 + r, lq = (int)fdiv((uint32_t)rr, a.fd_G);
-            S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row +
-                    (int64_t)(h * a.G + (rr - lq * a.G)) * a.o_head + d;
+            const int hq = h * a.G + (rr - lq * a.G);
+            S* to = static_cast<S*>(a.out) + b * a.o_b + lq * a.o_row + (int64_t)hq * a.o_head + d;
+            if (d == 0 && a.lse)
+                a.lse[((int64_t)b * a.Hq + hq) * a.Lq + lq] = top * kLn2 + logf(sum);
             if constexpr (ES == 2) {
                 u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv),
                         mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
@@ -332,8 +328,8 @@ stream_kernel(AttnArgs a) {
             const int64_t part = ((int64_t)bh * a.splits + split) * a.R + row0 + r;
             *reinterpret_cast<f32x4*>(a.part_o + part * a.D + d) = o;
             if (d == 0) {
-                a.part_ml[2 * part] = jm[r];
-                a.part_ml[2 * part + 1] = jm[16 + r];
+                a.part_ml[2 * part] = top;
+                a.part_ml[2 * part + 1] = sum;
             }
         }
     }
@@ -590,7 +586,7 @@ hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
     const int rows = a.R < 16 ? a.R : 16;
     const size_t stage = (PAGED ? (size_t)a.chunk * 8 : 0) + (size_t)(a.chunk / 32 + 2) * 4;
     const auto lds = [&](int nw) {
-        const size_t merge = (size_t)(nw * rows * (DP + 4) + 2 * nw * 16 + 32) * 4;
+        const size_t merge = (size_t)(nw * rows * (DP + 4) + 2 * nw * 16) * 4;
         return stage > merge ? stage : merge;
     };
     // as many waves as the registers allow (512 per lane and SIMD)

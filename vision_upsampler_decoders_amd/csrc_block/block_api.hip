@@ -455,9 +455,10 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
     a.words = (int)(round_up(max_length > 0 ? max_length : 1, 1024) / 64);
     const int64_t excess = max_length > keep ? max_length - keep : 0;
     const int64_t moves = excess < keep ? excess : keep;
-    const int64_t room = (kEvictLds - a.words * 12) / 4;  // (a few slots: all of them)
+    const int64_t room = (kEvictLds - a.words * 12) / 4;
     a.list = (int)(moves < room ? moves : room);
-    a.fused = keep <= kFusedKeep && lengths_out != lengths;
+    // (one kernel writes lengths_out while other heads may still read the counts)
+    a.fused = keep <= kFusedKeep && lengths_out != lengths && lengths_out != now;
     a.chunks = (int)(D * (int64_t)esize(dtype) / 16);
     a.fd_chunks = make_fastdiv((uint32_t)a.chunks);
     if ((__int128)B * Hkv * ceil_div(keep, 64) > kMaxInt) return CTCONV_ERR_SHAPE;

@@ -24,12 +24,15 @@ struct Pages {
     FastDiv fd_page;
 };
 
-// Element offset (within a head) of slot t, or -1 where it has no page.
-__device__ inline int64_t slot_offset(const Pages& p, int b, int t) {
-    const int col = (int)fdiv((uint32_t)t, p.fd_page);
-    const int page = p.table[b * p.table_stride + col];
+// Element offset (within a head) of slot t, which lies in `page`, or -1 where
+// there is no such page.
+__device__ inline int64_t offset_in_page(const Pages& p, int t, int32_t page) {
     if (page < 0 || page >= p.num_pages) return -1;
-    return (int64_t)page * p.page_stride + (int64_t)(t - col * p.page_size) * p.slot_stride;
+    const int at = t - (int)fdiv((uint32_t)t, p.fd_page) * p.page_size;
+    return (int64_t)page * p.page_stride + (int64_t)at * p.slot_stride;
+}
+__device__ inline int64_t slot_offset(const Pages& p, int b, int t) {
+    return offset_in_page(p, t, p.table[b * p.table_stride + (int)fdiv((uint32_t)t, p.fd_page)]);
 }
 
 __device__ inline int clamped(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
