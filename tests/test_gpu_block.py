@@ -339,6 +339,23 @@ def test_cache_evict(cc, case, dt):
     assert np.array_equal(to_host(c.vd), want[1], equal_nan=True)
 
 
+# rows of slots that start anywhere and end inside a group of four; short ones beside long ones
+EVICT_ODD = [
+    (4, 1, 8, 7, [1030, 2, 3, 5], 1, 0, 0, "random"),
+    (6, 1, 8, 7, [1030, 2, 3, 4, 1, 0], 2, 1, 0, "ties"),
+    (2, 3, 8, 7, [4099, 1025], 1000, 4, 32, "nan"),
+    (3, 1, 8, 13, [1039, 1037, 1038], 1030, 0, 0, "ties"),
+    (1, 2, 8, 5, [8190], 4097, 3, 5, "close"),
+    (2, 2, 8, 3, [4097, 2050], 2049, 0, 0, "level"),
+]
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("case", EVICT_ODD, ids=[str(i) for i in range(len(EVICT_ODD))])
+def test_cache_evict_odd_rows(cc, case, dt):
+    test_cache_evict(cc, case, dt)
+
+
 def test_cache_evict_in_place_and_missing_pages(cc):
     """The helper's in-place form: weights, positions and lengths are updated
     in their buffers, slots from keep on stay; rows without a page do not move."""

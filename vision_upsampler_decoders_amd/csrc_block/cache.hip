@@ -9,6 +9,12 @@ namespace block {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// N slots' values at once; slot arrays are only aligned to one value
+template <int N>
+struct Slots {
+    typedef float weights __attribute__((ext_vector_type(N), aligned(4)));
+    typedef int numbers __attribute__((ext_vector_type(N), aligned(4)));
+};
 
 // ---------------------------------------------------------------------------
 // Append.  Pure copying: 16 bytes of K and of V per lane and step, four steps
@@ -81,22 +87,43 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Evict, first kernel: which slots stay.  One workgroup per sequence and
 // head.  A slot's rank is a 32-bit key that orders like (protected, weight);
 // the m-th largest key is found digit by digit from the top (8 bits a pass,
-// counted in LDS with one private column per lane so that equal digits do
-// not collide), then one bit per slot says who stays, and prefix sums over
-// the 64-slot words pair the holes below m with the kept slots from m on.
+// counted in LDS in 32 columns so that lanes with equal digits hardly
+// collide), then one bit per slot says who stays, and prefix sums over the
+// 64-slot words pair the holes below m with the kept slots from m on.
+// Two passes over the slots as a rule: the first digit, then the keys that
+// share it and the next are gathered in LDS.  Everything is counted in
+// integers, so no order of the atomics changes a result.
+// 64 heads of up to 40001 slots: 29 us, bound by one compute unit's vector
+// instructions per head; then 36 us for the rows (below).  A few hundred slots
+// are one kernel, select and fill together.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kDigits = 256, kColumns = 32;
-constexpr int kBatch = 8;
+constexpr int kBatch = 2;                    // rounds in flight
 constexpr int kNear = 2048;  // keys gathered in LDS
 
-__device__ inline uint32_t rank_key(float w, bool safe) {
-    if (safe) return 0xFFFFFFFFu;
-    // NaN below everything; above the largest finite number as that
-    w = w != w ? -__builtin_huge_valf() : fminf(w, 3.402823466e38f);
-    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);  // -0 ranks like 0
-    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+// Orders like the weight: NaN like minus infinity, infinity like the largest
+// finite number, -0 like 0.  0 and 0xFFFFFFFF are no weight's key.
+__device__ inline uint32_t rank_key(float w) {
+    w = fminf(fmaxf(w + 0.f, -__builtin_huge_valf()), 3.402823466e38f);
+    const uint32_t u = __float_as_uint(w);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// Bits t .. t + N - 1 of a bit map from N slots of each lane (t = N times the
+// lane, from a multiple of 64 N).
+template <int N>
+__device__ inline void put_bits(uint64_t* map, int t, uint32_t mine) {
+    if constexpr (N == 1) {
+        const uint64_t w = __ballot(mine);
+        if ((threadIdx.x & 63) == 0) map[t >> 6] = w;
+    } else {
+        // two lanes' bits make a byte
+        const uint32_t next = __builtin_amdgcn_mov_dpp((int)mine, 0xF5, 0xF, 0xF, true);
+        if (!(threadIdx.x & 1))
+            reinterpret_cast<uint8_t*>(map)[t >> 3] = (uint8_t)(mine | next << 4);
+    }
 }
 
 // Exclusive prefix sums of v[0, n) in place; the total is returned to every
@@ -218,11 +245,15 @@ __device__ inline void fill_slots(const EvictArgs& a, int b, int h, const int (&
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// KEYS > 0: the keys of up to KEYS * kSelThreads slots stay in registers;
-// KEYS = 0: computed again from memory for each pass, in a loop.  (All 40 keys
-// of 40001 slots in registers took 37 us: every pass is then straight-line
-// code that runs once, at the rate at which instructions are fetched.)
-template <class S, int KEYS>
+// N slots per thread and round.  N = 1: one round, the keys stay in registers.
+// N = 4: more than kSelThreads slots; the keys are computed again from memory
+// for each pass, in a loop.  (All 40 keys of 40001 slots in registers took
+// 37 us: every pass is then straight-line code that runs once, at the rate at
+// which instructions are fetched.  One slot per thread and round took 39 us,
+// four 29: with no conversion behind a branch and one address for four, a pass
+// costs half the instructions, which bound it; more loads in flight change
+// nothing.  320 slots: 9.2 us with N = 1, 9.8 with N = 4.)
+template <class S, int N>
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     extern __shared__ __align__(16) uint32_t lds[];
     __shared__ int wave_sums[kSelWaves], found[4], digits[kDigits];
@@ -235,7 +266,8 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     uint64_t* ties = reinterpret_cast<uint64_t*>(work);  // later: a.words
     int* spare = reinterpret_cast<int*>(work);           // last: a.list kept slots from m on
     const int bh = blockIdx.x, b = bh / a.Hkv, h = bh - b * a.Hkv;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = clamped(a.lengths[b], a.pages.slots);
     const int m = n < a.keep ? n : a.keep;
     const float* weight = a.weight_sum + b * a.slot_b + h * a.slot_h;
@@ -245,40 +277,69 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const bool all = n == m;
     int moves = 0;
 
-    const int rounds = (n + kSelThreads - 1) / kSelThreads;
     if (!all) {
-        const auto key_of = [&](float w, int pos) {
-            return rank_key(w, pos < a.sink || (int64_t)pos >= seen - a.recent);
+        // protected: positions outside [sink, sink + open), one comparison
+        const int64_t edge_pos = seen - a.recent;
+        const uint32_t open = edge_pos > a.sink ? (uint32_t)(edge_pos - a.sink) : 0u;
+        // Keys of slots t .. t + N - 1; 0 for those past n.  The last N slots
+        // stand in for what would reach past them, then are shifted in place.
+        // No load is behind a branch.
+        typedef typename Slots<N>::weights Weights;
+        typedef typename Slots<N>::numbers Numbers;
+        const int last = n > N ? n - N : 0;
+        const int32_t* position_or = position ? position : reinterpret_cast<const int32_t*>(weight);
+        const auto load = [&](int t, Weights& w, Numbers& pos) {
+            const int at = t < last ? t : last;
+            w = *reinterpret_cast<const Weights*>(weight + at);
+            pos = *reinterpret_cast<const Numbers*>(position_or + at);
         };
-        // a batch's loads in flight, none behind a branch
-        const auto load = [&](auto& keys, int i0) {
-            constexpr int N = sizeof(keys) / sizeof(keys[0]);
-            float w[N];
-            int pos[N];
+        const auto keys_of = [&](int t, const Weights& w, const Numbers& pos,
+                                 uint32_t (&key)[N]) {
+            const int at = t < last ? t : last;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                int t = (i0 + i) * kSelThreads + tid;
-                t = t < n ? t : n - 1;
-                w[i] = weight[t];
-                pos[i] = position ? position[t] : t;
+            for (int e = 0; e < N; ++e) {
+                const uint32_t k = rank_key(w[e]);
+                const int q = position ? pos[e] : at + e;
+                key[e] = (uint32_t)q - (uint32_t)a.sink < open ? k : 0xFFFFFFFFu;
+            }
+            if (!__any(t + N > n)) return;
+            const int shift = t - at;
+            if constexpr (N == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) key[e] = shift & 1 ? (e < 3 ? key[e + 1] : 0u) : key[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) key[e] = shift & 2 ? (e < 2 ? key[e + 2] : 0u) : key[e];
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) keys[i] = key_of(w[i], pos[i]);
+            for (int e = 0; e < N; ++e) key[e] = t + e < n ? key[e] : 0u;
         };
-        uint32_t held[KEYS > 0 ? KEYS : kBatch];
-        if constexpr (KEYS > 0) load(held, 0);
-        // f(slot, key) for every slot of this thread, whole waves at a time
+        uint32_t held[N];
+        if constexpr (N == 1) {
+            Weights w;
+            Numbers pos;
+            load(tid, w, pos);
+            keys_of(tid, w, pos, held);
+        }
+        // f(t, keys of slots t .. t + N - 1), whole waves at a time
         const auto each = [&](auto f) {
-            if constexpr (KEYS > 0) {
-#pragma unroll
-                for (int i = 0; i < KEYS; ++i)
-                    if (i < rounds) f(i * kSelThreads + tid, held[i]);
+            const int from = N * 64 * wave;
+            if constexpr (N == 1) {
+                if (from < n) f(tid, held);
             } else {
-                for (int i0 = 0; i0 < rounds; i0 += kBatch) {
-                    load(held, i0);
+                constexpr int kRound = N * kSelThreads;
+                for (int t0 = 0; t0 + from < n; t0 += kBatch * kRound) {
+                    Weights w[kBatch];
+                    Numbers pos[kBatch];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        if (i0 + i < rounds) f((i0 + i) * kSelThreads + tid, held[i]);
+                    for (int i = 0; i < kBatch; ++i) load(t0 + i * kRound + N * tid, w[i], pos[i]);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int t = t0 + i * kRound;
+                        if (t + from >= n) break;
+                        uint32_t key[N];
+                        keys_of(t + N * tid, w[i], pos[i], key);
+                        f(t + N * tid, key);
+                    }
                 }
             }
         };
@@ -293,15 +354,19 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
             for (int i = tid; i < kDigits * kColumns; i += kSelThreads) hist[i] = 0;
             __syncthreads();
+            uint32_t* column = hist + (tid & (kColumns - 1));
             const auto count = [&](uint32_t key) {
-                atomicAdd(&hist[((key >> shift) & 255) * kColumns + (tid & (kColumns - 1))], 1u);
+                atomicAdd(&column[__builtin_amdgcn_ubfe(key, shift, 8) * kColumns], 1u);
             };
             if (near_n >= 0) {
                 for (int i = tid; i < near_n; i += kSelThreads)
                     if ((near[i] & mask) == prefix) count(near[i]);
             } else {
-                each([&](int t, uint32_t key) {
-                    if (t < n && (key & mask) == prefix) count(key);
+                // (slots past n count as key 0, below every other)
+                each([&](int, const uint32_t (&key)[N]) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if ((key[e] & mask) == prefix) count(key[e]);
                 });
             }
             __syncthreads();
@@ -345,18 +410,29 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             exact = found[1] == found[2];
             if (near_n < 0 && !exact && found[2] <= kNear) {
                 near_n = found[2];
-                each([&](int t, uint32_t key) {
-                    const uint64_t above = __ballot(t < n && (key & mask) > prefix);
-                    if (lane == 0) bits[t >> 6] = above;
-                    const bool is = t < n && (key & mask) == prefix;
-                    const uint64_t w = __ballot(is);
-                    if (w == 0) return;
-                    int at = 0;  // in any order: what follows does not depend on it
-                    if (lane == 0) at = atomicAdd(&found[3], __popcll(w));
-                    at = __builtin_amdgcn_readfirstlane(at) + __popcll(w & ((1ull << lane) - 1));
-                    if (is) {
-                        near[at] = key;
-                        near_slot[at] = t;
+                each([&](int t, const uint32_t (&key)[N]) {
+                    uint32_t above = 0;
+                    uint64_t equal[N];
+                    int count = 0, at = 0;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        above |= (key[e] & mask) > prefix ? 1u << e : 0u;
+                        equal[e] = __ballot((key[e] & mask) == prefix);
+                        count += __popcll(equal[e]);
+                    }
+                    put_bits<N>(bits, t, above);
+                    if (count == 0) return;
+                    // in any order: what follows does not depend on it
+                    if (lane == 0) at = atomicAdd(&found[3], count);
+                    at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        if ((equal[e] >> lane) & 1) {
+                            const int i = at + __popcll(equal[e] & ((1ull << lane) - 1));
+                            near[i] = key[e];
+                            near_slot[i] = t + e;
+                        }
+                        at += __popcll(equal[e]);
                     }
                 });
             }
@@ -378,13 +454,15 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 else if (key == prefix) mark(ties, near_slot[i]);
             }
         } else {
-            each([&](int t, uint32_t key) {
-                const uint64_t w = __ballot(t < n && (exact ? key >= prefix : key > prefix));
-                const uint64_t e = __ballot(t < n && key == prefix);
-                if (lane == 0) {
-                    bits[t >> 6] = w;
-                    if (!exact && (t >> 6) < words) ties[t >> 6] = e;
+            each([&](int t, const uint32_t (&key)[N]) {
+                uint32_t stay = 0, tie = 0;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    stay |= (exact ? key[e] >= prefix : key[e] > prefix) ? 1u << e : 0u;
+                    tie |= key[e] == prefix ? 1u << e : 0u;
                 }
+                put_bits<N>(bits, t, stay);
+                if (!exact) put_bits<N>(ties, t, tie);
             });
         }
         __syncthreads();
@@ -424,11 +502,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         }
         __syncthreads();
     }
-    const auto source_of = [&](int j) {
-        if (j >= m) return -1;
-        const uint64_t word = all ? ~0ull : bits[j >> 6];
-        if ((word >> (j & 63)) & 1) return j;
-        const int r = pre[j >> 6] + __popcll(~word & ((1ull << (j & 63)) - 1));
+    const auto spare_at = [&](int r) {
         if (listed) return spare[r];
         // the last word from `edge` on whose kept slots start at or before rank r
         int lo = edge, hi = words - 1;
@@ -440,22 +514,48 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         const uint64_t w = lo == edge ? bits[lo] & ~below : bits[lo];
         return lo * 64 + nth_bit(w, r - (pre[lo] - base));
     };
+    // sources of slots j .. j + M - 1 of one word
+    const auto sources = [&](int j, auto& src) {
+        constexpr int M = sizeof(src) / sizeof(src[0]);
+        const bool some = !all && j < m;
+        const uint64_t word = some ? bits[j >> 6] : ~0ull;
+        int r = some ? pre[j >> 6] + __popcll(~word & ((1ull << (j & 63)) - 1)) : 0;
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            const bool hole = j + e < m && !((word >> ((j + e) & 63)) & 1);
+            src[e] = j + e >= m ? -1 : j + e;
+            if (hole) src[e] = spare_at(r++);
+        }
+    };
     if (!a.fused) {
-#pragma unroll 4
-        for (int j = tid; j < a.keep; j += kSelThreads) source[j] = source_of(j);
+        for (int j = 4 * tid; j < a.keep; j += 4 * kSelThreads) {
+            int src[4];
+            sources(j, src);
+            if (j + 4 <= a.keep) {
+                *reinterpret_cast<Slots<4>::numbers*>(source + j) =
+                    Slots<4>::numbers{src[0], src[1], src[2], src[3]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < a.keep) source[j + e] = src[e];
+            }
+        }
         return;
     }
     MovedRow* rows = reinterpret_cast<MovedRow*>(work + ((a.list + 3) & ~3)) + wave * 64;
     for (int j0 = 0; j0 < a.keep; j0 += kSelThreads) {
         const int js[1] = {j0 + tid};
-        const int srcs[1] = {source_of(js[0])};
+        int srcs[1];
+        sources(js[0], srcs);
         if (js[0] < a.keep) source[js[0]] = srcs[0];
         fill_slots<S, 1>(a, b, h, js, srcs, rows);
     }
     if (a.lengths_out && h == 0 && tid == 0) a.lengths_out[b] = m;
 }
 
-// Second kernel: every wave fills 64 slots kFill times.
+// Second kernel: every wave fills 64 slots kFill times.  Bound by memory: 64
+// heads cut from up to 40001 to 32768 slots (rows of 256 bytes, moved one by
+// one: about 130 MB with the slots' numbers) take 36 us, 3.7 TB/s.
 constexpr int kFillThreads = 256, kFill = 4, kFillSlots = kFillThreads * kFill;
 
 template <class S>
@@ -500,9 +600,8 @@ hipError_t evict_t(const EvictArgs& a, hipStream_t s) {
     if (work < (size_t)a.words * 8) work = (size_t)a.words * 8;
     const size_t lds = (size_t)a.words * 12 + work;
     const int slots = a.words * 64;
-    const void* fn = slots <= kSelThreads     ? reinterpret_cast<const void*>(&select_kernel<S, 1>)
-                     : slots <= 4 * kSelThreads ? reinterpret_cast<const void*>(&select_kernel<S, 4>)
-                                                : reinterpret_cast<const void*>(&select_kernel<S, 0>);
+    const void* fn = slots <= kSelThreads ? reinterpret_cast<const void*>(&select_kernel<S, 1>)
+                                          : reinterpret_cast<const void*>(&select_kernel<S, 4>);
     if (lds > 48u << 10) {
         const hipError_t e =
             hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
