@@ -7,10 +7,11 @@
 // are the two-pass ones (mean, then the mean square of the deviations) over
 // the registers, in fp32.  A row of up to 256 16-byte pieces belongs to one
 // wave, which needs no barrier; longer rows to a workgroup of 256 or 1024.
-// Bound by memory: 32768 rows of 2048 bf16 with a gate take 148 us, 4.5 TB/s
-// (a copy reaches 5.15); one frame's rows take a launch.
+// Bound by memory: 32768 rows of 2048 bf16 with a gate take 115 us, 5.8 TB/s
+// (a copy, half of it writes, reaches 5.15); one frame's rows take a launch.
 
 #include "block_internal.h"
+#include "mfma_common.h"
 
 namespace ctconv {
 namespace block {
@@ -52,8 +53,7 @@ __device__ inline void store_piece(typename TR::storage* p, const float (&f)[VEC
             if constexpr (VEC == 4)
                 r[i] = __float_as_uint(f[i]);
             else
-                r[i] = (uint32_t)TR::from_f32(f[2 * i]) |
-                       ((uint32_t)TR::from_f32(f[2 * i + 1]) << 16);
+                r[i] = mfma::pack2<TR>(f[2 * i], f[2 * i + 1]);
         }
         if constexpr (STREAM)
             __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
@@ -78,52 +78,81 @@ __device__ inline float row_sum(float v, float* red) {
     return v;
 }
 
-// u := norm(u) * w + b over a row of C values, of which this lane holds
-// pieces p0 + i * NT.
-template <class TR, int VEC, int NT, int PIECES>
-__device__ inline void normalise(float (&u)[PIECES][VEC], int kind, const void* w, const void* b,
-                                 const NormArgs& a, int p0, int n_pieces, float* red) {
-    using S = typename TR::storage;
+// u := u - mean, and the factor of the norm over a row of C values, of which
+// this lane holds pieces p0 + i * NT (the rest of u is 0).  No branch writes u:
+// a row held twice where two branches meet costs registers and with them waves
+// (up to 178 registers against 88: 163 us against 115 for the rows above).
+template <int VEC, int NT, int PIECES>
+__device__ inline float centre(float (&u)[PIECES][VEC], int kind, const NormArgs& a, int p0,
+                               int n_pieces, float* red) {
+    float mean = 0.f;
     if (kind == CTCONV_NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s += u[i][e];
-        const float mean = row_sum<NT>(s, red) * a.inv_C;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                u[i][e] = p0 + i * NT < n_pieces ? u[i][e] - mean : 0.f;
+        mean = row_sum<NT>(s, red) * a.inv_C;
     }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const float m = p0 + i * NT < n_pieces ? mean : 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) u[i][e] -= m;
+    }
+    if (kind == CTCONV_NORM_NONE) return 1.f;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s = fmaf(u[i][e], u[i][e], s);
-    const float r = 1.f / sqrtf(row_sum<NT>(s, red) * a.inv_C + a.eps);
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const int p = p0 + i * NT;
-        if (p >= n_pieces) continue;
-        Piece<TR, VEC> pw, pb;
-        if (w) pw.load(static_cast<const S*>(w) + (int64_t)p * VEC);
-        if (b) pb.load(static_cast<const S*>(b) + (int64_t)p * VEC);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float v = u[i][e] * r;
-            if (w) v *= pw.get(e);
-            if (b) v += pb.get(e);
-            u[i][e] = v;
-        }
-    }
+    return 1.f / sqrtf(row_sum<NT>(s, red) * a.inv_C + a.eps);
 }
 
-__device__ inline float gated(float g, int fn) {
-    if (fn == CTCONV_GATE_SIGMOID) return 1.f / (1.f + expf(-g));
-    if (fn == CTCONV_GATE_TANH) return tanhf(g);
-    return g;
+// v := v * r * w + b for the piece at element `at`.
+template <class TR, int VEC>
+__device__ inline void apply(float (&v)[VEC], float r, const void* w, const void* b, int64_t at) {
+    using S = typename TR::storage;
+    Piece<TR, VEC> pw, pb;
+    if (w) pw.load(static_cast<const S*>(w) + at);
+    if (b) pb.load(static_cast<const S*>(b) + at);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] *= r;
+    if (w)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] *= pw.get(e);
+    if (b)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] += pb.get(e);
+}
+
+// The 16-bit types take the hardware's exponential and reciprocal (relative
+// error below 2^-16, beside the types' own 2^-9 and 2^-12): with the exact
+// ones the gate was half of the kernel's instructions.
+template <class TR, int VEC>
+__device__ inline void gate_values(const Piece<TR, VEC>& p, int fn, float (&g)[VEC]) {
+    constexpr bool SHORT = sizeof(typename TR::storage) == 2;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) g[e] = p.get(e);
+    if (fn == CTCONV_GATE_SIGMOID) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            g[e] = SHORT ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g[e] * -kLog2e))
+                         : 1.f / (1.f + expf(-g[e]));
+    } else if (fn == CTCONV_GATE_TANH) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float x = g[e];
+            if constexpr (SHORT) {
+                // 1 - 2 / (1 + e^2x); near 0, where that cancels, x - x^3 / 3
+                const float y = 1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
+                const float far = fmaf(-2.f, __builtin_amdgcn_rcpf(y), 1.f);
+                g[e] = fabsf(x) < 0.03125f ? fmaf(x * x * x, -1.f / 3.f, x) : far;
+            } else {
+                g[e] = tanhf(x);
+            }
+        }
+    }
 }
 
 // NT lanes per row, 256 / NT rows per workgroup of 256 lanes (one row where
@@ -146,6 +175,7 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void norm_kernel(NormArgs a) {
     Piece<TR, VEC> px[PIECES], ph[PIECES], pg[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
+        ph[i].raw = u32x4{0, 0, 0, 0};
         const int p = p0 + i * NT;
         if (p >= n_pieces) continue;
         ph[i].template load<STREAM>(hr + (int64_t)p * VEC);
@@ -156,37 +186,46 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) u[i][e] = p0 + i * NT < n_pieces ? ph[i].get(e) : 0.f;
-    if (a.post != CTCONV_NORM_NONE)
-        normalise<TR, VEC, NT, PIECES>(u, a.post, a.post_w, a.post_b, a, p0, n_pieces, red_all);
+        for (int e = 0; e < VEC; ++e) u[i][e] = ph[i].get(e);
+    const bool post = a.post != CTCONV_NORM_NONE;
+    const float rp = centre<VEC, NT, PIECES>(u, a.post, a, p0, n_pieces, red_all);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
         const int p = p0 + i * NT;
         if (p >= n_pieces) continue;
-        Piece<TR, VEC> ps;
-        if (a.scale) ps.load(static_cast<const S*>(a.scale) + (int64_t)p * VEC);
+        const int64_t at = (int64_t)p * VEC;
+        apply<TR, VEC>(u[i], rp, post ? a.post_w : nullptr, post ? a.post_b : nullptr, at);
+        if (a.scale) {
+            Piece<TR, VEC> ps;
+            ps.load(static_cast<const S*>(a.scale) + at);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float v = u[i][e];
-            if (a.scale) v *= ps.get(e);
-            if (gr) v *= gated(pg[i].get(e), a.gate_fn);
-            u[i][e] = px[i].get(e) + v;
+            for (int e = 0; e < VEC; ++e) u[i][e] *= ps.get(e);
         }
-        store_piece<TR, VEC, STREAM>(static_cast<S*>(a.x_out) + row * a.os + (int64_t)p * VEC, u[i]);
+        if (gr) {
+            float g[VEC];
+            gate_values<TR, VEC>(pg[i], a.gate_fn, g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) u[i][e] *= g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) u[i][e] += px[i].get(e);
+        store_piece<TR, VEC, STREAM>(static_cast<S*>(a.x_out) + row * a.os + at, u[i]);
     }
     if (a.pre == CTCONV_NORM_NONE) return;
-    normalise<TR, VEC, NT, PIECES>(u, a.pre, a.pre_w, a.pre_b, a, p0, n_pieces, red_all);
+    const float r = centre<VEC, NT, PIECES>(u, a.pre, a, p0, n_pieces, red_all);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
         const int p = p0 + i * NT;
-        if (p < n_pieces)
-            store_piece<TR, VEC, STREAM>(static_cast<S*>(a.y) + row * a.ys + (int64_t)p * VEC, u[i]);
+        if (p >= n_pieces) continue;
+        const int64_t at = (int64_t)p * VEC;
+        apply<TR, VEC>(u[i], r, a.pre_w, a.pre_b, at);
+        store_piece<TR, VEC, STREAM>(static_cast<S*>(a.y) + row * a.ys + at, u[i]);
     }
 }
 
 // More than the XCDs' L2 caches hold together: what is written is not there any
 // more when its reader comes, and rows read and written past the caches go
-// faster (32768 rows of 2048 bf16, 671 MB: 148 us against 155).
+// faster (32768 rows of 2048 bf16, 671 MB: 115 us against 127).
 constexpr int64_t kStreamBytes = 32 << 20;
 
 template <class TR, int VEC, int NT, int PIECES>
