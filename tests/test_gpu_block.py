@@ -645,3 +645,54 @@ def test_graph_replay(cc):
         got = outs + [s2[n] for n in "kvwl"]
         for i, (a, b) in enumerate(zip(got, eager[r])):
             assert torch.equal(a, b), (r, i)
+
+
+def test_helpers_refuse(cc):
+    """Arguments that do not fit are refused before any launch."""
+    import torch
+
+    B, H, D, page, cols = 2, 2, 32, 8, 4
+    cache = torch.zeros((10, H, page, D), device="cuda")
+    table = ints(np.zeros((B, cols)))
+    lengths = ints(np.zeros(B))
+    rows = torch.zeros((B, 1, H, D), device="cuda")
+    q = torch.zeros((B, H, D), device="cuda")
+    x = torch.zeros((3, D), device="cuda")
+    slots = torch.zeros((B, H, cols * page), device="cuda")
+    enc = torch.zeros((B, 5, H, D), device="cuda")
+    bad = [
+        (ValueError, lambda: cc.cache_append(rows, rows, cache, cache, table, None)),
+        (TypeError, lambda: cc.cache_append(rows, rows, cache, cache, table, lengths.long())),
+        (ValueError, lambda: cc.cache_append(rows, rows[:, :, :1], cache, cache, table, lengths)),
+        (ValueError, lambda: cc.cache_append(rows, rows, cache, cache[:, :1], table, lengths)),
+        (ValueError, lambda: cc.cache_append(rows, rows, cache, cache, table[:1], lengths)),
+        (ValueError, lambda: cc.cache_append(rows, rows, cache, cache, table, lengths,
+                                             positions=ints(np.zeros((B, H, 3))))),
+        (ValueError, lambda: cc.paged_attention(q, cache, cache, table, None)),
+        (TypeError, lambda: cc.paged_attention(q.half(), cache, cache, table, lengths)),
+        (ValueError, lambda: cc.paged_attention(q[..., :16], cache, cache, table, lengths)),
+        (ValueError, lambda: cc.paged_attention(q, cache, cache, table, lengths.cpu())),
+        (cc.CtconvError, lambda: cc.paged_attention(q, cache, cache, table, lengths, window=-1)),
+        (cc.CtconvError, lambda: cc.paged_attention(q, cache, cache, table, lengths,
+                                                    max_length=cols * page + 1)),
+        (cc.CtconvError, lambda: cc.paged_attention(q, cache, cache, table, lengths,
+                                                    scale=float("nan"))),
+        (ValueError, lambda: cc.cache_evict(cache, cache, table, lengths, None, 4)),
+        (ValueError, lambda: cc.cache_evict(cache, cache, table, lengths, slots, 0)),
+        (ValueError, lambda: cc.cache_evict(cache, cache, table, lengths, slots, 33)),
+        (TypeError, lambda: cc.cache_evict(cache, cache, table, lengths, slots.double(), 4)),
+        (ValueError, lambda: cc.cross_attention(q[:, None], enc, enc[:, :4])),
+        (ValueError, lambda: cc.cross_attention(q[:, None], enc, enc, mask=slots[0, :, :5] > 0,
+                                                lengths=lengths[:1])),
+        (TypeError, lambda: cc.cross_attention(q[:, None], enc, enc, mask=enc[:, :, 0, 0])),
+        (ValueError, lambda: cc.norm_residual(x, x[:2])),
+        (ValueError, lambda: cc.norm_residual(x, x, gate=x)),
+        (ValueError, lambda: cc.norm_residual(x, x, gate=x, gate_fn=cc.GATE_TANH,
+                                              rows_per_gate=2)),
+        (ValueError, lambda: cc.norm_residual(x, x, x_out=torch.zeros((D, 3), device="cuda").t())),
+        (cc.CtconvError, lambda: cc.norm_residual(x, x, eps=-1.0)),
+    ]
+    for i, (kind, call) in enumerate(bad):
+        with pytest.raises(kind):
+            call()
+            say(f"not refused: {i}")

@@ -917,6 +917,11 @@ def _rows_ready(name, t, dtype, device, dims: int):
     return t
 
 
+def _required(name, t):
+    if t is None:
+        raise ValueError(f"{name} is required")
+
+
 def _index(name, t, device, shape, dtype=None):
     """An int32 (or `dtype`) array of `shape` whose last dimension is contiguous, or None."""
     if t is None:
@@ -999,6 +1004,7 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, lengths, counts=Non
     pages, size, cols, H, Dc, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
     if (H, Dc) != (Hkv, D) or page_table.shape[0] != B:
         raise ValueError("the cache's heads, width or table rows do not match k_new")
+    _required("lengths", lengths)
     for name, t in (("lengths", lengths), ("counts", counts), ("now", now)):
         _index(name, t, dev, (B,))
     slots = _slot_arrays((("positions", positions, torch.int32),
@@ -1028,6 +1034,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, max_length=None, w
     pages, size, cols, Hkv, Dc, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
     if Dc != D or page_table.shape[0] != B:
         raise ValueError("the cache's width or table rows do not match q")
+    _required("lengths", lengths)
     _index("lengths", lengths, dev, (B,))
     slots = _slot_arrays((("weight_sum", weight_sum, torch.float32),), B, Hkv, cols * size, dev)
     y = _result(out, (B, Hq, D), dt, dev)
@@ -1056,10 +1063,10 @@ def cache_evict(k_cache, v_cache, page_table, lengths, weight_sum, keep: int, po
         raise ValueError("k_cache must be a device tensor")
     pages, size, cols, Hkv, D, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
     B, slots = page_table.shape[0], cols * size
-    if weight_sum is None:
-        raise ValueError("weight_sum is required")
+    _required("weight_sum", weight_sum)
     if not 1 <= keep <= slots:
         raise ValueError(f"keep must be between 1 and the table's {slots} slots")
+    _required("lengths", lengths)
     for name, t in (("lengths", lengths), ("now", now)):
         _index(name, t, dev, (B,))
     st = _slot_arrays((("weight_sum", weight_sum, torch.float32),
