@@ -87,8 +87,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Evict, first kernel: which slots stay.  One workgroup per sequence and
 // head.  A slot's rank is a 32-bit key that orders like (protected, weight);
 // the m-th largest key is found digit by digit from the top (8 bits a pass,
-// counted in LDS in 32 columns so that lanes with equal digits hardly
-// collide), then one bit per slot says who stays, and prefix sums over the
+// counted in LDS in 4 columns: lanes with equal digits then meet less, and more
+// columns cost more to clear and to add than they save: with 32, 320 slots
+// take 9.3 us instead of 8.3), then one bit per slot says who stays, and prefix sums over the
 // 64-slot words pair the holes below m with the kept slots from m on.
 // Two passes over the slots as a rule: the first digit, then the keys that
 // share it and the next are gathered in LDS.  Everything is counted in
@@ -99,9 +100,14 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
-constexpr int kDigits = 256, kColumns = 32;
+constexpr int kDigits = 256, kColumns = 4;
 constexpr int kBatch = 2;                    // rounds in flight
 constexpr int kNear = 2048;  // keys gathered in LDS
+
+// LDS words for the digits' counts, then for the ties' bit map.
+__host__ __device__ inline int count_words(int map_words) {
+    return 2 * map_words > kDigits * kColumns ? 2 * map_words : kDigits * kColumns;
+}
 
 // Orders like the weight: NaN like minus infinity, infinity like the largest
 // finite number, -0 like 0.  0 and 0xFFFFFFFF are no weight's key.
@@ -252,16 +258,17 @@ __device__ inline void fill_slots(const EvictArgs& a, int b, int h, const int (&
 // which instructions are fetched.  One slot per thread and round took 39 us,
 // four 29: with no conversion behind a branch and one address for four, a pass
 // costs half the instructions, which bound it; more loads in flight change
-// nothing.  320 slots: 9.2 us with N = 1, 9.8 with N = 4.)
+// nothing.  320 slots: N = 1 takes
+// 0.6 us of 9 less than N = 4.)
 template <class S, int N>
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     extern __shared__ __align__(16) uint32_t lds[];
-    __shared__ int wave_sums[kSelWaves], found[4], digits[kDigits];
+    __shared__ int wave_sums[kSelWaves], found[4];
     uint64_t* bits = reinterpret_cast<uint64_t*>(lds);   // a.words: who stays
     int* pre = reinterpret_cast<int*>(bits + a.words);   // a.words prefix sums
     uint32_t* work = reinterpret_cast<uint32_t*>(pre + a.words);
     uint32_t* hist = work;                               // kDigits x kColumns
-    uint32_t* near = hist + kDigits * kColumns;          // kNear keys and slots
+    uint32_t* near = work + count_words(a.words);        // kNear keys and slots
     int* near_slot = reinterpret_cast<int*>(near + kNear);
     uint64_t* ties = reinterpret_cast<uint64_t*>(work);  // later: a.words
     int* spare = reinterpret_cast<int*>(work);           // last: a.list kept slots from m on
@@ -370,20 +377,13 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 });
             }
             __syncthreads();
-            // four threads add up a digit's columns
-            int c = 0;
-            for (int i = 0; i < kColumns / 4; ++i)
-                c += hist[(tid >> 2) * kColumns + (((tid & 3) + 4 * (i + (tid >> 2))) & (kColumns - 1))];
-            c += __shfl_xor(c, 1);
-            c += __shfl_xor(c, 2);
-            if ((tid & 3) == 0) digits[tid >> 2] = c;
-            __syncthreads();
             if (wave == 0) {
                 // lane l: digits 255 - 4l .. 252 - 4l, from the top
                 int d[4], sum = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    d[i] = digits[255 - 4 * lane - i];
+                    const u32x4 c = reinterpret_cast<const u32x4*>(hist)[255 - 4 * lane - i];
+                    d[i] = (int)(c[0] + c[1] + c[2] + c[3]);
                     sum += d[i];
                 }
                 int inc = sum;
@@ -594,10 +594,9 @@ hipError_t append_t(const AppendArgs& a, hipStream_t s) {
 
 template <class S>
 hipError_t evict_t(const EvictArgs& a, hipStream_t s) {
-    const size_t count = (kDigits * kColumns + 2 * kNear) * 4;
+    const size_t count = (size_t)(count_words(a.words) + 2 * kNear) * 4;
     size_t work = (size_t)((a.list + 3) & ~3) * 4 + (a.fused ? kSelThreads * sizeof(MovedRow) : 0);
     if (work < count) work = count;
-    if (work < (size_t)a.words * 8) work = (size_t)a.words * 8;
     const size_t lds = (size_t)a.words * 12 + work;
     const int slots = a.words * 64;
     const void* fn = slots <= kSelThreads ? reinterpret_cast<const void*>(&select_kernel<S, 1>)
