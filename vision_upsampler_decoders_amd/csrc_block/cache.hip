@@ -89,8 +89,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // the m-th largest key is found digit by digit from the top (8 bits a pass,
 // counted in LDS in 4 columns: lanes with equal digits then meet less, and more
 // columns cost more to clear and to add than they save: with 32, 320 slots
-// take 9.3 us instead of 8.3), then one bit per slot says who stays, and prefix sums over the
-// 64-slot words pair the holes below m with the kept slots from m on.
+// take 9.3 us instead of 8.3), then one bit per slot says who stays, and
+// prefix sums over the 64-slot words pair the holes below m with the kept
+// slots from m on.
 // Two passes over the slots as a rule: the first digit, then the keys that
 // share it and the next are gathered in LDS.  Everything is counted in
 // integers, so no order of the atomics changes a result.
