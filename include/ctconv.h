@@ -555,8 +555,10 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
  *   now           device int32 [B] (rows seen in all), or NULL: lengths
  *   weight_out, positions_out   device [B, Hkv, keep], out_slot_strides =
  *                 batch, head: the values that slots [0, m) now have, then 0
- *                 and -1 up to keep; may be the input buffers (same strides),
- *                 in which case slots from keep on are left as they are.
+ *                 and -1 up to keep; rows of keep values lie apart.  May be the
+ *                 input buffers (same strides, keep at most their max_pages *
+ *                 page_size slots; CTCONV_ERR_SHAPE), in which case slots from
+ *                 keep on are left as they are.
  *                 positions_out may be NULL when positions is.
  *   lengths_out   device int32 [B], gets m; may be lengths; or NULL
  *   source        device int32 [B, Hkv, keep] dense: the slot that each of
@@ -565,7 +567,8 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
  * another sequence.  A row whose old or new slot has no page is not moved.
  * keep >= 1, sink >= 0, recent >= 0 (CTCONV_ERR_PARAM); max_length (a bound
  * on lengths) at most max_pages * page_size and 262144 (CTCONV_ERR_SHAPE).
- * keep may exceed the lengths: then nothing is given up.
+ * keep may exceed the lengths, and the table's slots where the results have
+ * arrays of their own: then nothing is given up.
  */
 ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* page_table,
                                  const int32_t* lengths, const int32_t* now,

@@ -48,6 +48,32 @@ bool rows_aligned(const int64_t* strides, const int64_t* sizes, int n, ctconv_dt
     return true;
 }
 
+// What is written: rows of `row` values that lie apart.  From the smallest
+// stride up, a step must pass everything below it.  (A layout whose dimensions
+// interleave without meeting is not told from one where they meet.)
+bool rows_apart(const int64_t* strides, std::initializer_list<int64_t> sizes, int64_t row) {
+    constexpr int kDims = 3;
+    int64_t step[kDims], size[kDims];
+    int n = 0, dim = 0;
+    for (const int64_t s : sizes) {
+        const int64_t st = strides[dim++];
+        if (s <= 1) continue;
+        int at = n++;
+        for (; at > 0 && step[at - 1] > st; --at) {
+            step[at] = step[at - 1];
+            size[at] = size[at - 1];
+        }
+        step[at] = st;
+        size[at] = s;
+    }
+    __int128 extent = row;
+    for (int i = 0; i < n; ++i) {
+        if (step[i] < extent) return false;
+        extent += (__int128)(size[i] - 1) * step[i];
+    }
+    return true;
+}
+
 struct Check {
     ctconv_status st = CTCONV_OK;
     bool align = true;
@@ -424,10 +450,15 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
     if (c.st == CTCONV_OK) c.st = slot_strides_ok(out_slot_strides, B, Hkv, keep);
     st = c.status();
     if (st != CTCONV_OK) return st;
-    // in place: the same slots
-    if ((weight_out == weight_sum || (positions && positions_out == positions)) &&
-        (slot_strides[0] != out_slot_strides[0] || slot_strides[1] != out_slot_strides[1]))
-        return CTCONV_ERR_PARAM;
+    // rows of `keep` results: a shorter one would run into the next head's, which another
+    // workgroup may still be reading
+    if (!rows_apart(out_slot_strides, {B, Hkv}, keep)) return CTCONV_ERR_SHAPE;
+    // in place: the same slots, and no more of them than there are
+    if (weight_out == weight_sum || (positions && positions_out == positions)) {
+        if (keep > page_size * max_pages) return CTCONV_ERR_SHAPE;
+        if (slot_strides[0] != out_slot_strides[0] || slot_strides[1] != out_slot_strides[1])
+            return CTCONV_ERR_PARAM;
+    }
     EvictArgs a;
     memset(&a, 0, sizeof(a));
     a.k = k_cache;
