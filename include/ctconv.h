@@ -458,7 +458,9 @@ ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int it
  * so are the rows they step to (every stride a multiple of 16 bytes) unless
  * a function says otherwise; CTCONV_ERR_ALIGN if not.  Index arrays are
  * int32.  A size below its minimum, or one that does not fit the kernel's
- * 64-bit addressing, is CTCONV_ERR_SHAPE.  With no row to compute (B, Lq or
+ * 64-bit addressing, is CTCONV_ERR_SHAPE, and so is what a call would write
+ * with strides that do not keep its rows apart (from the smallest stride up,
+ * a step must pass all that lies below it).  With no row to compute (B, Lq or
  * rows of 0) nothing is enqueued and pointers may be NULL.  Results do not
  * depend on the launch: no atomics, every sum in a fixed order.
  *

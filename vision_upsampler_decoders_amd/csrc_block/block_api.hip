@@ -300,6 +300,9 @@ ctconv_status ctconv_cache_append(const void* k_new, const void* v_new, void* k_
         c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
     st = c.status();
     if (st != CTCONV_OK) return st;
+    if (!rows_apart(kv_strides, {num_pages, page_size, Hkv}, D) ||
+        (slots && !rows_apart(slot_strides, {B, Hkv}, page_size * max_pages)))
+        return CTCONV_ERR_SHAPE;
     AppendArgs a;
     memset(&a, 0, sizeof(a));
     a.k_new = k_new;
@@ -382,6 +385,9 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
         c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
     st = c.status();
     if (st != CTCONV_OK) return st;
+    if (!rows_apart(out_strides, {B, Hq}, D) ||
+        (weight_sum && !rows_apart(slot_strides, {B, Hkv}, max_length)))
+        return CTCONV_ERR_SHAPE;
     if (p.bytes > 0 && (!workspace || workspace_bytes < (size_t)p.bytes))
         return CTCONV_ERR_WORKSPACE;
     AttnArgs a;
@@ -450,6 +456,7 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
     if (c.st == CTCONV_OK) c.st = slot_strides_ok(out_slot_strides, B, Hkv, keep);
     st = c.status();
     if (st != CTCONV_OK) return st;
+    if (!rows_apart(kv_strides, {num_pages, page_size, Hkv}, D)) return CTCONV_ERR_SHAPE;
     // rows of `keep` results: a shorter one would run into the next head's, which another
     // workgroup may still be reading
     if (!rows_apart(out_slot_strides, {B, Hkv}, keep)) return CTCONV_ERR_SHAPE;
@@ -532,6 +539,7 @@ ctconv_status ctconv_cross_attention(const void* q, const void* k, const void* v
     c.pointer(workspace);
     st = c.status();
     if (st != CTCONV_OK) return st;
+    if (!rows_apart(out_strides, {B, Lq, Hq}, D)) return CTCONV_ERR_SHAPE;
     if (p.bytes > 0 && (!workspace || workspace_bytes < (size_t)p.bytes))
         return CTCONV_ERR_WORKSPACE;
     AttnArgs a;
