@@ -470,11 +470,13 @@ ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int it
  *       + (t % page_size) * kv_strides[1] + head * kv_strides[2]
  * in both (kv_strides = page, slot, head).  The library's own layout is
  * [num_pages][Hkv][page_size][D]; any other order works by its strides.  A
- * page may be any size from 1 and page_table has max_pages columns.  Slots
- * whose table entry is outside [0, num_pages) are never touched: attention
- * does not see them, append and evict leave them out.  lengths[b], the
- * slots in use, is clamped to [0, min(max_length, max_pages * page_size)] by
-the calls that take max_length.
+ * page may be any size from 1 and page_table has max_pages columns.  A slot
+ * whose table entry is outside [0, num_pages) has no row: no call reads or
+ * writes one for it, attention does not see it, and evict leaves it where it
+ * is or gives it up, but never moves it or moves a row to it.  (Its place in
+ * the arrays of positions and weights is written by append like any other's.)
+ * lengths[b], the slots in use, is clamped to [0, min(max_length, max_pages *
+ * page_size)] by the calls that take max_length.
  * What lies past lengths[b] in a page is never used, whatever bits it holds.
  * ---------------------------------------------------------------------- */
 
@@ -548,7 +550,9 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
  * lengths[b] and m = min(n, keep), each head keeps m of its n slots: those
  * whose position is below `sink` or at least now[b] - recent, then those of
  * largest weight (a NaN weight counts as the smallest, weights above the
- * largest finite number as that); ties go to the lowest slot.  Kept slots
+ * largest finite number as that); ties go to the lowest slot.  Slots
+ * without a page are not chosen among: those below m stay and count as kept,
+ * those from m on are given up.  Kept slots
  * below m stay where they are, and the slots below m that are given up, in
  * ascending order, take the kept slots from m on, in ascending order: only
  * as many rows move as there are holes, and the result is dense in [0, m).
@@ -566,7 +570,7 @@ ctconv_status ctconv_paged_attention(const void* q, const void* k_cache, const v
  *   source        device int32 [B, Hkv, keep] dense: the slot that each of
  *                 the slots [0, m) came from, then -1 up to keep
  * K and V rows move in place; no page of the sequences may be shared with
- * another sequence.  A row whose old or new slot has no page is not moved.
+ * another sequence.
  * keep >= 1, sink >= 0, recent >= 0 (CTCONV_ERR_PARAM); max_length (a bound
  * on lengths) at most max_pages * page_size and 262144 (CTCONV_ERR_SHAPE).
  * keep may exceed the lengths, and the table's slots where the results have

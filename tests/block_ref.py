@@ -138,7 +138,10 @@ def evict(kc, vc, table, lengths, now, weights, positions, page, keep, sink, rec
             w = weights[b, h, :n].astype(np.float64)
             w = np.where(np.isnan(w), -np.inf, np.minimum(w, np.finfo(np.float32).max))
             safe = (pos < sink) | (pos >= seen - recent)
-            order = sorted(range(n), key=lambda t: (not safe[t], 0.0 if safe[t] else -w[t], t))
+            page_of = table[b, np.arange(n) // page]
+            gap = (page_of < 0) | (page_of >= kc.shape[0])  # stays below m, given up from m on
+            group = np.where(gap, np.where(np.arange(n) < m, 0, 3), np.where(safe, 1, 2))
+            order = sorted(range(n), key=lambda t: (group[t], -w[t] if group[t] == 2 else 0.0, t))
             kept = np.zeros(n, bool)
             kept[order[:m]] = True
             src = np.arange(m)
@@ -149,9 +152,8 @@ def evict(kc, vc, table, lengths, now, weights, positions, page, keep, sink, rec
             p_out[b, h, :m] = src if positions is None else positions[b, h, src]
             for j in holes:
                 p1, p0 = table[b, j // page], table[b, src[j] // page]
-                if 0 <= p0 < kc.shape[0] and 0 <= p1 < kc.shape[0]:
-                    kc[p1, h, j % page] = kc[p0, h, src[j] % page]
-                    vc[p1, h, j % page] = vc[p0, h, src[j] % page]
+                kc[p1, h, j % page] = kc[p0, h, src[j] % page]
+                vc[p1, h, j % page] = vc[p0, h, src[j] % page]
     return kc, vc, w_out, p_out, l_out, source
 
 

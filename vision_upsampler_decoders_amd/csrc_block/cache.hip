@@ -92,6 +92,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // take 9.3 us instead of 8.3), then one bit per slot says who stays, and
 // prefix sums over the 64-slot words pair the holes below m with the kept
 // slots from m on.
+// A slot without a page has no row that could move: below m it stays where it
+// is, ranked above every other, so that it is neither a hole nor a source; from
+// m on it is given up, ranked below every other (n - m slots lie there, so
+// enough with a page remain).  Only sequences that have such a slot look up the
+// page of each.
 // Two passes over the slots as a rule: the first digit, then the keys that
 // share it and the next are gathered in LDS.  Everything is counted in
 // integers, so no order of the atomics changes a result.
@@ -111,7 +116,10 @@ __host__ __device__ inline int count_words(int map_words) {
 }
 
 // Orders like the weight: NaN like minus infinity, infinity like the largest
-// finite number, -0 like 0.  0 and 0xFFFFFFFF are no weight's key.
+// finite number, -0 like 0.  No weight's key is as small as those of slots past
+// the end (0) and of given up ones without a page, or as large as those of
+// protected slots and of ones without a page that stay.
+constexpr uint32_t kNoPageGone = 1u, kProtected = 0xFFFFFFFEu, kNoPageStays = 0xFFFFFFFFu;
 __device__ inline uint32_t rank_key(float w) {
     w = fminf(fmaxf(w + 0.f, -__builtin_huge_valf()), 3.402823466e38f);
     const uint32_t u = __float_as_uint(w);
@@ -276,6 +284,12 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const int bh = blockIdx.x, b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int32_t* table = a.pages.table + b * a.pages.table_stride;
+    const auto pages_of = [&](int slots) {
+        return (int)fdiv((uint32_t)slots + (uint32_t)a.pages.page_size - 1, a.pages.fd_page);
+    };
+    // (asked for before the length has arrived)
+    const int32_t page0 = tid < pages_of(a.pages.slots) ? table[tid] : 0;
     const int n = clamped(a.lengths[b], a.pages.slots);
     const int m = n < a.keep ? n : a.keep;
     const float* weight = a.weight_sum + b * a.slot_b + h * a.slot_h;
@@ -295,6 +309,24 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         typedef typename Slots<N>::weights Weights;
         typedef typename Slots<N>::numbers Numbers;
         const int last = n > N ? n - N : 0;
+        // Does a slot lie in no page?  The waves' answers meet behind the barrier
+        // that the cleared counts need.
+        const auto missing = [&](int32_t page) {
+            return (uint32_t)page >= (uint32_t)a.pages.num_pages;
+        };
+        const int pages = pages_of(n);
+        bool gap = tid < pages && missing(page0);
+#pragma unroll 8
+        for (int i = tid + kSelThreads; i < pages; i += kSelThreads) gap |= missing(table[i]);
+        gap = __any(gap);
+        if (lane == 0) wave_sums[wave] = gap;
+        const auto clear = [&]() {
+            for (int i = tid; i < kDigits * kColumns; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+        };
+        clear();
+        gap = __any(wave_sums[lane % kSelWaves] != 0);
+        const bool gaps = __builtin_amdgcn_readfirstlane(gap);
         const int32_t* position_or = position ? position : reinterpret_cast<const int32_t*>(weight);
         const auto load = [&](int t, Weights& w, Numbers& pos) {
             const int at = t < last ? t : last;
@@ -308,7 +340,13 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             for (int e = 0; e < N; ++e) {
                 const uint32_t k = rank_key(w[e]);
                 const int q = position ? pos[e] : at + e;
-                key[e] = (uint32_t)q - (uint32_t)a.sink < open ? k : 0xFFFFFFFFu;
+                key[e] = (uint32_t)q - (uint32_t)a.sink < open ? k : kProtected;
+            }
+            if (gaps) {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (missing(table[fdiv((uint32_t)(at + e), a.pages.fd_page)]))
+                        key[e] = at + e < m ? kNoPageStays : kNoPageGone;
             }
             if (!__any(t + N > n)) return;
             const int shift = t - at;
@@ -360,8 +398,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         int near_n = -1;
         if (tid == 0) found[3] = 0;
         for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
-            for (int i = tid; i < kDigits * kColumns; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
+            if (shift < 24) clear();
             uint32_t* column = hist + (tid & (kColumns - 1));
             const auto count = [&](uint32_t key) {
                 atomicAdd(&column[__builtin_amdgcn_ubfe(key, shift, 8) * kColumns], 1u);
