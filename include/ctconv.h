@@ -520,7 +520,10 @@ ctconv_status ctconv_cache_append(const void* k_new, const void* v_new, void* k_
  *                 += the sum of p[t] over the query heads of h (slots outside
  *                 the window and past lengths[b] are left as they are);
  *                 slot_strides as in ctconv_cache_append
- * A sequence without a visible slot gets out = 0 and lse = -infinity.
+ * A sequence without a visible slot gets out = 0 and lse = -infinity, and so
+ * does a row whose scores are all -infinity.  A NaN in a row's query, or in a
+ * key that it sees, makes its out, its lse and the weights of the slots it
+ * sees NaN.
  * max_length: a bound on lengths that the caller knows (the work is split
  * and the workspace sized by it), 0 .. max_pages * page_size.  The reduction
  * over slots is split over workgroups and joined in a fixed order.
@@ -599,7 +602,8 @@ ctconv_status ctconv_cache_evict(void* k_cache, void* v_cache, const int32_t* pa
  *                sequence, no alignment
  *   lse          device fp32 [B, Hq, Lq] dense, or NULL
  * Rows of k and v that are not seen are never used, whatever bits they hold.
- * A sequence that sees no row gets out = 0 and lse = -infinity.
+ * A sequence that sees no row gets out = 0 and lse = -infinity; -infinity and
+ * NaN among the scores as in ctconv_paged_attention.
  * k and v may be NULL when Lk = 0.  Workspace, D, heads and scale as in
  * ctconv_paged_attention.
  */

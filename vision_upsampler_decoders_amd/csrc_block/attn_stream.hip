@@ -50,6 +50,13 @@ constexpr float kRaise = 8.f;
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A maximum as what weights are taken against: where nothing is seen (minus
+// infinity), 0, so that the weights of hidden scores are zero and a sum that
+// is NaN (no maximum is, see fmaxf) stays NaN.
+__device__ inline float reference_of(float top) {
+    return top == -__builtin_huge_valf() ? 0.f : top;
+}
+
 // The keys of sequence b that the call sees: [first, first + span).
 template <bool PAGED>
 __device__ inline void visible(const AttnArgs& a, int b, int& first, int& span) {
@@ -250,7 +257,7 @@ stream_kernel(AttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[e][i] *= f;
         }
-        const float ref = m == -__builtin_huge_valf() ? 0.f : m;
+        const float ref = reference_of(m);
         float p[VK];
 #pragma unroll
         for (int j = 0; j < VK; ++j) {
@@ -309,7 +316,7 @@ stream_kernel(AttnArgs a) {
         float top = mm[r];
 #pragma unroll
         for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w * 16 + r]);
-        const float low = top == -__builtin_huge_valf() ? 0.f : top;  // no key: factors 0
+        const float low = reference_of(top);  // no key: factors 0
         float sum = 0.f;
         f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -392,14 +399,11 @@ __device__ inline void join_stats(const float* const (&ml)[N], int64_t stride, i
 #pragma unroll
     for (int r = 0; r < N; ++r) {
         sum[r] = 0.f;
+        const float ref = reference_of(top[r]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (v[r][i][0] != -__builtin_huge_valf())
-                sum[r] += exp2_fast(v[r][i][0] - top[r]) * v[r][i][1];
-        for (int s = lane + 128; s < n; s += 64) {
-            const float m = ml[r][2 * s * stride];
-            if (m != -__builtin_huge_valf()) sum[r] += exp2_fast(m - top[r]) * ml[r][2 * s * stride + 1];
-        }
+        for (int i = 0; i < 2; ++i) sum[r] += exp2_fast(v[r][i][0] - ref) * v[r][i][1];
+        for (int s = lane + 128; s < n; s += 64)
+            sum[r] += exp2_fast(ml[r][2 * s * stride] - ref) * ml[r][2 * s * stride + 1];
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
@@ -456,21 +460,25 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(AttnArgs a) {
         float up = top;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) up = fmaxf(up, v[i][0]);
-        if (up == -__builtin_huge_valf()) continue;
-        const float old = exp2_fast(top - up);
+        const float ref = reference_of(up), old = exp2_fast(top - ref);
         top = up;
         sum *= old;
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] *= old;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const float f = s0 + i < n ? exp2_fast(v[i][0] - top) : 0.f;
+            const float f = s0 + i < n ? exp2_fast(v[i][0] - ref) : 0.f;
             sum = fmaf(f, v[i][1], sum);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[i][e], o[e]);
         }
     }
     join_write<TR>(a, b, h, r, d, o, top, sum);
+}
+
+// A slot's weight; none where it is hidden, whatever the row's sum is.
+__device__ inline float weight_of(float s, float lse2) {
+    return s == -__builtin_huge_valf() ? 0.f : exp2_fast(s - lse2);
 }
 
 template <class TR, bool PAGED>
@@ -495,9 +503,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
         if (grp < groups) {
             f32x4 o{0.f, 0.f, 0.f, 0.f};
             for (int s = grp; s < n; s += groups) {
-                const float m = ml[2 * (int64_t)s * a.R];
-                if (m == -__builtin_huge_valf()) continue;
-                const float f = exp2_fast(m - top);
+                const float f = exp2_fast(ml[2 * (int64_t)s * a.R] - reference_of(top));
                 const f32x4 x = *reinterpret_cast<const f32x4*>(
                     a.part_o + (p0 + (int64_t)s * a.R) * a.D + d);
 #pragma unroll
@@ -561,14 +567,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
                 if (r < rn) {
                     const float z = lse2[r];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) add[e] += exp2_fast(s[r][e] - z);
+                    for (int e = 0; e < 4; ++e) add[e] += weight_of(s[r][e], z);
                 }
             for (int r = kAhead; r < rn; ++r) {
                 const f32x4 t =
                     *reinterpret_cast<const f32x4*>(sr + (int64_t)(r0 + r) * a.score_stride);
                 const float z = lse2[r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) add[e] += exp2_fast(t[e] - z);
+                for (int e = 0; e < 4; ++e) add[e] += weight_of(t[e], z);
             }
         }
     }

@@ -389,7 +389,8 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
             top *= c;
             top = fmaxf(top, __shfl_xor(top, 32));
             const float up = fmaxf(m, top);
-            // nothing seen yet: weights and sum stay zero
+            // nothing seen yet: weights and sum stay zero, or become NaN where a
+            // score is
             const bool none = up == -__builtin_huge_valf();
             const float f = none || m == up ? 1.f : exp2_fast(m - up);
             m = up;
@@ -402,7 +403,7 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
             float prev = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = none ? 0.f : exp2_fast(fmaf(s[i], c, -up));
+                const float e = exp2_fast(none ? s[i] : fmaf(s[i], c, -up));
                 total += e;
                 if constexpr (ES == 2) {
                     if (i & 1) p.v[i >> 3][(i >> 1) & 3] = mfma::pack2<TR>(prev, e);
