@@ -449,9 +449,11 @@ ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int it
  * steps apart from the plain matrix products.  Forward only, like the rest
  * of the library; one element type per call; statistics, softmax sums and
  * accumulated weights in fp32; 16-bit operands of a matrix product are
- * accumulated in fp32, and softmax weights are rounded to the element type
- * where they multiply the values (a matrix instruction takes both operands
- * in one type).
+ * accumulated in fp32.  Where 16-bit softmax weights multiply the values (a
+ * matrix instruction takes both operands in one type) they go in two parts,
+ * the rounded weight and the rounded rest; with more than 64 query rows per
+ * key head, where the matrix product is what takes the time, they are rounded
+ * to the element type.
  *
  * Common rules.  Sizes and strides are int64, strides in elements, at least
  * 0, the last dimension contiguous.  Device pointers are 16-byte aligned and
