@@ -65,3 +65,37 @@ def test_few_rows_keep_the_weights(cc, n, D, dt):  # noqa: F811
             o, bound = attend(q64[b, r], kk[b, :, h], vv[b, :, h], D ** -0.5, dt)
             R.check(to_host(out)[b, r], o, bound, "paged")
             R.check(to_host(cross)[b, 0, r], o, bound, "cross")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("masked", [False, True])
+def test_many_small_weights_add_up(cc, masked, dt):  # noqa: F811
+    """One key that takes nearly all the weight, first, and 60000 keys of e^-18 of it each: the
+    values are theirs alone.  f16 weights are held against a reference of 2^-5 of the largest, so
+    that they end at 2^-30 of it (half a step of 2^-24 there), not at 2^-25."""
+    import torch
+
+    B, Lq, Lk, Hq, H, D = 16, 128, 60001, 16, 1, 64
+    say(f"small weights masked={masked} {dt}")
+    kind = torch_dtype(dt)
+    q = torch.zeros((B, Lq, Hq, D), dtype=kind, device="cuda")
+    q[..., 0] = 4.0
+    k = torch.zeros((1, Lk, H, D), dtype=kind, device="cuda")
+    k[:, 0, :, 0] = 4.5
+    v = torch.ones((1, Lk, H, D), dtype=kind, device="cuda")
+    v[:, 0] = 0.0
+    mask = None
+    n = Lk - 1
+    if masked:
+        mask = torch.ones((B, Lk), dtype=torch.bool, device="cuda")
+        mask[:, 1::3] = False
+        n = int(mask[0, 1:].sum())
+    ex = lambda t: t.expand(B, Lk, H, D)  # noqa: E731
+    out, lse = cc.cross_attention(q, ex(k), ex(v), mask=mask, scale=1.0)
+    torch.cuda.synchronize()
+    p = np.exp(-18.0)
+    want = n * p / (1 + n * p)
+    dp = 2 * (D + 4) * R.E * 18 + (n + 32) * R.E
+    bound = (2 * R.U[dt] + dp + n * R.E) * want + (n * 2.0 ** -30 if dt == "f16" else 0.0)
+    R.check(to_host(out), np.full(out.shape, want), bound, "out")
+    R.check(to_host(lse), np.full(lse.shape, 18 + np.log1p(n * p)), dp + 8 * R.E * 18, "lse")

@@ -20,14 +20,18 @@
 //    at D = 128 they cost about the same (16 matrix instructions of 32 cycles;
 //    16 exponentials of 16 and some 45 others of 4 cycles).
 //  - Weights are taken against a reference that is only moved when a half's
-//    weights sum to more than 2^10 in some lane; the sum is needed anyway,
-//    and a sum of positive numbers bounds each of them, so the maximum of the
-//    scores is not computed otherwise.  The reference starts at minus
-//    infinity, which makes the first sum infinite or NaN: not <= 2^10.
+//    weights sum to more than 2^10 times the reference's own in some lane; the
+//    sum is needed anyway, and a sum of positive numbers bounds each of them,
+//    so the maximum of the scores is not computed otherwise.  The reference
+//    starts at minus infinity, which makes the first sum infinite or NaN: not
+//    below any bound.
 //  - 16-bit weights are rounded to the element type for the product with V (a
-//    matrix instruction takes both operands in one type): relative error
-//    2^-9 or 2^-12 each, the size of the output's own rounding.  Their sum is
-//    taken before that, in fp32.
+//    matrix instruction takes both operands in one type): relative error up
+//    to 2^-8 (bf16) or 2^-11 (f16) each, the size of the output's own rounding.
+//    Their sum is taken before that, in fp32.  f16 ends at 2^-24: its weights
+//    are 2^5 times larger (the reference lies that much below the maximum), up
+//    to 2^15, so that what is dropped of a small one is 2^-30 of the largest:
+//    many keys of small weight beside one of a large one still add up.
 // LDS rows are spread over the banks by an exclusive-or of the 16-byte piece
 // with row bits.  K and V have two buffers each; tiles travel through
 // registers, from the moment that the tile before is written to LDS until a
@@ -58,6 +62,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr float kMostSum = 1024.f;
+// log2 of the weight that a maximum gets when the reference moves to it
+template <class TR>
+constexpr float kTopWeight = 0.f;
+template <>
+constexpr float kTopWeight<TF16> = 5.f;
 constexpr int kAhead = 4;  // LDS operands read ahead of their instruction
 
 template <class TR>
@@ -382,13 +391,13 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
     // After a half's weights: keep them, or move the reference and repeat.
     const auto settle = [&](const f32x16& s, Weights<TR>& p, float (&sum)[2]) {
         float total = sum[0] + sum[1];
-        if (__any(!(total <= kMostSum))) {
+        if (__any(!(total <= kMostSum * (1 << (int)kTopWeight<TR>)))) {
             float top = -__builtin_huge_valf();
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
             top *= c;
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float up = fmaxf(m, top);
+            const float up = fmaxf(m, top - kTopWeight<TR>);
             // nothing seen yet: weights and sum stay zero, or become NaN where a
             // score is
             const bool none = up == -__builtin_huge_valf();
