@@ -88,8 +88,9 @@ stream_kernel(AttnArgs a) {
     // of ragged sequences, which are empty, must not all fall to the same
     // ones (splits fastest, 16 of them: 212 us instead of 157 for 48 ragged
     // sequences up to 8192).
-    int item = blockIdx.x;
     const int tiles = a.B * a.Hkv * a.row_tiles;
+    if (block_number() >= (uint32_t)(tiles * a.splits)) return;
+    int item = (int)block_number();
     const int split = item / tiles;
     item -= split * tiles;
     const int tile = item % a.row_tiles;
@@ -442,7 +443,7 @@ template <class TR, bool PAGED>
 __global__ __launch_bounds__(kThreads) void join_few_kernel(AttnArgs a) {
     const int pieces = a.D / 4, rows = kThreads / pieces;
     const int grp = threadIdx.x / pieces, d = (threadIdx.x - grp * pieces) * 4;
-    const int64_t i = (int64_t)blockIdx.x * rows + grp;
+    const int64_t i = (int64_t)block_number() * rows + grp;
     if (grp >= rows || i >= (int64_t)a.B * a.Hkv * a.R) return;
     const int bh = (int)(i / a.R), r = (int)(i - (int64_t)bh * a.R);
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
@@ -494,8 +495,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
                                                         int weight_blocks) {
     __shared__ float part[kThreads * 4];
     const int tid = threadIdx.x, wave = tid >> 6;
-    if ((int)blockIdx.x < out_blocks) {
-        const int bh = blockIdx.x / a.R, r = blockIdx.x - bh * a.R;
+    if (block_number() >= (uint32_t)out_blocks + (uint32_t)(a.B * a.Hkv * weight_blocks)) return;
+    const int number = (int)block_number();
+    if (number < out_blocks) {
+        const int bh = number / a.R, r = number - bh * a.R;
         const int b = bh / a.Hkv, h = bh - b * a.Hkv;
         int first, span;
         visible<PAGED>(a, b, first, span);
@@ -529,7 +532,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
         return;
     }
     // weights of paged calls (Lq = 1, R = G)
-    const int item = blockIdx.x - out_blocks;
+    const int item = number - out_blocks;
     const int bh = item / weight_blocks, blk = item - bh * weight_blocks;
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
     int first, span;
@@ -593,7 +596,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int out_bloc
 
 template <class TR, int DP, bool PAGED, int NW>
 hipError_t stream_w(const AttnArgs& a, size_t lds, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * a.row_tiles * a.splits));
+    const dim3 grid = grid_of((int64_t)a.B * a.Hkv * a.row_tiles * a.splits);
     const void* fn = a.D == DP
                          ? reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, true, NW>)
                          : reinterpret_cast<const void*>(&stream_kernel<TR, DP, PAGED, false, NW>);
@@ -634,7 +637,7 @@ hipError_t join_t(const AttnArgs& a, hipStream_t s) {
     const int out_blocks = a.B * a.Hkv * a.R;
     if (a.splits <= kFewSplits && out_blocks >= kManyRows && !a.weight_sum) {
         const int rows = kThreads / (a.D / 4);
-        join_few_kernel<TR, PAGED><<<dim3((unsigned)((out_blocks + rows - 1) / rows)),
+        join_few_kernel<TR, PAGED><<<grid_of(((int64_t)out_blocks + rows - 1) / rows),
                                      dim3(kThreads), 0, s>>>(a);
         return hipGetLastError();
     }
@@ -643,7 +646,7 @@ hipError_t join_t(const AttnArgs& a, hipStream_t s) {
         a.weight_sum ? (int)((longest + kWeightSlots - 1) / kWeightSlots) : 0;
     const int64_t grid = out_blocks + (int64_t)a.B * a.Hkv * weight_blocks;
     join_kernel<TR, PAGED>
-        <<<dim3((unsigned)grid), dim3(kThreads), 0, s>>>(a, out_blocks, weight_blocks);
+        <<<grid_of(grid), dim3(kThreads), 0, s>>>(a, out_blocks, weight_blocks);
     return hipGetLastError();
 }
 

@@ -145,8 +145,10 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
 
     // (sequence, head) pairs stay on one XCD: their keys are read from its L2
     // by all of their row tiles.
-    const uint32_t per = gridDim.x >> 3;
-    int item = (int)((blockIdx.x & 7) * per + (blockIdx.x >> 3));
+    const uint32_t per = ((uint32_t)(a.B * a.Hkv * a.row_tiles * a.splits) + 7) >> 3;
+    const uint32_t number = block_number();
+    if (number >= 8 * per) return;
+    int item = (int)((number & 7) * per + (number >> 3));
     const int split = item % a.splits;
     item /= a.splits;
     const int tile = item % a.row_tiles;
@@ -603,7 +605,7 @@ hipError_t tile_d(const AttnArgs& a, hipStream_t s) {
     }
     AttnArgs args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)((items + 7) / 8 * 8)), dim3(kThreads), params, lds, s);
+    return hipLaunchKernel(fn, grid_of((items + 7) / 8 * 8), dim3(kThreads), params, lds, s);
 }
 
 template <class TR>

@@ -37,6 +37,17 @@ __device__ inline int64_t slot_offset(const Pages& p, int b, int t) {
 
 __device__ inline int clamped(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
 
+// A launch holds fewer than 2^32 threads along x: past kGridRow workgroups (of up
+// to 1024) they go to further rows of the grid, and those past the last one
+// end at once.
+constexpr int kGridRowBits = 20;
+inline dim3 grid_of(int64_t blocks) {
+    constexpr int64_t row = (int64_t)1 << kGridRowBits;
+    return blocks <= row ? dim3((unsigned)blocks)
+                         : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+__device__ inline uint32_t block_number() { return blockIdx.y << kGridRowBits | blockIdx.x; }
+
 struct AppendArgs {
     const void *k_new, *v_new;
     void *k, *v;

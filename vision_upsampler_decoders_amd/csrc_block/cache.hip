@@ -27,8 +27,10 @@ template <class S, bool STREAM>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     constexpr int VEC = 16 / sizeof(S);
     constexpr int UNROLL = 4;
-    const int b = (int)fdiv(blockIdx.x, a.fd_groups);
-    const int first = (int)(blockIdx.x - (uint32_t)b * a.groups) * a.rows_per_group;
+    const uint32_t item = block_number();
+    if (item >= (uint32_t)(a.B * a.groups)) return;
+    const int b = (int)fdiv(item, a.fd_groups);
+    const int first = (int)(item - (uint32_t)b * a.groups) * a.rows_per_group;
     const int len = a.lengths[b] < 0 ? 0 : a.lengths[b];
     int cnt = clamped(a.counts ? a.counts[b] : a.n, a.n);
     cnt = cnt < len ? cnt : len;
@@ -281,7 +283,8 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     int* near_slot = reinterpret_cast<int*>(near + kNear);
     uint64_t* ties = reinterpret_cast<uint64_t*>(work);  // later: a.words
     int* spare = reinterpret_cast<int*>(work);           // last: a.list kept slots from m on
-    const int bh = blockIdx.x, b = bh / a.Hkv, h = bh - b * a.Hkv;
+    if (block_number() >= (uint32_t)(a.B * a.Hkv)) return;
+    const int bh = (int)block_number(), b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t* table = a.pages.table + b * a.pages.table_stride;
@@ -600,7 +603,8 @@ template <class S>
 __global__ __launch_bounds__(kFillThreads) void fill_kernel(EvictArgs a) {
     __shared__ MovedRow rows[kFillThreads / 64][64 * kFill];
     const int tiles = (a.keep + kFillSlots - 1) / kFillSlots;
-    const int bh = blockIdx.x / tiles, tile = blockIdx.x - (uint32_t)bh * tiles;
+    if (block_number() >= (uint32_t)(a.B * a.Hkv * tiles)) return;
+    const int item = (int)block_number(), bh = item / tiles, tile = item - bh * tiles;
     const int b = bh / a.Hkv, h = bh - b * a.Hkv;
     if (a.lengths_out && h == 0 && tile == 0 && threadIdx.x == 0) {
         // the one place that reads lengths here: lengths_out may be lengths
@@ -622,7 +626,7 @@ constexpr int64_t kStreamBytes = 32 << 20;  // the XCDs' L2 caches together
 
 template <class S>
 hipError_t append_t(const AppendArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.B * a.groups));
+    const dim3 grid = grid_of((int64_t)a.B * a.groups);
     if ((int64_t)a.B * a.n * a.Hkv * a.D * 2 * (int64_t)sizeof(S) > kStreamBytes)
         append_kernel<S, true><<<grid, dim3(256), 0, s>>>(a);
     else
@@ -646,11 +650,11 @@ hipError_t evict_t(const EvictArgs& a, hipStream_t s) {
     }
     EvictArgs args = a;
     void* params[] = {&args};
-    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(a.B * a.Hkv)), dim3(kSelThreads),
+    const hipError_t e = hipLaunchKernel(fn, grid_of((int64_t)a.B * a.Hkv), dim3(kSelThreads),
                                          params, lds, s);
     if (e != hipSuccess || a.fused) return e;
     const int64_t tiles = ((int64_t)a.keep + kFillSlots - 1) / kFillSlots;
-    fill_kernel<S><<<dim3((unsigned)(a.B * a.Hkv * tiles)), dim3(kFillThreads), 0, s>>>(a);
+    fill_kernel<S><<<grid_of(a.B * a.Hkv * tiles), dim3(kFillThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 

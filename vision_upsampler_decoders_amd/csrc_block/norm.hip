@@ -163,8 +163,8 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void norm_kernel(NormArgs a) {
     constexpr int ROWS = NT > 256 ? 1 : 256 / NT;
     __shared__ float red_all[NT > 64 ? 16 : 1];
     static_assert(ROWS == 1 || NT == 64, "rows of a workgroup share no reduction buffer");
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT;
-    if (row >= a.rows) return;  // NT = 64: whole waves; else the grid is exact
+    const int64_t row = (int64_t)block_number() * ROWS + threadIdx.x / NT;
+    if (row >= a.rows) return;  // NT = 64: whole waves; else whole workgroups
     const int p0 = threadIdx.x % NT;
     const int n_pieces = a.C / VEC;
     const S* xr = static_cast<const S*>(a.x) + row * a.xs;
@@ -231,7 +231,7 @@ constexpr int64_t kStreamBytes = 32 << 20;
 template <class TR, int VEC, int NT, int PIECES>
 hipError_t run(const NormArgs& a, hipStream_t s) {
     constexpr int ROWS = NT > 256 ? 1 : 256 / NT;
-    const dim3 grid((unsigned)((a.rows + ROWS - 1) / ROWS)), block(NT > 256 ? NT : 256);
+    const dim3 grid = grid_of((a.rows + ROWS - 1) / ROWS), block(NT > 256 ? NT : 256);
     if constexpr (VEC > 1) {
         if (a.rows * a.C * (int64_t)sizeof(typename TR::storage) > kStreamBytes) {
             norm_kernel<TR, VEC, NT, PIECES, true><<<grid, block, 0, s>>>(a);
