@@ -161,7 +161,7 @@ int main() {
                 const int64_t C = rnd(1, 16384), rows = rnd(0, 3) ? rnd(1, 5000) : rnd(1, INT32_MAX);
                 const int64_t s5[5] = {C, rnd(0, 2 * C), C + rnd(0, 9), C + rnd(0, 99), C};
                 s = ctconv_norm_residual(buf, buf, buf, nullptr, buf, buf, buf, buf, buf, buf, rows, C,
-                                         s5, rnd(0, 3) ? rnd(1, 100) : rnd(1, INT32_MAX),
+                                         s5, rnd(0, 3) ? rnd(1, 100) : INT64_MAX - rnd(0, 9),
                                          (ctconv_norm)rnd(0, 2), (ctconv_norm)rnd(0, 2),
                                          (ctconv_gate)rnd(0, 3), 1e-5f, dt, nullptr);
                 break;

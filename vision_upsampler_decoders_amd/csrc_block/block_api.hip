@@ -615,7 +615,7 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
     if (rows == 0) return CTCONV_OK;
     if (!x || !h || !x_out || !strides || (gated && !gate) || (normed && !y))
         return CTCONV_ERR_NULL;
-    const int64_t gate_rows = gated ? ceil_div(rows, rows_per_gate) : 1;
+    const int64_t gate_rows = gated ? (rows - 1) / rows_per_gate + 1 : 1;
     Check c;
     bool vec = C % (16 / (int64_t)esize(dtype)) == 0;
     const struct {
