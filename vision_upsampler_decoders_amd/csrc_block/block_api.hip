@@ -165,20 +165,31 @@ int64_t tile_chunk(int64_t tiles, int64_t keys) {
     return round_up(ceil_div(keys, best), 128);
 }
 
-// Keys per workgroup of stream_kernel.
-//  - One workgroup of as many waves as it can have per row tile and no join,
-//    where few keys or many row tiles allow it: 500 keys on 8 tiles 9.8 us
-//    against 12.1 split, 1000 keys on 256 tiles 28 against 32; but 2000 keys on
-//    64 tiles 25 against 20 (bf16, D = 128).
+// Keys per workgroup of stream_kernel, and its waves (figures: one query row,
+// split against not, or 4 waves against as many as it can have).
+//  - One workgroup per row tile and no join, where few keys or many row tiles
+//    allow it: 500 keys on 8 tiles 7.6 us against 9.3, 1000 on 256 tiles 15.5
+//    against 18.7, 2000 on 256 tiles 25.7 against 28.6 (bf16, D = 64); but 500
+//    keys on 8 tiles 19.4 against 17.4 at D = 256, whose rows take a wave four
+//    times as long.
 //  - Else chunks that give every compute unit one round of the workgroups its
 //    registers hold (4, 3 or 1 of 4 waves for D up to 64, 128, 256): 30000
 //    keys on 8 tiles take 33 us in 469 workgroups, 40 in 938.  At least 256
 //    keys (a workgroup's start costs about as much as 128), at most 1024, so
 //    that ragged sequences still spread.
-void stream_split(int64_t tiles, int64_t keys, int64_t D, int64_t* chunk, bool* wide) {
-    *wide = (keys <= 512 && tiles <= 256) || (keys <= 1024 && tiles >= 128) ||
-            (keys <= 2048 && tiles >= 256);
-    if (*wide) {
+//  - More waves than 4 (16 up to D = 64, 8 up to 128) pay in fp32, whose blocks
+//    are half as long, where each gets a block or more and the tiles do not
+//    fill the chip by themselves: 500 keys on 256 tiles 15.0 us against 17.3,
+//    2000 53 against 82, at D = 128 1000 keys on 1024 tiles 192 against 227.
+//    Their merge costs more than they save with few keys (16 on 1024 tiles 16.8
+//    against 6.1), on many tiles (250 on 8192, D = 64, 244 against 189), and in
+//    16 bits throughout (500 on 8 tiles 8.3 against 7.6, on 1024 34.7 against
+//    24.2).
+void stream_split(int64_t tiles, int64_t keys, int64_t D, bool f32, int64_t* chunk, bool* wide) {
+    const bool whole = keys <= (D <= 128 ? 512 : 256) || (keys <= 1024 && tiles >= 128) ||
+                       (keys <= 2048 && tiles >= 256);
+    *wide = whole && f32 && keys > 128 && (D <= 64 ? tiles <= 256 : D <= 128 && tiles <= 1024);
+    if (whole) {
         *chunk = round_up(keys, 128);
         return;
     }
@@ -188,7 +199,7 @@ void stream_split(int64_t tiles, int64_t keys, int64_t D, int64_t* chunk, bool* 
 }
 
 ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span,
-                             bool weights, bool tile, Plan* p) {
+                             bool weights, bool tile, ctconv_dtype dt, Plan* p) {
     memset(p, 0, sizeof(*p));
     p->tile = tile;
     p->row_tiles = ceil_div(R, tile ? kTileRows : 16);
@@ -199,7 +210,7 @@ ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64
     if (tile) {
         chunk = tile_chunk((int64_t)tiles, keys);
     } else {
-        stream_split((int64_t)tiles, keys, D, &chunk, &p->wide);
+        stream_split((int64_t)tiles, keys, D, dt == CTCONV_F32, &chunk, &p->wide);
     }
     p->chunk = chunk;
     p->splits = span > 0 ? ceil_div(span, chunk) : 1;
@@ -252,7 +263,7 @@ ctconv_status paged_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
     if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
     if (max_length < 0 || max_length > kMaxInt - (1 << 20) || window < 0) return CTCONV_ERR_SHAPE;
     const int64_t span = window > 0 && window < max_length ? window : max_length;
-    return plan_attention(B, Hkv, Hq / Hkv, D, span, weights, false, p);
+    return plan_attention(B, Hkv, Hq / Hkv, D, span, weights, false, dt, p);
 }
 
 ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D,
@@ -265,7 +276,7 @@ ctconv_status cross_plan(int64_t B, int64_t Lq, int64_t Lk, int64_t Hq, int64_t 
     const int64_t R = Lq * (Hq / Hkv);
     // (fp32 rows past 512 bytes are too long for its LDS tiles)
     const bool tile = R > kTileFrom && D * (int64_t)esize(dt) <= 512;
-    return plan_attention(B, Hkv, R, D, Lk, false, tile, p);
+    return plan_attention(B, Hkv, R, D, Lk, false, tile, dt, p);
 }
 
 }  // namespace
