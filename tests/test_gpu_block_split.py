@@ -15,8 +15,9 @@ pytestmark = pytest.mark.gpu
 CASES = [
     (64, 16, 5, 64), (64, 16, 129, 32), (128, 64, 1, 16), (32, 8, 300, 64), (33, 8, 300, 64),
     (1, 8, 512, 64), (1, 8, 513, 64), (16, 16, 1024, 24), (16, 16, 1025, 24), (8, 15, 1000, 40),
-    (2, 4, 256, 256), (2, 4, 257, 200), (1, 8, 500, 256), (16, 16, 700, 136), (64, 16, 140, 128),
-    (41, 25, 140, 104), (16, 8, 128, 128), (16, 8, 129, 128),
+    (2, 4, 256, 256), (2, 4, 257, 200), (1, 8, 500, 256), (1, 8, 384, 144), (1, 8, 385, 144), (16, 16, 700, 136), (64, 16, 140, 128),
+    (41, 25, 140, 104), (16, 8, 128, 128), (16, 8, 129, 128), (16, 16, 65, 48),
+    (16, 17, 512, 64), (16, 17, 513, 64), (16, 17, 1025, 64),
 ]
 
 

@@ -618,8 +618,8 @@ hipError_t stream_d(const AttnArgs& a, hipStream_t s) {
         const size_t merge = (size_t)(nw * rows * (DP + 4) + 2 * nw * 16) * 4;
         return stage > merge ? stage : merge;
     };
-    // as many waves as the registers allow (512 per lane and SIMD), in fp32
-    constexpr int WIDE = sizeof(typename TR::storage) == 2 ? 4 : DP <= 64 ? 16 : DP <= 128 ? 8 : 4;
+    // as many waves as the registers allow (512 per lane and SIMD)
+    constexpr int WIDE = DP <= 64 ? 16 : DP <= 128 ? 8 : 4;
     if constexpr (WIDE > 4)
         if (a.wide) return stream_w<TR, DP, PAGED, WIDE>(a, lds(WIDE), s);
     return stream_w<TR, DP, PAGED, 4>(a, lds(4), s);

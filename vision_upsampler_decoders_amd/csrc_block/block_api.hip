@@ -166,29 +166,33 @@ int64_t tile_chunk(int64_t tiles, int64_t keys) {
 }
 
 // Keys per workgroup of stream_kernel, and its waves (figures: one query row,
-// split against not, or 4 waves against as many as it can have).
+// keys and values in memory, not in a cache).
 //  - One workgroup per row tile and no join, where few keys or many row tiles
-//    allow it: 500 keys on 8 tiles 7.6 us against 9.3, 1000 on 256 tiles 15.5
-//    against 18.7, 2000 on 256 tiles 25.7 against 28.6 (bf16, D = 64); but 500
-//    keys on 8 tiles 19.4 against 17.4 at D = 256, whose rows take a wave four
-//    times as long.
+//    allow it: 500 keys on 8 tiles 9.8 us against 12.1 split, 1000 keys on 256
+//    tiles 28 against 32; but 2000 keys on 64 tiles 25 against 20 (bf16, D =
+//    128).  Rows of more than 128 values take a wave longer: up to 500 of 256
+//    on 8 tiles 20.8 us against 19.4 split in bf16 (350: 17.2 against 19.3),
+//    56.3 against 35.7 in fp32 (350: 43.3 against 35.5).
 //  - Else chunks that give every compute unit one round of the workgroups its
 //    registers hold (4, 3 or 1 of 4 waves for D up to 64, 128, 256): 30000
 //    keys on 8 tiles take 33 us in 469 workgroups, 40 in 938.  At least 256
 //    keys (a workgroup's start costs about as much as 128), at most 1024, so
 //    that ragged sequences still spread.
-//  - More waves than 4 (16 up to D = 64, 8 up to 128) pay in fp32, whose blocks
-//    are half as long, where each gets a block or more and the tiles do not
-//    fill the chip by themselves: 500 keys on 256 tiles 15.0 us against 17.3,
-//    2000 53 against 82, at D = 128 1000 keys on 1024 tiles 192 against 227.
-//    Their merge costs more than they save with few keys (16 on 1024 tiles 16.8
-//    against 6.1), on many tiles (250 on 8192, D = 64, 244 against 189), and in
-//    16 bits throughout (500 on 8 tiles 8.3 against 7.6, on 1024 34.7 against
-//    24.2).
-void stream_split(int64_t tiles, int64_t keys, int64_t D, bool f32, int64_t* chunk, bool* wide) {
-    const bool whole = keys <= (D <= 128 ? 512 : 256) || (keys <= 1024 && tiles >= 128) ||
+//  - An undivided row tile takes as many waves as its registers allow (16 up to
+//    D = 64, 8 up to 128) where 4 would have more than a block of keys each and
+//    the tiles do not fill the chip by themselves, so that more loads are in
+//    flight: 500 keys of 64 on 64 tiles 9.4 us against 10.3 (fp32 12.7 against
+//    23.4), 2000 on 256 fp32 76 against 86.  More tiles bring loads enough, and
+//    the merge of many waves costs most of a short call (16 keys on 1024 tiles
+//    19.3 us against 6.7, 250 on 8192 198 against 136): there only where each
+//    wave has two blocks (1000 of 128 on 1024, fp32, 229 against 265).
+void stream_split(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, int64_t* chunk,
+                  bool* wide) {
+    const int64_t block = dt == CTCONV_F32 ? 16 : 32, waves = D <= 64 ? 16 : 8;
+    const int64_t few = D <= 128 ? 512 : dt == CTCONV_F32 ? 256 : 384;
+    const bool whole = keys <= few || (keys <= 1024 && tiles >= 128) ||
                        (keys <= 2048 && tiles >= 256);
-    *wide = whole && f32 && keys > 128 && (D <= 64 ? tiles <= 256 : D <= 128 && tiles <= 1024);
+    *wide = whole && D <= 128 && keys > (tiles <= 256 ? 4 : 2 * waves) * block;
     if (whole) {
         *chunk = round_up(keys, 128);
         return;
@@ -210,7 +214,7 @@ ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64
     if (tile) {
         chunk = tile_chunk((int64_t)tiles, keys);
     } else {
-        stream_split((int64_t)tiles, keys, D, dt == CTCONV_F32, &chunk, &p->wide);
+        stream_split((int64_t)tiles, keys, D, dt, &chunk, &p->wide);
     }
     p->chunk = chunk;
     p->splits = span > 0 ? ceil_div(span, chunk) : 1;

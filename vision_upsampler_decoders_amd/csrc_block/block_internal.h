@@ -100,7 +100,7 @@ struct AttnArgs {
     int B, Lq, Lk, Hq, Hkv, G, D, R;
     int window;
     int chunk, splits;           // keys per workgroup, workgroups per row tile
-    int wide;                    // stream kernel, fp32: a workgroup of as many waves as it can have
+    int wide;                    // stream kernel: a workgroup of as many waves as it can have
     int direct;                  // one workgroup per row tile, and no weights: no join
     int row_tiles;
     FastDiv fd_G;
