@@ -464,7 +464,8 @@ ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int it
  * with strides that do not keep its rows apart (from the smallest stride up,
  * a step must pass all that lies below it).  With no row to compute (B, Lq or
  * rows of 0) nothing is enqueued and pointers may be NULL.  Results do not
- * depend on the launch: no atomics, every sum in a fixed order.
+ * depend on the launch: every sum is taken in a fixed order, and atomics only
+ * count in integers.
  *
  * The paged cache.  k_cache and v_cache hold num_pages pages of page_size
  * slots for Hkv heads of D values: slot t of sequence b lies at

@@ -28,7 +28,7 @@
 //
 // Long calls are bound by memory, whole rows of 16-byte pieces in random pages:
 // 48 ragged sequences up to 8192 (32 query heads on 8 cache heads, D = 128,
-// bf16; 760 MB) take 147 us, 5.2 TB/s, and 7.5 for the join (a read-only sweep
+// bf16; 760 MB) take 147 us, 5.2 TB/s, and 7.3 for the join (a read-only sweep
 // of random 4 KB pieces reaches 6.0).  Single tokens to up to 1500 states of
 // 256 heads (D = 64, bf16; 50 MB) take 15 us and one frame's window of 250
 // slots 8: one round of workgroups each, whose loads, merge and stores follow
@@ -364,12 +364,14 @@ stream_kernel(AttnArgs a) {
 // Join.  A row's outputs are its splits' outputs weighted by 2^(m - maximum),
 // over the sum of their sums weighted the same.
 //  - Few splits of many rows: D / 4 lanes add a row's splits in ascending
-//    order, 256 / (D / 4) rows per workgroup.
+//    order, 256 / (D / 4) rows per workgroup.  A whole call with it and with a
+//    workgroup per row: 4096 rows of 3 splits 212 us against 219, 8192 of 5
+//    194 against 210; but 8 rows of 20000 keys 29 against 23.
 //  - Else: a workgroup per row; each of its lane groups takes every
 //    groups-th split in ascending order, then the groups are added in order.
 // The workgroups past those add the weights to weight_sum: 1024 slots each.
-// They need the sums of all splits, hence a second kernel: 12.5 us after 80 for
-// 3 ragged sequences up to 100003 (24 heads on 4, f16; 416 MB in all).
+// They need the sums of all splits, hence a second kernel: 9.8 us after 75 to 83
+// for 3 ragged sequences up to 100003 (24 heads on 4, f16; 416 MB in all).
 constexpr int kFewSplits = 16, kManyRows = 4096;
 constexpr int kAtOnce = 4;  // splits of a row whose loads are in flight together
 constexpr int kWeightSlots = 4 * kThreads;

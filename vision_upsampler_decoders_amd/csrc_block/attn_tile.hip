@@ -46,6 +46,10 @@
 // (the compiler then waits for all of them at every store, 333 us), operands
 // read right before their use (350), 3 workgroups per compute unit at D = 64
 // (spills: 243 against 174), wave priorities (no difference).
+// The 16-bit kernels for D up to 128 and 256 need more registers than there are:
+// 7 (bf16) and 8 (f16), 6 and 2, live in scratch memory.  At D = 128 bf16 touches
+// them outside the loop only; f16 reads one back in it, behind loads that it
+// then waits for: 331 us against 304 for the call above.
 
 #include "block_internal.h"
 #include "mfma_common.h"

@@ -14,6 +14,9 @@ namespace {
 constexpr int64_t kMaxInt = INT32_MAX;
 constexpr int64_t kMaxEvictSlots = 262144;  // select_kernel keeps a few bits per slot in LDS
 constexpr int64_t kEvictLds = 128 << 10;     // of the 160 KB, with what it declares itself
+// Up to this many kept slots eviction is one kernel: 8 heads cut to 256 slots
+// take 8.9 us against 11.4 in two, to 1000 12.1 against 15.1, to 2000 15.7
+// against 16.5, but to 3000 19.9 against 17.0, to 5000 25.8 against 17.8.
 constexpr int64_t kFusedKeep = 2048;
 constexpr int64_t kMaxRowValues = 16384;    // norm_kernel keeps a row in registers
 
@@ -144,7 +147,13 @@ struct Plan {
 };
 
 constexpr int64_t kTileRows = 128;  // query rows per workgroup of tile_kernel
-constexpr int64_t kTileFrom = 64;   // more rows per cache head than this: tile_kernel
+// More rows per cache head than this: tile_kernel.  No one limit is best for all.
+// 64 or 65 rows in stream_kernel and in tile_kernel (from memory; heads x keys,
+// us): bf16, D = 64: 8 x 2000 12.0 and 18.1, 64 x 500 11.0 and 13.3, 64 x 4000
+// 51.9 and 26.1; fp32: 15.3 and 49.2, 15.2 and 45.1, 82.1 and 86.2.  96 rows:
+// bf16 13.0 and 17.9, 12.3 and 14.2, 63.0 and 27.7; fp32 17.7 and 49.5, 20.6
+// and 45.5, 113 and 87.5.
+constexpr int64_t kTileFrom = 64;
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 

@@ -127,8 +127,9 @@ __device__ inline void apply(float (&v)[VEC], float r, const void* w, const void
 }
 
 // The 16-bit types take the hardware's exponential and reciprocal (relative
-// error below 2^-16, beside the types' own 2^-9 and 2^-12): with the exact
-// ones the gate was half of the kernel's instructions.
+// error below 2^-16, beside the types' own 2^-8 and 2^-11; the outputs' error
+// against 64 bits is the same to two digits): with the exact ones the gate
+// was half of the kernel's instructions, 138 us against 115 for the rows above.
 template <class TR, int VEC>
 __device__ inline void gate_values(const Piece<TR, VEC>& p, int fn, float (&g)[VEC]) {
     constexpr bool SHORT = sizeof(typename TR::storage) == 2;
