@@ -665,12 +665,205 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
                                    ctconv_gate gate_fn, float eps, ctconv_dtype dtype,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * Requests of many lengths.
+ *
+ * What a serving step needs around the paged cache when sequences take new
+ * rows in different numbers: pages for them (ctconv_cache_pages), their
+ * queries and keys turned by their positions on the way into the cache
+ * (ctconv_rotary_append; ctconv_rotary for tensors of their own), and their
+ * attention to all that the cache holds, in causal order
+ * (ctconv_chunk_attention).  The common rules of the block's functions above
+ * hold here too.
+ *
+ * New rows are packed (one sequence's rows behind the other's: row i of
+ * sequence b is row row_starts[b] + i of `rows` rows) or, for the attention,
+ * padded ([B, n, ...] with counts[b] rows in use).  What a buffer holds
+ * behind the last row of a sequence is neither used nor written.
+ * ---------------------------------------------------------------------- */
+
 /*
- * The five calls above with their arguments in two tables, for callers that
+ * Make page tables follow the lengths, and say where new rows go.
+ *
+ * Sequence b, of lengths[b] slots (with its new rows; clamped to [0,
+ * max_pages * page_size]), needs ceil(lengths[b] / page_size) pages and holds
+ * held[b] (clamped to [0, max_pages]; those of the first columns of its table
+ * row).  First, sequences that hold more than they need give the excess back:
+ * their pages, in order of sequence and column, go on top of the stack of free
+ * pages (entries outside [0, num_pages), which are no pages, do not).  Then
+ * sequences that need more take pages from the top of the stack, in order of
+ * sequence and column, and write them to their table rows; when the stack is
+ * empty, the columns left over get -1 (slots without a page), and
+ * held_out[b] * page_size < lengths[b] says so.
+ *   lengths, held, held_out   device int32 [B]; held_out (pages now held) may
+ *                 be held
+ *   page_table    device int32 [B, max_pages], table_stride per row; columns
+ *                 below held[b] and from the needed ones on stay as they are
+ *   free_pages    device int32 [num_pages]: the stack, its top at
+ *                 free_pages[free_count[0] - 1]
+ *   free_count, free_count_out   device int32 [1], may be one (clamped to
+ *                 [0, num_pages])
+ * With held_out and free_count_out apart from held and free_count a call can
+ * be repeated: it does the same again.
+ *
+ * Row maps, when counts is not NULL.  counts[b] (clamped to [0, lengths[b]])
+ * are the new rows of b, the last ones of its length, packed one sequence
+ * behind the other:
+ *   row_starts    device int32 [B + 1]: the sum of the counts before b
+ *   row_positions device int32 [rows]: now[b] - counts[b] + i; -1 behind the
+ *                 last row
+ *   row_slots     device int32 [rows]: where the row goes, page * page_size +
+ *                 place in the page; -1 where it has no page and behind the last row
+ *   now           device int32 [B], the rows seen in all, with the new ones;
+ *                 NULL: lengths
+ *   positions, weight_sum, slot_strides   slot arrays as in
+ *                 ctconv_cache_append, or NULL: the rows' slots get their
+ *                 position and weight 0
+ * rows that do not fit (row_starts[B] > rows) have no map.  row_positions and
+ * row_slots are required when rows > 0.
+ *
+ * B at most 8192, B * max_pages and num_pages * page_size below 2^31
+ * (CTCONV_ERR_SHAPE).  Index arrays need no alignment beyond their own 4 bytes
+ * (CTCONV_ERR_ALIGN).  No page may be held twice.
+ */
+ctconv_status ctconv_cache_pages(const int32_t* lengths, const int32_t* counts,
+                                 const int32_t* now, const int32_t* held,
+                                 const int32_t* free_count, int32_t* page_table,
+                                 int32_t* free_pages, int32_t* held_out, int32_t* free_count_out,
+                                 int32_t* row_starts, int32_t* row_positions, int32_t* row_slots,
+                                 int32_t* positions, float* weight_sum, int64_t B, int64_t rows,
+                                 int64_t Hkv, int64_t num_pages, int64_t page_size,
+                                 int64_t max_pages, int64_t table_stride,
+                                 const int64_t* slot_strides, void* stream);
+
+typedef enum {
+    CTCONV_ROTARY_HALF = 0, /* value j of the first R / 2 goes with value j + R / 2 */
+    CTCONV_ROTARY_PAIRS = 1 /* value 2 j goes with value 2 j + 1 */
+} ctconv_rotary_layout;
+
+/*
+ * Rotary positions: of every head the first R of D values, as R / 2 pairs
+ * (u, v), are turned by the angle a = positions[row] * frequencies[pair],
+ *     u' = scale * (u cos a - v sin a),   v' = scale * (v cos a + u sin a),
+ * and the values from R on are copied.
+ *   q, q_out      device [rows, Hq, D]; q_strides, q_out_strides = row, head
+ *   k, k_out      device [rows, Hk, D]; the same; NULL when Hk = 0 (Hq and Hk
+ *                 are not both 0)
+ *   positions     device int32 [rows]; rows of a negative position are not
+ *                 written
+ *   frequencies   device fp64 [R / 2], radians per position (negative ones
+ *                 turn back)
+ * Angles are reduced in fp64, so that far positions keep theirs; sines and
+ * products are fp32, each output rounded once.  R even, 2 .. D.  q_out may be
+ * q and k_out may be k (same pointer and strides); otherwise outputs must not
+ * overlap inputs.  scale finite (CTCONV_ERR_PARAM).
+ */
+ctconv_status ctconv_rotary(const void* q, const void* k, const int32_t* positions,
+                            const double* frequencies, void* q_out, void* k_out, int64_t rows,
+                            int64_t Hq, int64_t Hk, int64_t D, int64_t R,
+                            const int64_t* q_strides, const int64_t* k_strides,
+                            const int64_t* q_out_strides, const int64_t* k_out_strides,
+                            ctconv_rotary_layout layout, float scale, ctconv_dtype dtype,
+                            void* stream);
+
+/*
+ * The same on the way into the paged cache: q turned to q_out, k_new turned
+ * and v_new as it is to slot slots[row] (page * page_size + place, as
+ * ctconv_cache_pages writes row_slots) of k_cache and v_cache.  Rows of a
+ * negative position are not written anywhere, rows whose slot is outside
+ * [0, num_pages * page_size) not to the cache.
+ *   q, q_out      as above; Hq = 0: NULL (keys and values only)
+ *   k_new, v_new  device [rows, Hkv, D], new_strides = row, head (both)
+ *   kv_strides    page, slot, head
+ * No slot may be given to two rows; the cache must not overlap an input.
+ */
+ctconv_status ctconv_rotary_append(const void* q, const void* k_new, const void* v_new,
+                                   const int32_t* positions, const int32_t* slots,
+                                   const double* frequencies, void* q_out, void* k_cache,
+                                   void* v_cache, int64_t rows, int64_t Hq, int64_t Hkv,
+                                   int64_t D, int64_t R, int64_t num_pages, int64_t page_size,
+                                   const int64_t* q_strides, const int64_t* new_strides,
+                                   const int64_t* q_out_strides, const int64_t* kv_strides,
+                                   ctconv_rotary_layout layout, float scale, ctconv_dtype dtype,
+                                   void* stream);
+
+typedef enum {
+    CTCONV_ROTARY_NONE = 0,      /* f[i] = base^(-2 i / R) */
+    CTCONV_ROTARY_LINEAR = 1,    /* f / factor */
+    CTCONV_ROTARY_BASE = 2,      /* f of base * factor^(R / (R - 2)) */
+    CTCONV_ROTARY_RAMP_DIMS = 3, /* f and f / factor blended along the pairs */
+    CTCONV_ROTARY_RAMP_TURNS = 4 /* f and f / factor blended along the turns */
+} ctconv_rotary_scaling;
+
+/*
+ * Frequencies for ctconv_rotary, radians per position, for contexts `factor`
+ * times longer than the `original` one of a model (host only: frequencies
+ * [R / 2] is host memory).  The ramps keep what turns often in the original
+ * context and stretch what does not, keep * f + (1 - keep) * f / factor:
+ *   RAMP_DIMS   pair(t) = R log(original / (2 pi t)) / (2 log base) is where a
+ *               pair makes t turns; keep falls linearly from 1 at
+ *               max(floor(pair(high)), 0) to 0 at min(ceil(pair(low)), R - 1)
+ *               (queries and keys are then often scaled by 0.1 ln(factor) + 1)
+ *   RAMP_TURNS  keep rises linearly from 0 at `low` turns, original f / (2 pi),
+ *               to 1 at `high` turns
+ * CTCONV_ERR_SHAPE for an R that is odd or outside 2 .. 256; CTCONV_ERR_PARAM
+ * for an unknown scaling, base or factor not above 0 or not finite, and for
+ * the ramps an original not above 0, low not above 0, high not above low or,
+ * along the pairs, a base not above 1.
+ */
+ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_scaling scaling,
+                                        double factor, double original, double low, double high,
+                                        double* frequencies);
+
+/*
+ * Attention of each sequence's new rows, the last counts[b] of its lengths[b]
+ * slots, to the cache that holds them already: row i sees the slots
+ *     t in [max(0, e - window), e),   e = lengths[b] - counts[b] + i + 1
+ * (window 0: from 0); s, p, out and lse as in ctconv_paged_attention.
+ *   q, out        device, q_strides, out_strides = batch, row, head
+ *                 row_starts given: [rows, Hq, D] (the batch stride is not
+ *                 used); NULL: [B, n, Hq, D], rows = B * n
+ *   row_starts    device int32 [B + 1] or NULL: counts[b] = row_starts[b + 1] -
+ *                 row_starts[b] (clamped to [0, n]); rows outside [0, rows) do
+ *                 not exist
+ *   counts        device int32 [B] or NULL (n), clamped to [0, n]; not used with
+ *                 row_starts
+ *   n             a bound on counts that the caller knows
+ *   lse           device fp32 [rows, Hq] dense (row b * n + i when padded), or NULL
+ *   weight_sum    device fp32 [B, Hkv, slots] or NULL: weight_sum[b][h][t] +=
+ *                 the sum of p[t] over the new rows and the query heads of h
+ *                 (slots that no row sees are left as they are); slot_strides
+ *                 as in ctconv_cache_append
+ * A row that sees nothing gets out = 0 and lse = -infinity.  Infinities and
+ * NaN in a slot reach only the rows that see it, an infinite value as such.  16-bit weights meet the
+ * values in two parts with up to 64 query rows (n times Hq / Hkv) per key head,
+ * rounded to the element type with more.  Workspace, D, heads, scale and
+ * max_length as in ctconv_paged_attention.  out must not overlap an input.
+ */
+ctconv_status ctconv_chunk_attention_workspace_bytes(int64_t B, int64_t rows, int64_t n,
+                                                     int64_t Hq, int64_t Hkv, int64_t D,
+                                                     int64_t max_length, int64_t window,
+                                                     int weights, ctconv_dtype dtype,
+                                                     size_t* bytes);
+ctconv_status ctconv_chunk_attention(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* page_table, const int32_t* lengths,
+                                     const int32_t* row_starts, const int32_t* counts, void* out,
+                                     float* lse, float* weight_sum, int64_t B, int64_t rows,
+                                     int64_t n, int64_t Hq, int64_t Hkv, int64_t D,
+                                     int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                     int64_t max_length, int64_t window, const int64_t* q_strides,
+                                     const int64_t* kv_strides, const int64_t* out_strides,
+                                     int64_t table_stride, const int64_t* slot_strides,
+                                     float scale, ctconv_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * The calls above with their arguments in two tables, for callers that
  * prepare the sizes once and pay per argument afterwards (a foreign-function
  * binding; the Python plans use it): the function is called with
  *   buffers   its buffer pointers, in the order of its signature
- *   sizes     every other argument up to the dtype, in the order of its
+ *   sizes     every other argument up to the dtype (up to the strides of
+ *             ctconv_cache_pages, which has none), in the order of its
  *             signature: integers and enumerators as they are, the values of
  *             a stride array one after the other (all arrays are needed
  *             here), scale and eps as the bits of a double
@@ -683,7 +876,11 @@ typedef enum {
     CTCONV_OP_PAGED_ATTENTION = 1, /*  8 buffers, 21 sizes */
     CTCONV_OP_CACHE_EVICT = 2,     /* 11 buffers, 19 sizes */
     CTCONV_OP_CROSS_ATTENTION = 3, /*  7 buffers, 21 sizes */
-    CTCONV_OP_NORM_RESIDUAL = 4    /* 10 buffers, 13 sizes */
+    CTCONV_OP_NORM_RESIDUAL = 4,   /* 10 buffers, 13 sizes */
+    CTCONV_OP_CACHE_PAGES = 16,    /* 14 buffers,  9 sizes */
+    CTCONV_OP_ROTARY = 17,         /*  6 buffers, 16 sizes */
+    CTCONV_OP_ROTARY_APPEND = 18,  /*  9 buffers, 19 sizes */
+    CTCONV_OP_CHUNK_ATTENTION = 19 /* 10 buffers, 25 sizes */
 } ctconv_block_op;
 ctconv_status ctconv_block_run(ctconv_block_op op, const int64_t* sizes, void* const* buffers,
                                void* workspace, size_t workspace_bytes, void* stream);

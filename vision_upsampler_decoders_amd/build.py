@@ -33,7 +33,8 @@ FLAGS = [
 
 SOURCES = ["ctconv_api.hip", "prepack.hip", "gather.hip", "pointwise.hip", "stream.hip",
            "depthwise.hip", "polyphase.hip", "polyrw.hip", "noalloc.hip", "clock.hip"]
-BLOCK_SOURCES = ["block_api.hip", "norm.hip", "cache.hip", "attn_stream.hip", "attn_tile.hip"]
+BLOCK_SOURCES = ["block_api.hip", "request_api.hip", "block_run.hip", "norm.hip", "cache.hip",
+                 "pages.hip", "rotary.hip", "attn_stream.hip", "attn_tile.hip", "attn_chunk.hip"]
 HEADERS = [os.path.join(CSRC, "ctconv_internal.h"), os.path.join(CSRC, "mfma_common.h"),
            os.path.join(INCLUDE, "ctconv.h")]
 
@@ -63,7 +64,7 @@ def _stale(src: str) -> bool:
     t = os.path.getmtime(obj)
     deps = [_path(src), *HEADERS]
     if src in BLOCK_SOURCES:
-        deps.append(os.path.join(BLOCK, "block_internal.h"))
+        deps += [os.path.join(BLOCK, f) for f in os.listdir(BLOCK) if f.endswith(".h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -51,8 +51,8 @@
 // them outside the loop only; f16 reads one back in it, behind loads that it
 // then waits for: 331 us against 304 for the call above.
 
+#include "attn_mma.h"
 #include "block_internal.h"
-#include "mfma_common.h"
 
 namespace ctconv {
 namespace block {
@@ -62,8 +62,6 @@ namespace {
 using mfma::u32x2;
 using mfma::u32x4;
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr int kThreads = 256;
 constexpr float kMostSum = 1024.f;
 // log2 of the weight that a maximum gets when the reference moves to it
@@ -72,34 +70,6 @@ constexpr float kTopWeight = 0.f;
 template <>
 constexpr float kTopWeight<TF16> = 5.f;
 constexpr int kAhead = 4;  // LDS operands read ahead of their instruction
-
-template <class TR>
-struct Mma32;
-template <>
-struct Mma32<TBF16> {
-    __device__ static inline void step(f32x16& acc, const u32x4 a, const u32x4 b) {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                      __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
-    }
-};
-template <>
-struct Mma32<TF16> {
-    __device__ static inline void step(f32x16& acc, const u32x4 a, const u32x4 b) {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                     __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
-    }
-};
-template <>
-struct Mma32<TF32> {
-    // a half holds values 4 half .. 4 half + 3 of 8; instruction e consumes
-    // value e of both halves
-    __device__ static inline void step(f32x16& acc, const u32x4 a, const u32x4 b) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]),
-                                                       __uint_as_float(b[e]), acc, 0, 0, 0);
-    }
-};
 
 template <class TR, int DP>
 struct Shape {

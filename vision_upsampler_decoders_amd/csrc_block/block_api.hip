@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "block_check.h"
 #include "block_internal.h"
 
 using namespace ctconv;
@@ -11,7 +12,6 @@ using namespace ctconv::block;
 
 namespace {
 
-constexpr int64_t kMaxInt = INT32_MAX;
 constexpr int64_t kMaxEvictSlots = 262144;  // select_kernel keeps a few bits per slot in LDS
 constexpr int64_t kEvictLds = 128 << 10;     // of the 160 KB, with what it declares itself
 // Up to this many kept slots eviction is one kernel: 8 heads cut to 256 slots
@@ -19,120 +19,6 @@ constexpr int64_t kEvictLds = 128 << 10;     // of the 160 KB, with what it decl
 // against 16.5, but to 3000 19.9 against 17.0, to 5000 25.8 against 17.8.
 constexpr int64_t kFusedKeep = 2048;
 constexpr int64_t kMaxRowValues = 16384;    // norm_kernel keeps a row in registers
-
-size_t esize(ctconv_dtype dt) { return dt == CTCONV_F32 ? 4 : 2; }
-
-bool dtype_ok(int dt) { return dt == CTCONV_F32 || dt == CTCONV_BF16 || dt == CTCONV_F16; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-ctconv_status to_status(hipError_t e) { return e == hipSuccess ? CTCONV_OK : CTCONV_ERR_HIP; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Strides of a tensor whose last dimension holds D values: not negative, the
-// last element addressable.
-ctconv_status strides_ok(const int64_t* strides, const int64_t* sizes, int n, int64_t D,
-                         ctconv_dtype dt) {
-    __int128 last = D;
-    for (int i = 0; i < n; ++i) {
-        if (strides[i] < 0) return CTCONV_ERR_SHAPE;
-        if (sizes[i] > 0) last += (__int128)(sizes[i] - 1) * strides[i];
-    }
-    if (last * (int64_t)esize(dt) > INT64_MAX) return CTCONV_ERR_SHAPE;
-    return CTCONV_OK;
-}
-
-// Every row starts on 16 bytes (strides of a dimension of one are not stepped).
-bool rows_aligned(const int64_t* strides, const int64_t* sizes, int n, ctconv_dtype dt) {
-    const int64_t step = 16 / (int64_t)esize(dt);
-    for (int i = 0; i < n; ++i)
-        if (sizes[i] > 1 && strides[i] % step != 0) return false;
-    return true;
-}
-
-// What is written: rows of `row` values that lie apart.  From the smallest
-// stride up, a step must pass everything below it.  (A layout whose dimensions
-// interleave without meeting is not told from one where they meet.)
-bool rows_apart(const int64_t* strides, std::initializer_list<int64_t> sizes, int64_t row) {
-    constexpr int kDims = 3;
-    int64_t step[kDims], size[kDims];
-    int n = 0, dim = 0;
-    for (const int64_t s : sizes) {
-        const int64_t st = strides[dim++];
-        if (s <= 1) continue;
-        int at = n++;
-        for (; at > 0 && step[at - 1] > st; --at) {
-            step[at] = step[at - 1];
-            size[at] = size[at - 1];
-        }
-        step[at] = st;
-        size[at] = s;
-    }
-    __int128 extent = row;
-    for (int i = 0; i < n; ++i) {
-        if (step[i] < extent) return false;
-        extent += (__int128)(size[i] - 1) * step[i];
-    }
-    return true;
-}
-
-struct Check {
-    ctconv_status st = CTCONV_OK;
-    bool align = true;
-    void tensor(const void* p, const int64_t* strides, std::initializer_list<int64_t> sizes,
-                int64_t D, ctconv_dtype dt) {
-        const ctconv_status s = strides_ok(strides, sizes.begin(), (int)sizes.size(), D, dt);
-        if (st == CTCONV_OK) st = s;
-        if (p && !aligned16(p)) align = false;
-        if (!rows_aligned(strides, sizes.begin(), (int)sizes.size(), dt)) align = false;
-    }
-    void pointer(const void* p) {
-        if (p && !aligned16(p)) align = false;
-    }
-    ctconv_status status() const {
-        return st != CTCONV_OK ? st : align ? CTCONV_OK : CTCONV_ERR_ALIGN;
-    }
-};
-
-// Heads and row width of the attention and cache calls.
-ctconv_status head_sizes(int64_t B, int64_t Hkv, int64_t D, ctconv_dtype dt) {
-    if (!dtype_ok(dt)) return CTCONV_ERR_DTYPE;
-    if (B < 0 || B > kMaxInt || Hkv < 1 || Hkv > 65535) return CTCONV_ERR_SHAPE;
-    if (D < 8 || D > 256 || D % 8 != 0) return CTCONV_ERR_SHAPE;
-    return CTCONV_OK;
-}
-
-ctconv_status page_sizes(int64_t num_pages, int64_t page_size, int64_t max_pages) {
-    if (num_pages < 1 || num_pages > kMaxInt || page_size < 1 || page_size > kMaxInt ||
-        max_pages < 1 || max_pages > kMaxInt)
-        return CTCONV_ERR_SHAPE;
-    // slot numbers, and what rounding up to whole workgroups adds, fit int32
-    if ((__int128)page_size * max_pages > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
-    return CTCONV_OK;
-}
-
-Pages make_pages(const int32_t* table, int64_t table_stride, const int64_t* kv_strides,
-                 int64_t num_pages, int64_t page_size, int64_t max_pages, int64_t max_length) {
-    Pages p;
-    p.table = table;
-    p.table_stride = table_stride;
-    p.page_stride = kv_strides[0];
-    p.slot_stride = kv_strides[1];
-    p.head_stride = kv_strides[2];
-    p.num_pages = (int)num_pages;
-    p.page_size = (int)page_size;
-    const int64_t slots = page_size * max_pages;
-    p.slots = (int)(slots < max_length ? slots : max_length);
-    p.fd_page = make_fastdiv((uint32_t)page_size);
-    return p;
-}
-
-// Slot arrays (positions, weights): one value per slot.
-ctconv_status slot_strides_ok(const int64_t* strides, int64_t B, int64_t Hkv, int64_t slots) {
-    const int64_t sizes[2] = {B, Hkv};
-    return strides_ok(strides, sizes, 2, slots, CTCONV_F32);
-}
 
 // The split of one attention call: R query rows per (sequence, cache head),
 // at most `span` visible keys.
@@ -155,8 +41,6 @@ constexpr int64_t kTileRows = 128;  // query rows per workgroup of tile_kernel
 // and 45.5, 113 and 87.5.
 constexpr int64_t kTileFrom = 64;
 
-int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
-
 // Keys per workgroup of tile_kernel.  A workgroup costs about one tile on top
 // of its own (its first loads, its last stores), and the compute units take
 // the workgroups in rounds; splitting pays a join.
@@ -172,43 +56,6 @@ int64_t tile_chunk(int64_t tiles, int64_t keys) {
         }
     }
     return round_up(ceil_div(keys, best), 128);
-}
-
-// Keys per workgroup of stream_kernel, and its waves (figures: one query row,
-// keys and values in memory, not in a cache).
-//  - One workgroup per row tile and no join, where few keys or many row tiles
-//    allow it: 500 keys on 8 tiles 9.8 us against 12.1 split, 1000 keys on 256
-//    tiles 28 against 32; but 2000 keys on 64 tiles 25 against 20 (bf16, D =
-//    128).  Rows of more than 128 values take a wave longer: up to 500 of 256
-//    on 8 tiles 20.8 us against 19.4 split in bf16 (350: 17.2 against 19.3),
-//    56.3 against 35.7 in fp32 (350: 43.3 against 35.5).
-//  - Else chunks that give every compute unit one round of the workgroups its
-//    registers hold (4, 3 or 1 of 4 waves for D up to 64, 128, 256): 30000
-//    keys on 8 tiles take 33 us in 469 workgroups, 40 in 938.  At least 256
-//    keys (a workgroup's start costs about as much as 128), at most 1024, so
-//    that ragged sequences still spread.
-//  - An undivided row tile takes as many waves as its registers allow (16 up to
-//    D = 64, 8 up to 128) where 4 would have more than a block of keys each and
-//    the tiles do not fill the chip by themselves, so that more loads are in
-//    flight: 500 keys of 64 on 64 tiles 9.4 us against 10.3 (fp32 12.7 against
-//    23.4), 2000 on 256 fp32 76 against 86.  More tiles bring loads enough, and
-//    the merge of many waves costs most of a short call (16 keys on 1024 tiles
-//    19.3 us against 6.7, 250 on 8192 198 against 136): there only where each
-//    wave has two blocks (1000 of 128 on 1024, fp32, 229 against 265).
-void stream_split(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, int64_t* chunk,
-                  bool* wide) {
-    const int64_t block = dt == CTCONV_F32 ? 16 : 32, waves = D <= 64 ? 16 : 8;
-    const int64_t few = D <= 128 ? 512 : dt == CTCONV_F32 ? 256 : 384;
-    const bool whole = keys <= few || (keys <= 1024 && tiles >= 128) ||
-                       (keys <= 2048 && tiles >= 256);
-    *wide = whole && D <= 128 && keys > (tiles <= 256 ? 4 : 2 * waves) * block;
-    if (whole) {
-        *chunk = round_up(keys, 128);
-        return;
-    }
-    const int64_t room = D <= 64 ? 1024 : D <= 128 ? 768 : 256;
-    const int64_t c = round_up(ceil_div(keys * tiles, room), 128);
-    *chunk = c < 256 ? 256 : c > 1024 ? 1024 : c;
 }
 
 ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span,
@@ -247,13 +94,6 @@ ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64
     p->part_ml_bytes = round_up((int64_t)parts * 8, 16);
     p->bytes = p->score_bytes + p->part_o_bytes + p->part_ml_bytes;
     return CTCONV_OK;
-}
-
-// |scale| log2(e), not zero: hidden scores are minus infinity times it.
-// (Scores times 1e-30 weigh the same as scores times 0.)
-float score_factor(float scale) {
-    const float c = fabsf(scale) * kLog2e;
-    return c > 1e-30f ? c : 1e-30f;
 }
 
 void apply_plan(const Plan& p, void* ws, AttnArgs* a) {
@@ -696,64 +536,6 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
     a.eps = eps;
     a.inv_C = (float)(1.0 / (double)C);
     return to_status(launch_norm(a, dtype, vec, static_cast<hipStream_t>(stream)));
-}
-
-ctconv_status ctconv_block_run(ctconv_block_op op, const int64_t* sizes, void* const* buffers,
-                               void* workspace, size_t workspace_bytes, void* stream) {
-    if (!sizes || !buffers) return CTCONV_ERR_NULL;
-    int which;
-    memcpy(&which, &op, sizeof which);  // a C caller may pass any int
-    const int64_t* z = sizes;
-    void* const* p = buffers;
-    const auto f32 = [](int64_t bits) {
-        double d;
-        memcpy(&d, &bits, sizeof d);
-        return (float)d;
-    };
-    const auto i32 = [&](int i) { return static_cast<int32_t*>(p[i]); };
-    const auto fp = [&](int i) { return static_cast<float*>(p[i]); };
-    // enumerators: any int64 outside them becomes one that the call refuses
-    const auto code = [](int64_t v) { return v < 0 || v > 1000 ? -1 : (int)v; };
-    const auto as_dtype = [&](int64_t v) {
-        const int c = code(v);
-        ctconv_dtype d;
-        memcpy(&d, &c, sizeof d);
-        return d;
-    };
-    switch (which) {
-        case CTCONV_OP_CACHE_APPEND:
-            return ctconv_cache_append(p[0], p[1], p[2], p[3], i32(4), i32(5), i32(6), i32(7),
-                                       i32(8), fp(9), z[0], z[1], z[2], z[3], z[4], z[5], z[6],
-                                       z + 7, z + 10, z[13], z + 14, as_dtype(z[16]), stream);
-        case CTCONV_OP_PAGED_ATTENTION:
-            return ctconv_paged_attention(p[0], p[1], p[2], i32(3), i32(4), p[5], fp(6), fp(7),
-                                          z[0], z[1], z[2], z[3], z[4], z[5], z[6], z[7], z[8],
-                                          z + 9, z + 11, z + 14, z[16], z + 17, f32(z[19]),
-                                          as_dtype(z[20]), workspace, workspace_bytes, stream);
-        case CTCONV_OP_CACHE_EVICT:
-            return ctconv_cache_evict(p[0], p[1], i32(2), i32(3), i32(4), fp(5), i32(6), fp(7),
-                                      i32(8), i32(9), i32(10), z[0], z[1], z[2], z[3], z[4], z[5],
-                                      z[6], z[7], z[8], z[9], z + 10, z[13], z + 14, z + 16,
-                                      as_dtype(z[18]), stream);
-        case CTCONV_OP_CROSS_ATTENTION:
-            return ctconv_cross_attention(p[0], p[1], p[2], i32(3),
-                                          static_cast<const uint8_t*>(p[4]), p[5], fp(6), z[0],
-                                          z[1], z[2], z[3], z[4], z[5], z + 6, z + 9, z + 12,
-                                          z + 15, z[18], f32(z[19]), as_dtype(z[20]), workspace,
-                                          workspace_bytes, stream);
-        case CTCONV_OP_NORM_RESIDUAL: {
-            const int kinds[3] = {code(z[8]), code(z[9]), code(z[10])};
-            ctconv_norm post, pre;
-            ctconv_gate gate;
-            memcpy(&post, &kinds[0], sizeof(int));
-            memcpy(&pre, &kinds[1], sizeof(int));
-            memcpy(&gate, &kinds[2], sizeof(int));
-            return ctconv_norm_residual(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9],
-                                        z[0], z[1], z + 2, z[7], post, pre, gate, f32(z[11]),
-                                        as_dtype(z[12]), stream);
-        }
-    }
-    return CTCONV_ERR_PARAM;
 }
 
 }  // extern "C"

@@ -106,6 +106,10 @@ struct AttnArgs {
     FastDiv fd_G;
     float c;                     // |scale| * log2(e)
     int negate;                  // scale < 0: the queries change sign
+    // Chunk calls: each sequence's own number of rows.
+    const int32_t *row_starts, *counts;
+    float* lse2;                 // log2 of the sums of weights, [rows, Hq] (weights)
+    int n, rows;                 // most rows of a sequence, rows of the call
 };
 
 struct NormArgs {
@@ -117,6 +121,36 @@ struct NormArgs {
     float eps, inv_C;
 };
 
+// ctconv_cache_pages.
+struct TablesArgs {
+    const int32_t *lengths, *counts, *now, *held, *free_count;
+    int32_t *table, *free_pages, *held_out, *free_count_out;
+    int32_t *row_starts, *row_positions, *row_slots, *positions;
+    float* weight_sum;
+    int64_t table_stride, slot_b, slot_h;
+    int B, rows, Hkv, num_pages, page_size, max_pages;
+    int fused;  // few rows: mapped by the workgroup that moves the pages
+    FastDiv fd_page;
+};
+
+// ctconv_rotary and ctconv_rotary_append; strides in elements.
+struct RotaryArgs {
+    const void *q, *k, *v;
+    const int32_t *positions, *slots;
+    const double* frequencies;
+    void *q_out, *k_out, *v_out;
+    int64_t q_row, q_head, k_row, k_head;  // (of k and v)
+    int64_t q_out_row, q_out_head, k_out_row, k_out_head;
+    int64_t page_stride, slot_stride;
+    int rows, Hq, Hk, D;
+    int half;                    // pairs
+    int page_size, num_slots;
+    int units, v_units, items;   // pairs of pieces per head of q or k, of v, per row
+    int per;                     // rows of a workgroup
+    float scale;
+    FastDiv fd_page, fd_units, fd_v_units, fd_items, fd_half;
+};
+
 hipError_t launch_append(const AppendArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_evict(const EvictArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, ctconv_dtype dt, bool vec, hipStream_t s);
@@ -126,6 +160,13 @@ hipError_t launch_attn_stream(const AttnArgs& a, ctconv_dtype dt, bool paged, hi
 hipError_t launch_attn_tile(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 // The partial results of `splits` workgroups joined, and the slots' weights.
 hipError_t launch_attn_join(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s);
+// The chunk call with few query rows per key head, the join of its splits and its weights.
+hipError_t launch_chunk_stream(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
+hipError_t launch_chunk_join(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
+hipError_t launch_chunk_weights(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
+hipError_t launch_tables(const TablesArgs& a, hipStream_t s);
+hipError_t launch_rotary(const RotaryArgs& a, ctconv_dtype dt, bool pairs, bool append,
+                         hipStream_t s);
 
 }  // namespace block
 }  // namespace ctconv

@@ -1,0 +1,422 @@
+// C ABI of the operators on requests of many lengths: argument validation,
+// planning and launches.  No allocation, no synchronisation, no global state.
+
+#include <math.h>
+#include <string.h>
+
+#include "block_check.h"
+#include "block_internal.h"
+
+using namespace ctconv;
+using namespace ctconv::block;
+
+namespace {
+
+constexpr int64_t kMostSequences = 8192;  // tables_kernel keeps 16 bytes of each in LDS
+constexpr int64_t kFusedRows = 2048;
+constexpr double kTwoPi = 6.283185307179586476925;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int as_int(const void* e) {  // a C caller may pass any int for an enumerator
+    int v;
+    memcpy(&v, e, sizeof v);
+    return v;
+}
+
+ctconv_status rotary_sizes(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int layout,
+                           float scale, ctconv_dtype dt) {
+    if (!dtype_ok(dt)) return CTCONV_ERR_DTYPE;
+    if (layout != CTCONV_ROTARY_HALF && layout != CTCONV_ROTARY_PAIRS) return CTCONV_ERR_PARAM;
+    if (rows < 0 || rows > kMaxInt || Hq < 0 || Hq > 65535 || Hk < 0 || Hk > 65535 || Hq + Hk < 1)
+        return CTCONV_ERR_SHAPE;
+    if (D < 8 || D > 256 || D % 8 != 0 || R < 2 || R > D || R % 2 != 0) return CTCONV_ERR_SHAPE;
+    if (!isfinite(scale)) return CTCONV_ERR_PARAM;
+    return CTCONV_OK;
+}
+
+void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, float scale,
+                   RotaryArgs* a) {
+    memset(a, 0, sizeof(*a));
+    a->rows = (int)rows;
+    a->Hq = (int)Hq;
+    a->Hk = (int)Hk;
+    a->D = (int)D;
+    a->half = (int)(R / 2);
+    a->scale = scale;
+    a->fd_half = make_fastdiv((uint32_t)a->half);
+}
+
+struct ChunkPlan {
+    bool wide;
+    int64_t row_tiles, chunk, splits;
+    int64_t part_o_bytes, part_ml_bytes, lse_bytes, bytes;
+};
+
+ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t Hkv, int64_t D,
+                         int64_t max_length, int64_t window, bool weights, ctconv_dtype dt,
+                         ChunkPlan* p) {
+    memset(p, 0, sizeof(*p));
+    const ctconv_status st = head_sizes(B, Hkv, D, dt);
+    if (st != CTCONV_OK) return st;
+    if (Hq < 1 || Hq > kMaxInt || Hq % Hkv != 0) return CTCONV_ERR_SHAPE;
+    if (rows < 0 || rows > kMaxInt || n < 0 || n > kMaxInt) return CTCONV_ERR_SHAPE;
+    if (max_length < 0 || max_length > kMaxInt - (1 << 20) || window < 0) return CTCONV_ERR_SHAPE;
+    const int64_t G = Hq / Hkv;
+    if ((__int128)n * G > kMaxInt) return CTCONV_ERR_SHAPE;
+    const int64_t R = n * G;
+    p->row_tiles = ceil_div(R, 16);
+    const __int128 tiles = (__int128)B * Hkv * p->row_tiles;
+    if (tiles > kMaxInt || (__int128)B * Hkv * R > kMaxInt) return CTCONV_ERR_SHAPE;
+    const int64_t together = n < 16 ? n : 16;  // rows of one tile end up to this far apart
+    int64_t span = window > 0 && window + together < max_length ? window + together : max_length;
+    span = span > 0 ? span : 1;
+    if (tiles >= 2048)
+        p->chunk = round_up(span, 128);
+    else
+        stream_split((int64_t)tiles, span, D, dt, &p->chunk, &p->wide);
+    p->splits = ceil_div(span, p->chunk);
+    const __int128 values = (__int128)rows * Hq;
+    const __int128 parts = p->splits > 1 ? values * p->splits : 0;
+    if (tiles * p->splits > kMaxInt - 8 || parts * D > ((__int128)1 << 59) ||
+        values > ((__int128)1 << 59))
+        return CTCONV_ERR_SHAPE;
+    p->part_o_bytes = (int64_t)parts * D * 4;
+    p->part_ml_bytes = round_up((int64_t)parts * 8, 16);
+    p->lse_bytes = weights ? round_up((int64_t)values * 4, 16) : 0;
+    p->bytes = p->part_o_bytes + p->part_ml_bytes + p->lse_bytes;
+    return CTCONV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ctconv_status ctconv_cache_pages(const int32_t* lengths, const int32_t* counts,
+                                 const int32_t* now, const int32_t* held,
+                                 const int32_t* free_count, int32_t* page_table,
+                                 int32_t* free_pages, int32_t* held_out, int32_t* free_count_out,
+                                 int32_t* row_starts, int32_t* row_positions, int32_t* row_slots,
+                                 int32_t* positions, float* weight_sum, int64_t B, int64_t rows,
+                                 int64_t Hkv, int64_t num_pages, int64_t page_size,
+                                 int64_t max_pages, int64_t table_stride,
+                                 const int64_t* slot_strides, void* stream) {
+    if (B < 0 || B > kMostSequences || rows < 0 || rows > kMaxInt || Hkv < 1 || Hkv > 65535 ||
+        table_stride < 0)
+        return CTCONV_ERR_SHAPE;
+    ctconv_status st = page_sizes(num_pages, page_size, max_pages);
+    if (st != CTCONV_OK) return st;
+    if ((__int128)B * max_pages > kMaxInt || (__int128)num_pages * page_size > kMaxInt)
+        return CTCONV_ERR_SHAPE;
+    if (B == 0) return CTCONV_OK;
+    const bool slots = counts && (positions || weight_sum);
+    if (!lengths || !held || !free_count || !page_table || !free_pages || !held_out ||
+        !free_count_out || (counts && !row_starts) ||
+        (counts && rows > 0 && (!row_positions || !row_slots)) || (slots && !slot_strides))
+        return CTCONV_ERR_NULL;
+    const int64_t table_rows[1] = {table_stride}, sizes[1] = {B};
+    st = strides_ok(table_rows, sizes, 1, max_pages, CTCONV_F32);
+    if (st == CTCONV_OK && slots) st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
+    if (st != CTCONV_OK) return st;
+    const void* const arrays[] = {lengths,    counts,        now,       held,      free_count,
+                                  page_table, free_pages,    held_out,  free_count_out,
+                                  row_starts, row_positions, row_slots, positions, weight_sum};
+    for (const void* p : arrays)
+        if (!aligned4(p)) return CTCONV_ERR_ALIGN;
+    if (!rows_apart(table_rows, {B}, max_pages) ||
+        (slots && !rows_apart(slot_strides, {B, Hkv}, page_size * max_pages)))
+        return CTCONV_ERR_SHAPE;
+    TablesArgs a;
+    memset(&a, 0, sizeof(a));
+    a.lengths = lengths;
+    a.counts = counts;
+    a.now = now;
+    a.held = held;
+    a.free_count = free_count;
+    a.table = page_table;
+    a.free_pages = free_pages;
+    a.held_out = held_out;
+    a.free_count_out = free_count_out;
+    a.row_starts = row_starts;
+    a.row_positions = row_positions;
+    a.row_slots = row_slots;
+    a.positions = slots ? positions : nullptr;
+    a.weight_sum = slots ? weight_sum : nullptr;
+    a.table_stride = table_stride;
+    if (slots) {
+        a.slot_b = slot_strides[0];
+        a.slot_h = slot_strides[1];
+    }
+    a.B = (int)B;
+    a.rows = counts ? (int)rows : 0;
+    a.Hkv = (int)Hkv;
+    a.num_pages = (int)num_pages;
+    a.page_size = (int)page_size;
+    a.max_pages = (int)max_pages;
+    a.fused = counts && rows <= kFusedRows;
+    a.fd_page = make_fastdiv((uint32_t)page_size);
+    return to_status(launch_tables(a, static_cast<hipStream_t>(stream)));
+}
+
+ctconv_status ctconv_rotary(const void* q, const void* k, const int32_t* positions,
+                            const double* frequencies, void* q_out, void* k_out, int64_t rows,
+                            int64_t Hq, int64_t Hk, int64_t D, int64_t R,
+                            const int64_t* q_strides, const int64_t* k_strides,
+                            const int64_t* q_out_strides, const int64_t* k_out_strides,
+                            ctconv_rotary_layout layout, float scale, ctconv_dtype dtype,
+                            void* stream) {
+    const int kind = as_int(&layout);
+    ctconv_status st = rotary_sizes(rows, Hq, Hk, D, R, kind, scale, dtype);
+    if (st != CTCONV_OK) return st;
+    if (rows == 0) return CTCONV_OK;
+    if (!positions || !frequencies || (Hq > 0 && (!q || !q_out || !q_strides || !q_out_strides)) ||
+        (Hk > 0 && (!k || !k_out || !k_strides || !k_out_strides)))
+        return CTCONV_ERR_NULL;
+    RotaryArgs a;
+    rotary_common(rows, Hq, Hk, D, R, scale, &a);
+    Check c;
+    c.pointer(frequencies);
+    if (Hq > 0) {
+        c.tensor(q, q_strides, {rows, Hq}, D, dtype);
+        c.tensor(q_out, q_out_strides, {rows, Hq}, D, dtype);
+        a.q = q;
+        a.q_out = q_out;
+        a.q_row = q_strides[0];
+        a.q_head = q_strides[1];
+        a.q_out_row = q_out_strides[0];
+        a.q_out_head = q_out_strides[1];
+    }
+    if (Hk > 0) {
+        c.tensor(k, k_strides, {rows, Hk}, D, dtype);
+        c.tensor(k_out, k_out_strides, {rows, Hk}, D, dtype);
+        a.k = k;
+        a.k_out = k_out;
+        a.k_row = k_strides[0];
+        a.k_head = k_strides[1];
+        a.k_out_row = k_out_strides[0];
+        a.k_out_head = k_out_strides[1];
+    }
+    st = c.status();
+    if (st == CTCONV_OK && !aligned4(positions)) st = CTCONV_ERR_ALIGN;
+    if (st != CTCONV_OK) return st;
+    if ((Hq > 0 && !rows_apart(q_out_strides, {rows, Hq}, D)) ||
+        (Hk > 0 && !rows_apart(k_out_strides, {rows, Hk}, D)))
+        return CTCONV_ERR_SHAPE;
+    // in place: the same rows
+    const auto moved = [](const void* in, const void* out, const int64_t* s, const int64_t* t) {
+        return in == out && (s[0] != t[0] || s[1] != t[1]);
+    };
+    if ((Hq > 0 && moved(q, q_out, q_strides, q_out_strides)) ||
+        (Hk > 0 && moved(k, k_out, k_strides, k_out_strides)))
+        return CTCONV_ERR_PARAM;
+    a.positions = positions;
+    a.frequencies = frequencies;
+    return to_status(launch_rotary(a, dtype, kind == CTCONV_ROTARY_PAIRS, false,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+ctconv_status ctconv_rotary_append(const void* q, const void* k_new, const void* v_new,
+                                   const int32_t* positions, const int32_t* slots,
+                                   const double* frequencies, void* q_out, void* k_cache,
+                                   void* v_cache, int64_t rows, int64_t Hq, int64_t Hkv,
+                                   int64_t D, int64_t R, int64_t num_pages, int64_t page_size,
+                                   const int64_t* q_strides, const int64_t* new_strides,
+                                   const int64_t* q_out_strides, const int64_t* kv_strides,
+                                   ctconv_rotary_layout layout, float scale, ctconv_dtype dtype,
+                                   void* stream) {
+    const int kind = as_int(&layout);
+    ctconv_status st = rotary_sizes(rows, Hq, Hkv, D, R, kind, scale, dtype);
+    if (st != CTCONV_OK) return st;
+    if (Hkv < 1) return CTCONV_ERR_SHAPE;
+    st = page_sizes(num_pages, page_size, 1);
+    if (st != CTCONV_OK) return st;
+    if ((__int128)num_pages * page_size > kMaxInt) return CTCONV_ERR_SHAPE;
+    if (rows == 0) return CTCONV_OK;
+    if (!k_new || !v_new || !positions || !slots || !frequencies || !k_cache || !v_cache ||
+        !new_strides || !kv_strides || (Hq > 0 && (!q || !q_out || !q_strides || !q_out_strides)))
+        return CTCONV_ERR_NULL;
+    RotaryArgs a;
+    rotary_common(rows, Hq, Hkv, D, R, scale, &a);
+    Check c;
+    c.pointer(frequencies);
+    if (Hq > 0) {
+        c.tensor(q, q_strides, {rows, Hq}, D, dtype);
+        c.tensor(q_out, q_out_strides, {rows, Hq}, D, dtype);
+        a.q = q;
+        a.q_out = q_out;
+        a.q_row = q_strides[0];
+        a.q_head = q_strides[1];
+        a.q_out_row = q_out_strides[0];
+        a.q_out_head = q_out_strides[1];
+    }
+    c.tensor(k_new, new_strides, {rows, Hkv}, D, dtype);
+    c.tensor(k_cache, kv_strides, {num_pages, page_size, Hkv}, D, dtype);
+    c.pointer(v_new);
+    c.pointer(v_cache);
+    st = c.status();
+    if (st == CTCONV_OK && !(aligned4(positions) && aligned4(slots))) st = CTCONV_ERR_ALIGN;
+    if (st != CTCONV_OK) return st;
+    if ((Hq > 0 && !rows_apart(q_out_strides, {rows, Hq}, D)) ||
+        !rows_apart(kv_strides, {num_pages, page_size, Hkv}, D))
+        return CTCONV_ERR_SHAPE;
+    if (Hq > 0 && q == q_out &&
+        (q_strides[0] != q_out_strides[0] || q_strides[1] != q_out_strides[1]))
+        return CTCONV_ERR_PARAM;
+    a.k = k_new;
+    a.v = v_new;
+    a.k_out = k_cache;
+    a.v_out = v_cache;
+    a.k_row = new_strides[0];
+    a.k_head = new_strides[1];
+    a.page_stride = kv_strides[0];
+    a.slot_stride = kv_strides[1];
+    a.k_out_head = kv_strides[2];
+    a.positions = positions;
+    a.slots = slots;
+    a.frequencies = frequencies;
+    a.page_size = (int)page_size;
+    a.num_slots = (int)(num_pages * page_size);
+    a.fd_page = make_fastdiv((uint32_t)page_size);
+    return to_status(launch_rotary(a, dtype, kind == CTCONV_ROTARY_PAIRS, true,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_scaling scaling,
+                                        double factor, double original, double low, double high,
+                                        double* frequencies) {
+    const int kind = as_int(&scaling);
+    if (R < 2 || R > 256 || R % 2 != 0) return CTCONV_ERR_SHAPE;
+    if (kind < CTCONV_ROTARY_NONE || kind > CTCONV_ROTARY_RAMP_TURNS) return CTCONV_ERR_PARAM;
+    const auto positive = [](double v) { return isfinite(v) && v > 0; };
+    if (!positive(base) || !positive(factor)) return CTCONV_ERR_PARAM;
+    const bool dims = kind == CTCONV_ROTARY_RAMP_DIMS, turns = kind == CTCONV_ROTARY_RAMP_TURNS;
+    if ((dims || turns) &&
+        (!positive(original) || !positive(low) || !isfinite(high) || high <= low))
+        return CTCONV_ERR_PARAM;
+    if (dims && base <= 1) return CTCONV_ERR_PARAM;
+    if (!frequencies) return CTCONV_ERR_NULL;
+    if (kind == CTCONV_ROTARY_BASE && R > 2) base *= pow(factor, (double)R / (double)(R - 2));
+    double from = 0, to = 1;
+    if (dims) {
+        const auto pair = [&](double t) {
+            return (double)R * log(original / (t * kTwoPi)) / (2 * log(base));
+        };
+        from = fmax(floor(pair(high)), 0);
+        to = fmin(ceil(pair(low)), (double)(R - 1));
+    }
+    for (int64_t i = 0; i < R / 2; ++i) {
+        const double f = pow(base, -2.0 * (double)i / (double)R);
+        double keep = 1;
+        if (kind == CTCONV_ROTARY_LINEAR) keep = 0;
+        if (dims) keep = 1 - fmin(fmax(((double)i - from) / fmax(to - from, 0.001), 0), 1);
+        if (turns) keep = fmin(fmax((original * f / kTwoPi - low) / (high - low), 0), 1);
+        frequencies[i] = keep * f + (1 - keep) * f / factor;
+    }
+    return CTCONV_OK;
+}
+
+ctconv_status ctconv_chunk_attention_workspace_bytes(int64_t B, int64_t rows, int64_t n,
+                                                     int64_t Hq, int64_t Hkv, int64_t D,
+                                                     int64_t max_length, int64_t window,
+                                                     int weights, ctconv_dtype dtype,
+                                                     size_t* bytes) {
+    if (!bytes) return CTCONV_ERR_NULL;
+    ChunkPlan p;
+    const ctconv_status st =
+        chunk_plan(B, rows, n, Hq, Hkv, D, max_length, window, weights != 0, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    *bytes = (size_t)p.bytes;
+    return CTCONV_OK;
+}
+
+ctconv_status ctconv_chunk_attention(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* page_table, const int32_t* lengths,
+                                     const int32_t* row_starts, const int32_t* counts, void* out,
+                                     float* lse, float* weight_sum, int64_t B, int64_t rows,
+                                     int64_t n, int64_t Hq, int64_t Hkv, int64_t D,
+                                     int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                     int64_t max_length, int64_t window, const int64_t* q_strides,
+                                     const int64_t* kv_strides, const int64_t* out_strides,
+                                     int64_t table_stride, const int64_t* slot_strides,
+                                     float scale, ctconv_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    ChunkPlan p;
+    ctconv_status st = chunk_plan(B, rows, n, Hq, Hkv, D, max_length, window,
+                                  weight_sum != nullptr, dtype, &p);
+    if (st != CTCONV_OK) return st;
+    st = page_sizes(num_pages, page_size, max_pages);
+    if (st != CTCONV_OK) return st;
+    if (max_length > page_size * max_pages || table_stride < 0) return CTCONV_ERR_SHAPE;
+    if (!row_starts && (__int128)B * n != rows) return CTCONV_ERR_SHAPE;
+    if (!isfinite(scale)) return CTCONV_ERR_PARAM;
+    if (B == 0 || rows == 0 || n == 0) return CTCONV_OK;
+    if (!q || !k_cache || !v_cache || !page_table || !lengths || !out || !q_strides ||
+        !kv_strides || !out_strides || (weight_sum && !slot_strides))
+        return CTCONV_ERR_NULL;
+    const int64_t batch = row_starts ? 1 : B, in_batch = row_starts ? rows : n;
+    Check c;
+    c.tensor(q, q_strides, {batch, in_batch, Hq}, D, dtype);
+    c.tensor(out, out_strides, {batch, in_batch, Hq}, D, dtype);
+    c.tensor(k_cache, kv_strides, {num_pages, page_size, Hkv}, D, dtype);
+    c.pointer(v_cache);
+    c.pointer(workspace);
+    if (weight_sum && c.st == CTCONV_OK)
+        c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
+    st = c.status();
+    if (st != CTCONV_OK) return st;
+    if (!rows_apart(out_strides, {batch, in_batch, Hq}, D) ||
+        (weight_sum && !rows_apart(slot_strides, {B, Hkv}, max_length)))
+        return CTCONV_ERR_SHAPE;
+    if (p.bytes > 0 && (!workspace || workspace_bytes < (size_t)p.bytes))
+        return CTCONV_ERR_WORKSPACE;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.out = out;
+    a.lse = lse;
+    a.lengths = lengths;
+    a.weight_sum = weight_sum;
+    a.row_starts = row_starts;
+    a.counts = row_starts ? nullptr : counts;
+    a.pages = make_pages(page_table, table_stride, kv_strides, num_pages, page_size, max_pages,
+                         max_length);
+    a.q_b = q_strides[0];
+    a.q_row = q_strides[1];
+    a.q_head = q_strides[2];
+    a.o_b = out_strides[0];
+    a.o_row = out_strides[1];
+    a.o_head = out_strides[2];
+    if (weight_sum) {
+        a.slot_b = slot_strides[0];
+        a.slot_h = slot_strides[1];
+    }
+    a.B = (int)B;
+    a.n = (int)n;
+    a.rows = (int)rows;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.G = (int)(Hq / Hkv);
+    a.R = (int)(n * a.G);
+    a.D = (int)D;
+    a.window = (int)(window < max_length ? window : 0);
+    a.fd_G = make_fastdiv((uint32_t)a.G);
+    a.c = score_factor(scale);
+    a.negate = scale < 0;
+    a.row_tiles = (int)p.row_tiles;
+    a.chunk = (int)p.chunk;
+    a.splits = (int)p.splits;
+    a.wide = p.wide;
+    char* at = static_cast<char*>(workspace);
+    a.part_o = reinterpret_cast<float*>(at);
+    a.part_ml = reinterpret_cast<float*>(at + p.part_o_bytes);
+    a.lse2 = weight_sum ? reinterpret_cast<float*>(at + p.part_o_bytes + p.part_ml_bytes) : nullptr;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    st = to_status(launch_chunk_stream(a, dtype, s));
+    if (st == CTCONV_OK && a.splits > 1) st = to_status(launch_chunk_join(a, dtype, s));
+    if (st == CTCONV_OK && weight_sum) st = to_status(launch_chunk_weights(a, dtype, s));
+    return st;
+}
+
+}  // extern "C"

@@ -32,7 +32,9 @@ EXPORTED = (
     "ctconv_scratch_bytes", "ctconv_clock_probe_bytes", "ctconv_clock_probe",
     "ctconv_cache_append", "ctconv_paged_attention_workspace_bytes", "ctconv_paged_attention",
     "ctconv_cache_evict", "ctconv_cross_attention_workspace_bytes", "ctconv_cross_attention",
-    "ctconv_norm_residual", "ctconv_block_run",
+    "ctconv_norm_residual", "ctconv_block_run", "ctconv_cache_pages", "ctconv_rotary",
+    "ctconv_rotary_append", "ctconv_rotary_frequencies",
+    "ctconv_chunk_attention_workspace_bytes", "ctconv_chunk_attention",
 )
 
 DW_AUTO, DW_ROW, DW_ELEMENT = 0, 1, 2
@@ -41,6 +43,8 @@ ACT_NONE, ACT_ELU = 0, 1
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 GATE_NONE, GATE_LINEAR, GATE_SIGMOID, GATE_TANH = 0, 1, 2, 3
+ROTARY_HALF, ROTARY_PAIRS = 0, 1
+ROTARY_NONE, ROTARY_LINEAR, ROTARY_BASE, ROTARY_RAMP_DIMS, ROTARY_RAMP_TURNS = 0, 1, 2, 3, 4
 
 
 class CtconvError(RuntimeError):
@@ -129,6 +133,22 @@ def load(path: str = LIB_PATH):
     lib.ctconv_paged_attention.argtypes = [c_vp] * 8 + [c_i64] * 9 + [
         _i64p, _i64p, _i64p, c_i64, _i64p, c_f, c_int, c_vp, c_sz, c_vp]
     lib.ctconv_paged_attention.restype = c_int
+    lib.ctconv_cache_pages.argtypes = [c_vp] * 14 + [c_i64] * 7 + [_i64p, c_vp]
+    lib.ctconv_cache_pages.restype = c_int
+    lib.ctconv_rotary.argtypes = [c_vp] * 6 + [c_i64] * 5 + [_i64p] * 4 + [c_int, c_f, c_int, c_vp]
+    lib.ctconv_rotary.restype = c_int
+    lib.ctconv_rotary_append.argtypes = [c_vp] * 9 + [c_i64] * 7 + [_i64p] * 4 + [c_int, c_f, c_int,
+                                                                              c_vp]
+    lib.ctconv_rotary_append.restype = c_int
+    c_d = ctypes.c_double
+    lib.ctconv_rotary_frequencies.argtypes = [c_i64, c_d, c_int] + [c_d] * 4 + [c_vp]
+    lib.ctconv_rotary_frequencies.restype = c_int
+    lib.ctconv_chunk_attention_workspace_bytes.argtypes = [c_i64] * 8 + [c_int, c_int,
+                                                                         ctypes.POINTER(c_sz)]
+    lib.ctconv_chunk_attention_workspace_bytes.restype = c_int
+    lib.ctconv_chunk_attention.argtypes = [c_vp] * 10 + [c_i64] * 11 + [
+        _i64p, _i64p, _i64p, c_i64, _i64p, c_f, c_int, c_vp, c_sz, c_vp]
+    lib.ctconv_chunk_attention.restype = c_int
     lib.ctconv_cache_evict.argtypes = [c_vp] * 11 + [c_i64] * 10 + [_i64p, c_i64, _i64p, _i64p,
                                                                     c_int, c_vp]
     lib.ctconv_cache_evict.restype = c_int
@@ -694,6 +714,7 @@ class ConvWS(Conv):
 
 OP_CACHE_APPEND, OP_PAGED_ATTENTION, OP_CACHE_EVICT = 0, 1, 2
 OP_CROSS_ATTENTION, OP_NORM_RESIDUAL = 3, 4
+OP_CACHE_PAGES, OP_ROTARY, OP_ROTARY_APPEND, OP_CHUNK_ATTENTION = 16, 17, 18, 19
 
 
 def _strides(given, default):
@@ -899,6 +920,140 @@ class NormResidual(_Plan):
                        scale_ptr or 0, gate_ptr or 0, pre_weight_ptr or 0, pre_bias_ptr or 0,
                        x_out_ptr or 0, y_ptr or 0),
             None, 0, stream)
+        if st != 0:
+            raise CtconvError(self._name, st)
+
+
+class CachePages(_Plan):
+    """ctconv_cache_pages for one shape: tables of B sequences, maps of `rows` new rows at most."""
+
+    def __init__(self, B: int, rows: int, num_pages: int, page_size: int, max_pages: int,
+                 Hkv: int = 1, table_stride=None, slot_strides=None):
+        self.B, self.rows, self.Hkv = int(B), int(rows), int(Hkv)
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.max_pages = int(max_pages)
+        self.slots = self.page_size * self.max_pages
+        self._prepare("ctconv_cache_pages", OP_CACHE_PAGES, 14,
+                      (self.B, self.rows, self.Hkv, self.num_pages, self.page_size,
+                       self.max_pages,
+                       self.max_pages if table_stride is None else int(table_stride),
+                       _strides(slot_strides, (self.Hkv * self.slots, self.slots))))
+
+    def __call__(self, lengths_ptr, counts_ptr, now_ptr, held_ptr, free_count_ptr, table_ptr,
+                 free_pages_ptr, held_out_ptr, free_count_out_ptr, row_starts_ptr,
+                 row_positions_ptr, row_slots_ptr, positions_ptr, weight_ptr, stream: int) -> None:
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(lengths_ptr or 0, counts_ptr or 0, now_ptr or 0, held_ptr or 0,
+                       free_count_ptr or 0, table_ptr or 0, free_pages_ptr or 0, held_out_ptr or 0,
+                       free_count_out_ptr or 0, row_starts_ptr or 0, row_positions_ptr or 0,
+                       row_slots_ptr or 0, positions_ptr or 0, weight_ptr or 0),
+            None, 0, stream)
+        if st != 0:
+            raise CtconvError(self._name, st)
+
+
+class Rotary(_Plan):
+    """ctconv_rotary for one shape; dense [rows, H, D] tensors without strides.
+    R: values of a head that turn, default all."""
+
+    def __init__(self, rows: int, Hq: int, Hk: int, D: int, R=None, layout: int = ROTARY_HALF,
+                 scale: float = 1.0, dtype: int = CTCONV_F32, q_strides=None, k_strides=None,
+                 q_out_strides=None, k_out_strides=None):
+        self.rows, self.Hq, self.Hk, self.D = int(rows), int(Hq), int(Hk), int(D)
+        self.R, self.dtype = self.D if R is None else int(R), dtype
+        q, k = (self.Hq * self.D, self.D), (self.Hk * self.D, self.D)
+        self._prepare("ctconv_rotary", OP_ROTARY, 6,
+                      (self.rows, self.Hq, self.Hk, self.D, self.R, _strides(q_strides, q),
+                       _strides(k_strides, k), _strides(q_out_strides, q),
+                       _strides(k_out_strides, k), layout, float(scale), dtype))
+
+    def __call__(self, q_ptr, k_ptr, positions_ptr, frequencies_ptr, q_out_ptr, k_out_ptr,
+                 stream: int) -> None:
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(q_ptr or 0, k_ptr or 0, positions_ptr or 0, frequencies_ptr or 0,
+                       q_out_ptr or 0, k_out_ptr or 0),
+            None, 0, stream)
+        if st != 0:
+            raise CtconvError(self._name, st)
+
+
+class RotaryAppend(_Plan):
+    """ctconv_rotary_append for one shape; dense [rows, H, D] rows and pages of
+    [Hkv, page_size, D] without strides."""
+
+    def __init__(self, rows: int, Hq: int, Hkv: int, D: int, num_pages: int, page_size: int,
+                 R=None, layout: int = ROTARY_HALF, scale: float = 1.0, dtype: int = CTCONV_F32,
+                 q_strides=None, new_strides=None, q_out_strides=None, kv_strides=None):
+        self.rows, self.Hq, self.Hkv, self.D = int(rows), int(Hq), int(Hkv), int(D)
+        self.R, self.dtype = self.D if R is None else int(R), dtype
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        q, k = (self.Hq * self.D, self.D), (self.Hkv * self.D, self.D)
+        page = self.page_size * self.D
+        self._prepare("ctconv_rotary_append", OP_ROTARY_APPEND, 9,
+                      (self.rows, self.Hq, self.Hkv, self.D, self.R, self.num_pages,
+                       self.page_size, _strides(q_strides, q), _strides(new_strides, k),
+                       _strides(q_out_strides, q),
+                       _strides(kv_strides, (self.Hkv * page, self.D, page)), layout,
+                       float(scale), dtype))
+
+    def __call__(self, q_ptr, k_new_ptr, v_new_ptr, positions_ptr, slots_ptr, frequencies_ptr,
+                 q_out_ptr, k_ptr, v_ptr, stream: int) -> None:
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(q_ptr or 0, k_new_ptr or 0, v_new_ptr or 0, positions_ptr or 0,
+                       slots_ptr or 0, frequencies_ptr or 0, q_out_ptr or 0, k_ptr or 0,
+                       v_ptr or 0),
+            None, 0, stream)
+        if st != 0:
+            raise CtconvError(self._name, st)
+
+
+def ctconv_chunk_attention_workspace_bytes(B: int, rows: int, n: int, Hq: int, Hkv: int, D: int,
+                                           max_length: int, window: int, weights: bool,
+                                           dtype: int) -> int:
+    nb = ctypes.c_size_t(0)
+    _check("ctconv_chunk_attention_workspace_bytes",
+           load().ctconv_chunk_attention_workspace_bytes(B, rows, n, Hq, Hkv, D, max_length,
+                                                         window, int(bool(weights)), dtype,
+                                                         ctypes.byref(nb)))
+    return int(nb.value)
+
+
+class ChunkAttention(_Paged):
+    """ctconv_chunk_attention for one shape: `rows` new rows in all (packed; B * n
+    when padded), n at most of a sequence.  weights: whether calls pass a
+    weight_sum.  scale: D ** -0.5.  Without strides q and out are dense, packed
+    [rows, Hq, D] or padded [B, n, Hq, D]."""
+
+    def __init__(self, B: int, rows: int, n: int, Hq: int, Hkv: int, D: int, num_pages: int,
+                 page_size: int, max_pages: int, max_length=None, window: int = 0, scale=None,
+                 weights: bool = False, dtype: int = CTCONV_F32, q_strides=None, kv_strides=None,
+                 out_strides=None, table_stride=None, slot_strides=None):
+        self._cache(B, Hkv, D, num_pages, page_size, max_pages, kv_strides, table_stride,
+                    slot_strides)
+        self.rows, self.n, self.Hq = int(rows), int(n), int(Hq)
+        self.window, self.dtype, self.weights = int(window), dtype, bool(weights)
+        self.max_length = self.slots if max_length is None else int(max_length)
+        dense = (self.n * self.Hq * self.D, self.Hq * self.D, self.D)
+        self.workspace_bytes = ctconv_chunk_attention_workspace_bytes(
+            self.B, self.rows, self.n, self.Hq, self.Hkv, self.D, self.max_length, self.window,
+            self.weights, dtype)
+        self._prepare("ctconv_chunk_attention", OP_CHUNK_ATTENTION, 10,
+                      (self.B, self.rows, self.n, self.Hq, self.Hkv, self.D, self.num_pages,
+                       self.page_size, self.max_pages, self.max_length, self.window,
+                       _strides(q_strides, dense), self._kv, _strides(out_strides, dense),
+                       self._table, self._slot, _scale(scale, self.D), dtype))
+
+    def __call__(self, q_ptr, k_ptr, v_ptr, table_ptr, lengths_ptr, row_starts_ptr, counts_ptr,
+                 out_ptr, lse_ptr, weight_ptr, ws_ptr, ws_bytes: int, stream: int) -> None:
+        st = self._fn(
+            self._op, self._sizes_ptr,
+            self._pack(q_ptr or 0, k_ptr or 0, v_ptr or 0, table_ptr or 0, lengths_ptr or 0,
+                       row_starts_ptr or 0, counts_ptr or 0, out_ptr or 0, lse_ptr or 0,
+                       weight_ptr or 0),
+            ws_ptr, ws_bytes, stream)
         if st != 0:
             raise CtconvError(self._name, st)
 
@@ -1159,3 +1314,225 @@ def norm_residual(x, h, post: int = NORM_NONE, post_weight=None, post_bias=None,
          xo.data_ptr(), _ptr(yo), _stream(stream))
     _claim(side, x, h, gate, pw, pb, sc, nw, nb, xo, yo)
     return xo, yo
+
+
+def _on_device(device, stream):
+    """The call's stream must be on its tensors' device (the kernels run there)."""
+    torch = _torch()
+    on = torch.cuda.current_stream().device if stream is None else stream.device
+    if on != device:
+        raise ValueError(f"the tensors are on {device}, the stream is on {on}")
+
+
+def cache_pages(page_table, held, free_pages, free_count, lengths, num_pages=None,
+                page_size: int = 16, counts=None, now=None, rows=None, positions=None,
+                weight_sum=None, stream=None):
+    """Make page tables follow the lengths, in place (see ctconv_cache_pages):
+    page_table int32 [B, max_pages], held int32 [B], the stack free_pages int32
+    [num_pages] with free_count int32 [1] on it.  With counts int32 [B], the
+    new rows of each sequence (lengths counts them already), returns their maps
+    (row_starts [B + 1], row_positions [rows], row_slots [rows]) for `rows` rows
+    in all, and sets positions int32 and weight_sum fp32 [B, Hkv, slots] (or
+    None) of their slots.  Without counts returns None."""
+    torch = _torch()
+    if not page_table.is_cuda:
+        raise ValueError("page_table must be a device tensor")
+    dev = page_table.device
+    _on_device(dev, stream)
+    _rows_ready("page_table", page_table, torch.int32, dev, 2)
+    B, cols = page_table.shape
+    for name, t, shape in (("held", held, (B,)), ("lengths", lengths, (B,)),
+                           ("free_count", free_count, (1,))):
+        _required(name, t)
+        _index(name, t, dev, shape)
+    _required("free_pages", free_pages)
+    pages = free_pages.numel() if num_pages is None else int(num_pages)
+    _index("free_pages", free_pages, dev, (pages,))
+    for name, t in (("counts", counts), ("now", now)):
+        _index(name, t, dev, (B,))
+    if counts is None:
+        if positions is not None or weight_sum is not None or rows:
+            raise ValueError("row maps and slot arrays need counts")
+        rows = 0
+    elif rows is None:
+        raise ValueError("rows, the number of rows to map, is required with counts")
+    Hkv, slots = 1, None
+    some = positions if positions is not None else weight_sum
+    if some is not None:
+        Hkv = some.shape[1] if some.dim() == 3 else 0
+        slots = _slot_arrays((("positions", positions, torch.int32),
+                              ("weight_sum", weight_sum, torch.float32)), B, Hkv,
+                             cols * page_size, dev)
+    maps = None
+    if counts is not None:
+        maps = tuple(torch.empty(n, dtype=torch.int32, device=dev) for n in (B + 1, rows, rows))
+        if B == 0:  # nothing is enqueued for no sequence
+            maps[0].zero_()
+            maps[1].fill_(-1)
+            maps[2].fill_(-1)
+    plan = CachePages(B, rows, pages, page_size, cols, Hkv, page_table.stride(0), slots)
+    side = _side_stream(stream, dev)
+    starts, at, to = maps if maps is not None else (None, None, None)
+    plan(lengths.data_ptr(), _ptr(counts), _ptr(now), held.data_ptr(), free_count.data_ptr(),
+         page_table.data_ptr(), free_pages.data_ptr(), held.data_ptr(), free_count.data_ptr(),
+         _ptr(starts), _ptr(at), _ptr(to), _ptr(positions), _ptr(weight_sum), _stream(stream))
+    _claim(side, lengths, counts, now, held, free_count, page_table, free_pages, starts, at, to,
+           positions, weight_sum)
+    return maps
+
+
+def rotary_frequencies(R: int, base: float = 10000.0, scaling: int = ROTARY_NONE,
+                       factor: float = 1.0, original: float = 4096.0, low: float = 1.0,
+                       high: float = 4.0, device=None):
+    """fp64 [R / 2], radians per position, for rotary and rotary_append (see
+    ctconv_rotary_frequencies)."""
+    torch = _torch()
+    host = (ctypes.c_double * max(1, int(R) // 2))()
+    _check("ctconv_rotary_frequencies",
+           load().ctconv_rotary_frequencies(R, base, scaling, factor, original, low, high,
+                                            ctypes.addressof(host)))
+    return torch.tensor(list(host), dtype=torch.float64, device=device)
+
+
+def _rotary_rows(q, k, positions, frequencies):
+    """Checks what rotary and rotary_append share: (rows, Hq, Hk, D, R, device, dtype)."""
+    torch = _torch()
+    some = q if q is not None else k
+    if some is None or not some.is_cuda:
+        raise ValueError("q or k must be a device tensor")
+    dev, dt = some.device, some.dtype
+    for name, t in (("q", q), ("k", k)):
+        if t is not None:
+            _rows_ready(name, t, dt, dev, 3)
+            if t.shape[0] != some.shape[0] or t.shape[2] != some.shape[2]:
+                raise ValueError("q and k must be [rows, heads, D] of the same rows and width")
+    rows, _, D = some.shape
+    _required("positions", positions)
+    _index("positions", positions, dev, (rows,))
+    _required("frequencies", frequencies)
+    _check_tensor("frequencies", frequencies, torch.float64, dev)
+    if frequencies.dim() != 1 or not frequencies.is_contiguous():
+        raise ValueError("frequencies must be a contiguous [R / 2] tensor")
+    return (rows, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], D,
+            2 * frequencies.numel(), dev, dt)
+
+
+def rotary(q, k, positions, frequencies, layout: int = ROTARY_HALF, scale: float = 1.0,
+           q_out=None, k_out=None, stream=None):
+    """(q, k) turned by their rows' positions (see ctconv_rotary): q [rows, Hq, D]
+    and k [rows, Hk, D] (one of them may be None), positions int32 [rows],
+    frequencies fp64 [R / 2].  q_out may be q and k_out may be k; without them rows of
+    a negative position are left undefined."""
+    torch = _torch()
+    rows, Hq, Hk, D, R, dev, dt = _rotary_rows(q, k, positions, frequencies)
+    _on_device(dev, stream)
+    yq = None if q is None else _result(q_out, (rows, Hq, D), dt, dev, "q_out")
+    yk = None if k is None else _result(k_out, (rows, Hk, D), dt, dev, "k_out")
+
+    def strides(t):
+        return None if t is None else t.stride()[:2]
+
+    plan = Rotary(rows, Hq, Hk, D, R, layout, scale, dtype_code(q if q is not None else k),
+                  strides(q), strides(k), strides(yq), strides(yk))
+    side = _side_stream(stream, dev)
+    plan(_ptr(q), _ptr(k), positions.data_ptr(), frequencies.data_ptr(), _ptr(yq), _ptr(yk),
+         _stream(stream))
+    _claim(side, q, k, positions, frequencies, yq, yk)
+    return yq, yk
+
+
+def rotary_append(q, k_new, v_new, positions, slots, frequencies, k_cache, v_cache,
+                  layout: int = ROTARY_HALF, scale: float = 1.0, q_out=None, stream=None):
+    """q turned (returned; None without q), and k_new turned and v_new copied to the
+    slots of the cache (see ctconv_rotary_append): q [rows, Hq, D], k_new, v_new
+    [rows, Hkv, D], positions and slots int32 [rows] (row_positions and
+    row_slots of cache_pages), k_cache, v_cache [num_pages, Hkv, page_size, D]."""
+    torch = _torch()
+    _required("k_new", k_new)
+    rows, Hq, Hkv, D, R, dev, dt = _rotary_rows(q, k_new, positions, frequencies)
+    _on_device(dev, stream)
+    _required("v_new", v_new)
+    _rows_ready("v_new", v_new, dt, dev, 3)
+    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
+        k_new, v_new = k_new.contiguous(), v_new.contiguous()
+        if v_new.shape != k_new.shape:
+            raise ValueError("k_new and v_new must have the same shape")
+    _required("slots", slots)
+    _index("slots", slots, dev, (rows,))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _rows_ready(name, t, dt, dev, 4)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    pages, H, size, Dc = k_cache.shape
+    if (H, Dc) != (Hkv, D):
+        raise ValueError("the cache's heads or width do not match k_new")
+    st = k_cache.stride()
+    yq = None if q is None else _result(q_out, (rows, Hq, D), dt, dev, "q_out")
+    plan = RotaryAppend(rows, Hq, Hkv, D, pages, size, R, layout, scale, dtype_code(k_new),
+                        None if q is None else q.stride()[:2], k_new.stride()[:2],
+                        None if q is None else yq.stride()[:2], (st[0], st[2], st[1]))
+    side = _side_stream(stream, dev)
+    plan(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+         frequencies.data_ptr(), _ptr(yq), k_cache.data_ptr(), v_cache.data_ptr(),
+         _stream(stream))
+    _claim(side, q, k_new, v_new, positions, slots, frequencies, yq, k_cache, v_cache)
+    return yq
+
+
+def chunk_attention(q, k_cache, v_cache, page_table, lengths, row_starts=None, counts=None, n=None,
+                    max_length=None, window: int = 0, scale=None, weight_sum=None, out=None,
+                    lse=None, workspace=None, stream=None):
+    """(out, lse) of each sequence's new rows over the paged cache that holds them
+    already (see ctconv_chunk_attention).  Packed: q [rows, Hq, D] with
+    row_starts int32 [B + 1] and n, a bound on the rows of a sequence (default:
+    rows).  Padded: q [B, n, Hq, D] with counts int32 [B] or None.  lse fp32
+    [rows, Hq] or [B, n, Hq].  weight_sum fp32 [B, Hkv, slots] or None is added
+    to.  Without out and lse, what lies behind a sequence's rows is undefined."""
+    torch = _torch()
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    dev, dt = q.device, q.dtype
+    _on_device(dev, stream)
+    packed = row_starts is not None
+    _rows_ready("q", q, dt, dev, 3 if packed else 4)
+    pages, size, cols, Hkv, Dc, kv = _cache_tensors(k_cache, v_cache, page_table, dt, dev)
+    B, (Hq, D) = page_table.shape[0], q.shape[-2:]
+    if packed:
+        if counts is not None:
+            raise ValueError("counts follow from row_starts")
+        rows = q.shape[0]
+        n = rows if n is None else int(n)
+        _index("row_starts", row_starts, dev, (B + 1,))
+        q_strides = (0,) + tuple(q.stride()[:2])
+    else:
+        if n is not None and n != q.shape[1]:
+            raise ValueError("n follows from q")
+        n = q.shape[1]
+        rows = q.shape[0] * n
+        _index("counts", counts, dev, (B,))
+        q_strides = q.stride()[:3]
+    if Dc != D or (not packed and q.shape[0] != B):
+        raise ValueError("the cache's width or table rows do not match q")
+    _required("lengths", lengths)
+    _index("lengths", lengths, dev, (B,))
+    slots = _slot_arrays((("weight_sum", weight_sum, torch.float32),), B, Hkv, cols * size, dev)
+    y = _result(out, tuple(q.shape), dt, dev)
+    if lse is None:
+        lse = torch.empty(tuple(q.shape[:-1]), dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("lse", lse, torch.float32, dev, shape=tuple(q.shape[:-1]))
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    y_strides = (0,) + tuple(y.stride()[:2]) if packed else y.stride()[:3]
+    plan = ChunkAttention(B, rows, n, Hq, Hkv, D, pages, size, cols, max_length, window, scale,
+                          weight_sum is not None, dtype_code(q), q_strides, kv, y_strides,
+                          page_table.stride(0), slots)
+    ws = _workspace(workspace, plan.workspace_bytes, dev)
+    side = _side_stream(stream, dev)
+    plan(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+         lengths.data_ptr(), _ptr(row_starts), _ptr(counts), y.data_ptr(), lse.data_ptr(),
+         _ptr(weight_sum), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+         _stream(stream))
+    _claim(side, q, k_cache, v_cache, page_table, lengths, row_starts, counts, y, lse, weight_sum,
+           ws)
+    return y, lse
