@@ -34,7 +34,8 @@ FLAGS = [
 SOURCES = ["ctconv_api.hip", "prepack.hip", "gather.hip", "pointwise.hip", "stream.hip",
            "depthwise.hip", "polyphase.hip", "polyrw.hip", "noalloc.hip", "clock.hip"]
 BLOCK_SOURCES = ["block_api.hip", "request_api.hip", "block_run.hip", "norm.hip", "cache.hip",
-                 "pages.hip", "rotary.hip", "attn_stream.hip", "attn_tile.hip", "attn_chunk.hip"]
+                 "pages.hip", "rotary.hip", "attn_stream.hip", "attn_tile.hip", "attn_chunk.hip",
+                 "attn_chunk_tile.hip"]
 HEADERS = [os.path.join(CSRC, "ctconv_internal.h"), os.path.join(CSRC, "mfma_common.h"),
            os.path.join(INCLUDE, "ctconv.h")]
 

@@ -45,6 +45,7 @@
 
 #pragma once
 
+#include "attn_chunk.h"
 #include "block_internal.h"
 #include "mfma_common.h"
 
@@ -60,8 +61,6 @@ using mfma::u32x4;
 constexpr float kRaise = 8.f;
 constexpr int kPiece = 1024;
 
-__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
 // A maximum as what weights are taken against: where nothing is seen (minus
 // infinity), 0, so that the weights of hidden scores are zero and a sum that
 // is NaN (no maximum is, see fmaxf) stays NaN.
@@ -76,64 +75,6 @@ __device__ inline void visible(const AttnArgs& a, int b, int& first, int& span) 
     const int n = a.lengths ? clamped(a.lengths[b], hi) : hi;
     first = PAGED && a.window > 0 && n > a.window ? n - a.window : 0;
     span = n - first;
-}
-
-// The new rows of sequence b: row i of `count` has slot off + i; `live` of them exist.
-struct ChunkRows {
-    int len, count, live, off;
-    int64_t row0;  // the first one's number in the call
-};
-__device__ inline ChunkRows chunk_rows(const AttnArgs& a, int b) {
-    ChunkRows r;
-    r.len = clamped(a.lengths[b], a.pages.slots);
-    if (a.row_starts) {
-        const int from = a.row_starts[b];
-        const int64_t given = (int64_t)a.row_starts[b + 1] - from;
-        r.row0 = from;
-        r.count = given < 0 ? 0 : given > a.n ? a.n : (int)given;
-        const int room = from >= 0 && from < a.rows ? a.rows - from : 0;
-        r.live = r.count < room ? r.count : room;
-    } else {
-        r.row0 = (int64_t)b * a.n;
-        r.live = r.count = a.counts ? clamped(a.counts[b], a.n) : a.n;
-    }
-    r.off = r.len - r.count;
-    return r;
-}
-// The slots that some of the rows i0 .. i1 see: [first, first + span).
-__device__ inline void chunk_span(const AttnArgs& a, const ChunkRows& r, int i0, int i1, int& first,
-                                  int& span) {
-    first = a.window > 0 && r.off + i0 + 1 > a.window ? r.off + i0 + 1 - a.window : 0;
-    span = r.off + i1 + 1 - first;
-    span = span > 0 ? span : 0;
-}
-// Log-sum-exp of a chunk call's row: the result, and what its weights are taken against.
-__device__ inline void write_lse(const AttnArgs& a, int64_t at, float top, float sum) {
-    if (a.lse) a.lse[at] = top * kLn2 + logf(sum);
-    // a row without a visible slot adds nothing: exp2(s - infinity)
-    if (a.lse2)
-        a.lse2[at] = top == -__builtin_huge_valf() && sum == 0.f
-                         ? __builtin_huge_valf()
-                         : top + __builtin_amdgcn_logf(sum);
-}
-// Bits [0, x) of 32.
-__device__ inline uint32_t low_bits(int x) {
-    return x >= 32 ? 0xFFFFFFFFu : x <= 0 ? 0u : (1u << x) - 1;
-}
-
-// The infinities and NaN of packed values, set to zero; whether there were any.
-template <class TR>
-__device__ inline bool take_odd(uint32_t& w) {
-    if constexpr (std::is_same_v<TR, TF32>) {
-        const bool odd = (w & 0x7F800000u) == 0x7F800000u;
-        w = odd ? 0u : w;
-        return odd;
-    } else {
-        constexpr uint32_t E = std::is_same_v<TR, TBF16> ? 0x7F80u : 0x7C00u;
-        const bool low = (w & E) == E, high = (w >> 16 & E) == E;
-        w &= (low ? 0xFFFF0000u : 0xFFFFFFFFu) & (high ? 0xFFFFu : 0xFFFFFFFFu);
-        return low || high;
-    }
 }
 
 template <class TR, int DP, bool PAGED, bool EXACT, int NW, bool CHUNK = false>

@@ -41,23 +41,6 @@ constexpr int64_t kTileRows = 128;  // query rows per workgroup of tile_kernel
 // and 45.5, 113 and 87.5.
 constexpr int64_t kTileFrom = 64;
 
-// Keys per workgroup of tile_kernel.  A workgroup costs about one tile on top
-// of its own (its first loads, its last stores), and the compute units take
-// the workgroups in rounds; splitting pays a join.
-int64_t tile_chunk(int64_t tiles, int64_t keys) {
-    const int64_t cus = 256, steps = ceil_div(keys, 64);
-    int64_t best = 1, cost = INT64_MAX;
-    for (int64_t s = 1; s <= 16 && s <= ceil_div(steps, 4); ++s) {
-        const int64_t c =
-            ceil_div(tiles * s, cus) * (ceil_div(steps, s) + 1) + (s > 1 ? 4 + s : 0);
-        if (c < cost) {
-            cost = c;
-            best = s;
-        }
-    }
-    return round_up(ceil_div(keys, best), 128);
-}
-
 ctconv_status plan_attention(int64_t B, int64_t Hkv, int64_t R, int64_t D, int64_t span,
                              bool weights, bool tile, ctconv_dtype dt, Plan* p) {
     memset(p, 0, sizeof(*p));

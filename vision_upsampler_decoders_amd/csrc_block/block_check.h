@@ -136,6 +136,23 @@ inline float score_factor(float scale) {
     return c > 1e-30f ? c : 1e-30f;
 }
 
+// Keys per workgroup of tile_kernel.  A workgroup costs about one tile on top
+// of its own (its first loads, its last stores), and the compute units take
+// the workgroups in rounds; splitting pays a join.
+inline int64_t tile_chunk(int64_t tiles, int64_t keys) {
+    const int64_t cus = 256, steps = ceil_div(keys, 64);
+    int64_t best = 1, cost = INT64_MAX;
+    for (int64_t s = 1; s <= 16 && s <= ceil_div(steps, 4); ++s) {
+        const int64_t c =
+            ceil_div(tiles * s, cus) * (ceil_div(steps, s) + 1) + (s > 1 ? 4 + s : 0);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    return round_up(ceil_div(keys, best), 128);
+}
+
 // Keys per workgroup of stream_kernel, and its waves (figures: one query row,
 // keys and values in memory, not in a cache).
 //  - One workgroup per row tile and no join, where few keys or many row tiles

@@ -160,9 +160,12 @@ hipError_t launch_attn_stream(const AttnArgs& a, ctconv_dtype dt, bool paged, hi
 hipError_t launch_attn_tile(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 // The partial results of `splits` workgroups joined, and the slots' weights.
 hipError_t launch_attn_join(const AttnArgs& a, ctconv_dtype dt, bool paged, hipStream_t s);
-// The chunk call with few query rows per key head, the join of its splits and its weights.
+// The chunk call with few query rows per key head and with many (row_tiles: of
+// all sequences), the joins of their splits, and the weights.
 hipError_t launch_chunk_stream(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_chunk_join(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
+hipError_t launch_chunk_tile(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
+hipError_t launch_chunk_tile_join(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_chunk_weights(const AttnArgs& a, ctconv_dtype dt, hipStream_t s);
 hipError_t launch_tables(const TablesArgs& a, hipStream_t s);
 hipError_t launch_rotary(const RotaryArgs& a, ctconv_dtype dt, bool pairs, bool append,

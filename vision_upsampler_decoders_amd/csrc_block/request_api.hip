@@ -14,6 +14,10 @@ namespace {
 
 constexpr int64_t kMostSequences = 8192;  // tables_kernel keeps 16 bytes of each in LDS
 constexpr int64_t kFusedRows = 2048;
+// More query rows per key head than this: tile_kernel.
+constexpr int64_t kTileFrom = 64;
+// Most keys of a workgroup of tile_kernel.
+constexpr int64_t kMostChunk = 16384;
 constexpr double kTwoPi = 6.283185307179586476925;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -48,6 +52,7 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
 }
 
 struct ChunkPlan {
+    bool tile;  // many rows per key head: tile_kernel, else stream_kernel
     bool wide;
     int64_t row_tiles, chunk, splits;
     int64_t part_o_bytes, part_ml_bytes, lse_bytes, bytes;
@@ -65,16 +70,26 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     const int64_t G = Hq / Hkv;
     if ((__int128)n * G > kMaxInt) return CTCONV_ERR_SHAPE;
     const int64_t R = n * G;
-    p->row_tiles = ceil_div(R, 16);
-    const __int128 tiles = (__int128)B * Hkv * p->row_tiles;
+    // (fp32 rows past 512 bytes are too long for its LDS tiles)
+    p->tile = R > kTileFrom && D * (int64_t)esize(dt) <= 512;
+    const int64_t height = p->tile ? 128 : 16;
+    // of all sequences: each may end inside a tile
+    const __int128 all = (__int128)rows * G / 128 + B, most = (__int128)B * ceil_div(R, height);
+    const __int128 row_tiles = p->tile ? (all < most ? all : most) : most;
+    const __int128 tiles = row_tiles * Hkv;
     if (tiles > kMaxInt || (__int128)B * Hkv * R > kMaxInt) return CTCONV_ERR_SHAPE;
-    const int64_t together = n < 16 ? n : 16;  // rows of one tile end up to this far apart
+    p->row_tiles = (int64_t)(p->tile ? row_tiles : ceil_div(R, height));
+    const int64_t together = n < height ? n : height;  // rows of a tile end up to this far apart
     int64_t span = window > 0 && window + together < max_length ? window + together : max_length;
     span = span > 0 ? span : 1;
-    if (tiles >= 2048)
+    if (p->tile) {
+        p->chunk = tile_chunk((int64_t)tiles, span);
+        if (p->chunk > kMostChunk) p->chunk = kMostChunk;
+    } else if (tiles >= 2048) {
         p->chunk = round_up(span, 128);
-    else
+    } else {
         stream_split((int64_t)tiles, span, D, dt, &p->chunk, &p->wide);
+    }
     p->splits = ceil_div(span, p->chunk);
     const __int128 values = (__int128)rows * Hq;
     const __int128 parts = p->splits > 1 ? values * p->splits : 0;
@@ -413,8 +428,10 @@ ctconv_status ctconv_chunk_attention(const void* q, const void* k_cache, const v
     a.part_ml = reinterpret_cast<float*>(at + p.part_o_bytes);
     a.lse2 = weight_sum ? reinterpret_cast<float*>(at + p.part_o_bytes + p.part_ml_bytes) : nullptr;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    st = to_status(launch_chunk_stream(a, dtype, s));
-    if (st == CTCONV_OK && a.splits > 1) st = to_status(launch_chunk_join(a, dtype, s));
+    st = to_status(p.tile ? launch_chunk_tile(a, dtype, s) : launch_chunk_stream(a, dtype, s));
+    if (st == CTCONV_OK && a.splits > 1)
+        st = to_status(p.tile ? launch_chunk_tile_join(a, dtype, s)
+                              : launch_chunk_join(a, dtype, s));
     if (st == CTCONV_OK && weight_sum) st = to_status(launch_chunk_weights(a, dtype, s));
     return st;
 }
