@@ -56,19 +56,23 @@ __device__ inline uint32_t low_bits(int x) {
     return x >= 32 ? 0xFFFFFFFFu : x <= 0 ? 0u : (1u << x) - 1;
 }
 
-// The infinities and NaN of packed values, set to zero; whether there were any.
+// The infinities and NaN of packed values, set to zero; not 0 where there were any.
+// (An exponent of ones is the one that carries into the sign bit.  No compare
+// masks: the tile kernel's scalar registers are full.)
 template <class TR>
-__device__ inline bool take_odd(uint32_t& w) {
+__device__ inline uint32_t take_odd(uint32_t& w) {
+    uint32_t odd;
     if constexpr (std::is_same_v<TR, TF32>) {
-        const bool odd = (w & 0x7F800000u) == 0x7F800000u;
-        w = odd ? 0u : w;
-        return odd;
+        odd = (uint32_t)((int32_t)((w & 0x7FFFFFFFu) + 0x00800000u) >> 31);
     } else {
-        constexpr uint32_t E = std::is_same_v<TR, TBF16> ? 0x7F80u : 0x7C00u;
-        const bool low = (w & E) == E, high = (w >> 16 & E) == E;
-        w &= (low ? 0xFFFF0000u : 0xFFFFFFFFu) & (high ? 0xFFFFu : 0xFFFFFFFFu);
-        return low || high;
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+        constexpr uint16_t one = std::is_same_v<TR, TBF16> ? 0x0080 : 0x0400;
+        const u16x2 t = __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu) + u16x2{one, one};
+        odd = __builtin_bit_cast(uint32_t, (i16x2)(__builtin_bit_cast(i16x2, t) >> (int16_t)15));
     }
+    w &= ~odd;
+    return odd;
 }
 
 // The row tiles of 128 of all sequences, for calls with many rows: those of a

@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kThreads) void chunk_tile_join_kernel(AttnArgs a) {
 template <class TR, int DP>
 hipError_t tile_d(const AttnArgs& a, hipStream_t s) {
     using Sh = Shape<TR, DP>;
-    const size_t lds = Sh::LDS + 4 * Sh::KT * sizeof(int64_t);
+    const size_t lds = Sh::LDS + 4 * Sh::KT * sizeof(int64_t) + sizeof(int);
     const void* fn = a.D == DP ? reinterpret_cast<const void*>(&tile_kernel<TR, DP, true, true>)
                                : reinterpret_cast<const void*>(&tile_kernel<TR, DP, false, true>);
     if (lds > 64u << 10) {

@@ -274,7 +274,7 @@ again:
                 for (int j = 0; j < VK; ++j)
                     if ((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1)
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) odd |= take_odd<TR>(vr[j][w]);
+                        for (int w = 0; w < VW; ++w) odd |= take_odd<TR>(vr[j][w]) != 0;
             }
         }
         f32x4 s[NT];

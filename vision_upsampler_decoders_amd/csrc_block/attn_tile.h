@@ -117,62 +117,6 @@ struct Weights<TF32> {
     f32x16 v;
 };
 
-// The rows of one wave, key by key: lane (col, half) holds the pieces of row col that
-// the matrix instructions take, and its output values.  For sums that are not
-// finite; a value that is not counts whatever small weight its slot has.
-template <class TR, int DP, class Q, class A>
-__device__ void odd_rows(const AttnArgs& a, int b, int slot0, int n, bool live, int begin, int end,
-                         int half, const Q& qf, const typename TR::storage* kb,
-                         const typename TR::storage* vb, A& acc, float& m, float& l) {
-    using S = typename TR::storage;
-    constexpr int VEC = Shape<TR, DP>::VEC, NF = Shape<TR, DP>::NF, ND = Shape<TR, DP>::ND;
-    const auto score = [&](int64_t at) {
-        float dot = 0.f;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int d = (2 * f + half) * VEC;
-            if (d >= a.D) continue;
-            const u32x4 q = qf[f];
-            for (int e = 0; e < VEC; ++e) {
-                S u;
-                if constexpr (sizeof(S) == 2) u = (S)(q[e >> 1] >> (16 * (e & 1)));
-                else u = __uint_as_float(q[e]);
-                dot = fmaf(TR::to_f32(u), TR::to_f32(kb[at + d + e]), dot);
-            }
-        }
-        return (dot + __shfl_xor(dot, 32)) * a.c;
-    };
-    m = -__builtin_huge_valf();
-    l = 0.f;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
-    for (int pass = 0; pass < 2; ++pass) {
-        const float low = m == -__builtin_huge_valf() ? 0.f : m;
-        for (int key = 0; key < n; ++key) {
-            const int64_t at = slot_offset(a.pages, b, slot0 + key);
-            if (at < 0) continue;  // the same for all lanes
-            const float s = score(at);
-            if (!live || key < begin || key >= end) continue;
-            if (pass == 0) {
-                m = fmaxf(m, s);
-                continue;
-            }
-            const float p = exp2_fast(s - low);
-            l += half == 0 ? p : 0.f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at_d = 32 * d + 8 * (i >> 2) + 4 * half + (i & 3);
-                    const float v = at_d < a.D ? TR::to_f32(vb[at + at_d]) : 0.f;
-                    acc[d][i] = fabsf(v) <= __FLT_MAX__ ? fmaf(p, v, acc[d][i]) : acc[d][i] + v;
-                }
-        }
-    }
-}
-
 // EXACT: D = DP (else K pieces past the row are zeroed on their way).
 // CHUNK: the new rows of sequences over the paged cache (see above).
 template <class TR, int DP, bool EXACT, bool CHUNK = false>
@@ -229,10 +173,10 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
     }
     n = n < a.chunk ? n : a.chunk;
 
-    const int row = tile * 128 + wave * 32 + col;
-    const bool live = row < rows;
-    const int lq = live ? (int)fdiv((uint32_t)row, a.fd_G) : 0;
-    const int hq = h * a.G + (live ? row - lq * a.G : 0);
+    int row = tile * 128 + wave * 32 + col;
+    bool live = row < rows;
+    int lq = live ? (int)fdiv((uint32_t)row, a.fd_G) : 0;
+    int hq = h * a.G + (live ? row - lq * a.G : 0);
     // CHUNK: the keys that this lane's row sees; whether the wave has no row at all
     const int my_end = CHUNK ? cr.off + lq + 1 - slot0 : 0;
     const int my_begin = CHUNK && a.window > 0 ? my_end - a.window : 0;
@@ -422,7 +366,31 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
             *reinterpret_cast<u32x4*>(lds + buf + to) = kr[i];
         }
     };
-    const auto store_v = [&](int buf, uint64_t seen) __attribute__((always_inline)) {
+    // CHUNK: a hidden value's weight is 0, but 0 times an infinity or a NaN is NaN.
+    // Tiles that not every row sees whole go without such values; they are added to
+    // the rows that see them at the end.
+    int* const odd_values = reinterpret_cast<int*>(ring + 4 * KT);
+    const auto store_v = [&](int buf, uint64_t seen, int t) __attribute__((always_inline)) {
+        if constexpr (CHUNK)
+            if (t * KT < all_from || t * KT + KT > all_to) {
+                uint32_t odd = 0;
+                if constexpr (ES == 2) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int w = 0; w < VDW; ++w) odd |= take_odd<TR>(vr[VDW * j + w]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < LOADS; ++i)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t u = vr4[i][w];
+                            odd |= take_odd<TR>(u);
+                            vr4[i][w] = u;
+                        }
+                }
+                if (odd) *odd_values = 1;
+            }
         if constexpr (ES == 2) {
             if (seen != ~0ull) {
                 // what an unseen key's row holds may be NaN: zero, not 0 * NaN
@@ -464,23 +432,40 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
     float m = -__builtin_huge_valf(), l = 0.f;
 
-    // LDS offsets of this lane's operands; what else varies is constant
-    uint32_t k_at[NF > 8 ? 8 : NF];
+    // LDS offsets of this lane's operands; what else varies is constant.  Piece f of a
+    // key lies at the first one's offset with bits of f turned, value tile i the
+    // same: CHUNK, which is short of registers, keeps the first ones only.
+    constexpr int KAT = CHUNK ? 1 : NF > 8 ? 8 : NF, VAT = CHUNK && ES == 2 ? 1 : 4;
+    uint32_t k_at[KAT];
 #pragma unroll
-    for (int f = 0; f < (NF > 8 ? 8 : NF); ++f)
+    for (int f = 0; f < KAT; ++f)
         k_at[f] = col * Sh::ROW + (((2 * f + half) ^ (col & 15 & (PIECES - 1))) << 4);
-    uint32_t v_at[4];
+    uint32_t v_at[VAT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < VAT; ++i)
         v_at[i] = ES == 2 ? col * (KT * 2) +
                                 (((2 * i + half) ^ (((col >> 1) ^ (col >> 4)) & 7)) << 4)
                           : 4 * half * Sh::ROW + ((col + (((i ^ half) & 1) << 5)) << 2);
+    // (volatile, or the turned ones are computed ahead of the loop and kept)
+    const auto turned = [](uint32_t at, int f) __attribute__((always_inline)) {
+        uint32_t to;
+        asm volatile("v_xor_b32 %0, %1, %2" : "=v"(to) : "i"(f << 5), "v"(at));
+        return to;
+    };
+    const auto k_piece_at = [&](int f) __attribute__((always_inline)) {
+        if constexpr (CHUNK) return f == 0 ? k_at[0] : turned(k_at[0], f);
+        else return k_at[f];
+    };
+    const auto v_piece_at = [&](int i) __attribute__((always_inline)) {
+        if constexpr (VAT == 1) return i == 0 ? v_at[0] : turned(v_at[0], i);
+        else return v_at[i];
+    };
 
     // Operands and instructions of S_new = K Q^T, piece f of half kh.
     const auto k_piece = [&](int kbuf, int kh, int f) __attribute__((always_inline)) {
         // pieces 8 and up (rows of 512 bytes and more) repeat the pattern of
         // the low four bits 256 bytes on
-        return *reinterpret_cast<const u32x4*>(lds + kbuf + kh * 32 * Sh::ROW + k_at[f & 7] +
+        return *reinterpret_cast<const u32x4*>(lds + kbuf + kh * 32 * Sh::ROW + k_piece_at(f & 7) +
                                                (f >> 3) * 256);
     };
     // Of acc += V^T P^T, i of a half: 16-bit, step i / ND, output tile i % ND;
@@ -491,7 +476,7 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
         // above col move it by 2 d
         const int d = i % ND, st = i / ND;
         return *reinterpret_cast<const u32x4*>(lds + vbuf + d * 32 * (KT * 2) +
-                                               v_at[((2 * vh + st) ^ d) & 3]);
+                                               v_piece_at(((2 * vh + st) ^ d) & 3));
     };
     const auto v_value = [&](int vbuf, int vh, int i) __attribute__((always_inline)) {
         const int d = i % ND, st = i / ND;
@@ -648,13 +633,14 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
                 put_offsets(t);
             }
             ask_page(3);
+            if (tid == 0) *odd_values = 0;
             __syncthreads();
         }
         load_k(0);
         load_v(0);
         bits = CHUNK ? seen_next[0] : seen_keys(0);
         store_k(k_buf(0));
-        store_v(v_buf(0), bits);
+        store_v(v_buf(0), bits, 0);
         if constexpr (ES == 2) {
 #pragma unroll
             for (int i = 0; i < 8 * VDW; ++i) vr[i] = 0;
@@ -664,7 +650,7 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
             for (int i = 0; i < LOADS; ++i) vr4[i] = u32x4{0, 0, 0, 0};
             zero(pb.v);
         }
-        store_v(v_buf(1), ~0ull);  // "tile -1": zeros times zeros
+        store_v(v_buf(1), ~0ull, 0);  // "tile -1": zeros times zeros
         load_k(1);
         load_v(1);
         __syncthreads();
@@ -688,7 +674,7 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
             __syncthreads();
             const uint32_t late = (uint32_t)(bits >> 32);
             bits = CHUNK ? seen_next[0] : seen_keys(t + 1);
-            store_v(v_buf(P ^ 1), bits);
+            store_v(v_buf(P ^ 1), bits, t + 1);
             load_v(t + 2);
             hide(sb, late, t * KT + 32);
             // behind the last tile: scores that are not used
@@ -708,19 +694,49 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
         });
     }
     if constexpr (CHUNK) {
-        // A hidden value's weight is 0, but 0 times an infinity or a NaN is NaN, and
-        // in a sum for good.  A workgroup whose sums are not all finite leaves its
-        // rows to a path that goes by what each row sees.
-        float worst = 0.f;
+        // What was taken out of the values of tiles that not every row sees whole.
+        __syncthreads();
+        if (*odd_values) {
+            // [0, whole_from) and [whole_to, n)
+            const int whole_from = (all_from > 0 ? all_from + KT - 1 : 0) & ~(KT - 1);
+            const int whole_to = all_to & ~(KT - 1);
+            for (int key = 0; key < n; ++key) {
+                if (key == whole_from && whole_to > key) key = whole_to;
+                if (key >= n) break;
+                const int64_t at = slot_offset(a.pages, b, slot0 + key);
+                if (at < 0) continue;
+                const bool sees = key >= my_begin && key < my_end;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) worst += 0.f * acc[d][i];
-        if (__any(worst != 0.f)) {
-            odd_rows<TR, DP>(a, b, slot0, n, live, my_begin, my_end, half, qf, kb, vb, acc, m, l);
+                    for (int i = 0; i < 4; ++i) {
+                        const int at_d = 32 * d + 8 * i;
+                        if (at_d >= a.D) continue;
+                        S v[4];
+                        const S* from = vb + at + at_d + 4 * half;
+                        if constexpr (ES == 2)
+                            *reinterpret_cast<u32x2*>(v) = *reinterpret_cast<const u32x2*>(from);
+                        else
+                            *reinterpret_cast<u32x4*>(v) = *reinterpret_cast<const u32x4*>(from);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = TR::to_f32(v[e]);
+                            acc[d][4 * i + e] += sees && !(fabsf(x) <= __FLT_MAX__) ? x : 0.f;
+                        }
+                    }
+            }
         }
     }
     l += __shfl_xor(l, 32);
+    // CHUNK: the row's numbers again (kept, they would hold registers in the loop)
+    if constexpr (CHUNK) {
+        int here = tile * 128 + (int)threadIdx.x / 64 * 32 + ((int)threadIdx.x & 31);
+        asm volatile("" : "+v"(here));
+        row = here;
+        live = row < rows;
+        lq = live ? (int)fdiv((uint32_t)row, a.fd_G) : 0;
+        hq = h * a.G + (live ? row - lq * a.G : 0);
+    }
     if (!live) return;
     if (direct) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
