@@ -835,10 +835,11 @@ ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_sc
  *                 (slots that no row sees are left as they are); slot_strides
  *                 as in ctconv_cache_append
  * A row that sees nothing gets out = 0 and lse = -infinity.  Infinities and
- * NaN in a slot reach only the rows that see it, an infinite value as such.  16-bit weights meet the
- * values in two parts with up to 64 query rows (n times Hq / Hkv) per key head,
- * rounded to the element type with more.  Workspace, D, heads, scale and
- * max_length as in ctconv_paged_attention.  out must not overlap an input.
+ * NaN in a slot reach only the rows that see it.  16-bit weights meet the
+ * values in two parts with up to 16 query rows (n times Hq / Hkv) per key head;
+ * with more they may be rounded to the element type.  Workspace, D, heads,
+ * scale and max_length as in ctconv_paged_attention.  out must not overlap an
+ * input.
  */
 ctconv_status ctconv_chunk_attention_workspace_bytes(int64_t B, int64_t rows, int64_t n,
                                                      int64_t Hq, int64_t Hkv, int64_t D,

@@ -78,8 +78,9 @@ __device__ inline uint32_t take_odd(uint32_t& w) {
 // The row tiles of 128 of all sequences, for calls with many rows: those of a
 // sequence from the last one down (it sees the most keys), each in the same number
 // of splits, the heads fastest (workgroups go to the XCDs in turn, so that a head's
-// tiles meet its keys in one L2).  False behind the last one.  Called by whole
-// workgroups of `waves` waves.
+// tiles meet its keys in one L2).  False behind the last one.  split_too: item
+// `number` is a split of a tile, else a tile.  Called by whole workgroups of
+// `waves` waves.
 __device__ inline int chunk_splits(const AttnArgs& a, const ChunkRows& r) {
     int span = r.off + r.live;
     // (128 rows lie at most this far apart)
@@ -87,19 +88,18 @@ __device__ inline int chunk_splits(const AttnArgs& a, const ChunkRows& r) {
     span = a.window > 0 && span > most ? most : span;
     return span > a.chunk ? (span + a.chunk - 1) / a.chunk : 1;
 }
-__device__ inline bool chunk_item(const AttnArgs& a, int waves, int& b, int& h, int& tile,
-                                  int& split) {
+__device__ inline bool chunk_item(const AttnArgs& a, int waves, uint32_t number, bool split_too,
+                                  int& b, int& h, int& tile, int& split) {
     __shared__ uint32_t sums[4], found[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint32_t number = block_number();
-    uint32_t target = number / a.Hkv;
+    const uint32_t target = number / a.Hkv;
     h = (int)(number - target * a.Hkv);
     uint32_t before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64 * waves) {
         uint32_t mine = 0;
         if (b0 + tid < a.B) {
             const ChunkRows r = chunk_rows(a, b0 + tid);
-            mine = (uint32_t)((r.live * a.G + 127) >> 7) * chunk_splits(a, r);
+            mine = (uint32_t)((r.live * a.G + 127) >> 7) * (split_too ? chunk_splits(a, r) : 1);
         }
         uint32_t to = mine;
 #pragma unroll
@@ -123,7 +123,7 @@ __device__ inline bool chunk_item(const AttnArgs& a, int waves, int& b, int& h, 
             b = __builtin_amdgcn_readfirstlane((int)found[0]);
             const int at = __builtin_amdgcn_readfirstlane((int)found[1]);
             const ChunkRows r = chunk_rows(a, b);
-            const int splits = chunk_splits(a, r);
+            const int splits = split_too ? chunk_splits(a, r) : 1;
             tile = at / splits;
             split = at - tile * splits;
             tile = ((r.live * a.G + 127) >> 7) - 1 - tile;

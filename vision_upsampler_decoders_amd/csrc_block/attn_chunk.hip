@@ -73,13 +73,19 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(AttnArgs a) {
 // sums of all slots have to be known before any slot can be weighed, so the
 // scores are computed again.  A wave keeps its keys in registers (32 or 64 of
 // them, a key per row of the matrix instruction) and walks the query rows, 32 at a
-// time; a lane adds up its query column and the columns are added at the end.
-template <class TR, int DP>
-__global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int key_blocks) {
+// time, the next ones on their way; a lane adds up its query column and the
+// columns are added at the end.  The waves of a workgroup take keys of their own and
+// the same rows (which they then find in the L1 cache), or, where that would leave
+// compute units idle (apart), the same keys and every fourth rows.
+template <class TR, int DP, bool EXACT>
+__global__ __launch_bounds__(kThreads, DP * sizeof(typename TR::storage) > 512 ? 1 : 2) void
+chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
     using S = typename TR::storage;
     constexpr int ES = sizeof(S), VEC = 16 / ES;
     constexpr int NF = DP / (2 * VEC);
-    constexpr int KG = NF <= 16 ? 2 : 1;  // groups of 32 keys of a wave
+    constexpr int KG = NF <= 8 ? 2 : 1;  // groups of 32 keys of a wave
+    constexpr bool AHEAD = EXACT || NF != 16;  // (registers for the next rows)
+    __shared__ float parts[kWaves][KG * 32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
     const uint32_t number = block_number();
@@ -87,7 +93,7 @@ __global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int
     const int h = (int)(number % a.Hkv), bk = (int)(number / a.Hkv);
     const int b = bk / key_blocks, kb = bk - b * key_blocks;
     const ChunkRows cr = chunk_rows(a, b);
-    const int key0 = (kb * kWaves + wave) * KG * 32, key_end = key0 + KG * 32;
+    const int key0 = (apart ? kb : kb * kWaves + wave) * KG * 32, key_end = key0 + KG * 32;
     // rows that see some of the keys
     int lo = key0 - cr.off;
     lo = lo > 0 ? lo : 0;
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int
         const int64_t most = (int64_t)key_end - 1 - cr.off + a.window;
         hi = most < hi ? (int)most : hi;
     }
-    if (lo >= hi) return;
+    if (lo >= hi) return;  // (apart: for all waves)
 
     u32x4 kf[KG][NF];
     bool there[KG];
@@ -110,7 +116,11 @@ __global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int
         for (int f = 0; f < NF; ++f) {
             const int d = (2 * f + half) * VEC;
             kf[g][f] = u32x4{0, 0, 0, 0};
-            if (there[g] && d < a.D) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
+            if (there[g] && (EXACT || d < a.D)) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
+            // the sign of the scale (the keys' pieces past a row stay 0)
+            const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kf[g][f][i] ^= flip;
         }
     }
     f32x16 sum[KG];
@@ -118,44 +128,62 @@ __global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int
     for (int g = 0; g < KG; ++g)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[g][i] = 0.f;
-    const S* qb = static_cast<const S*>(a.q) + (a.row_starts ? cr.row0 * a.q_row : b * a.q_b);
-    const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+    const S* qb = static_cast<const S*>(a.q) + (a.row_starts ? cr.row0 * a.q_row : b * a.q_b) +
+                  (int64_t)(h * a.G) * a.q_head;
     const float* lse2 = a.lse2 + cr.row0 * a.Hq + h * a.G;
-    const int r_end = hi * a.G;
-    for (int r0 = lo * a.G; r0 < r_end; r0 += 32) {
-        const int r = r0 + col;
-        const bool live = r < r_end;
-        const int lq = live ? (int)fdiv((uint32_t)r, a.fd_G) : 0;
-        const int hq = live ? r - lq * a.G : 0;
-        const S* qr = qb + lq * a.q_row + (int64_t)(h * a.G + hq) * a.q_head;
-        u32x4 qf[NF];
+    const int r_end = hi * a.G, step = apart ? 32 * kWaves : 32;
+    u32x4 next[NF];
+    float next_low;
+    int next_end;
+    // Rows past the last one are read as that one and weigh nothing.
+    const auto load = [&](int r0) __attribute__((always_inline)) {
+        const int r = r0 + col < r_end ? r0 + col : r_end - 1;
+        const int lq = (int)fdiv((uint32_t)r, a.fd_G), hq = r - lq * a.G;
+        const S* qr = qb + lq * a.q_row + hq * a.q_head;
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
             const int d = (2 * f + half) * VEC;
-            qf[f] = u32x4{0, 0, 0, 0};
-            if (live && d < a.D) qf[f] = *reinterpret_cast<const u32x4*>(qr + d);
+            next[f] = *reinterpret_cast<const u32x4*>(qr + (EXACT || d < a.D ? d : 0));
         }
-        const float low = live ? lse2[(int64_t)lq * a.Hq + hq] : __builtin_huge_valf();
-        const int end = cr.off + lq + 1, begin = a.window > 0 ? end - a.window : 0;
-        const bool whole = __all(!live || (begin <= key0 && end >= key_end));
+        next_low = lse2[(int64_t)lq * a.Hq + hq];
+        if (r0 + col >= r_end) next_low = __builtin_huge_valf();
+        next_end = cr.off + lq + 1;
+    };
+    int r0 = lo * a.G + (apart ? 32 * wave : 0);
+    if (AHEAD && r0 < r_end) load(r0);
+    for (; r0 < r_end; r0 += step) {
+        if (!AHEAD) load(r0);
+        u32x4 qf[NF];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) qf[f] = next[f];
+        const float low = next_low;
+        const int end = next_end, begin = a.window > 0 ? end - a.window : 0;
+        if (AHEAD && r0 + step < r_end) load(r0 + step);
+        const bool whole = __all(begin <= key0 && end >= key_end);
+        f32x16 s[KG];
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[g][i] = 0.f;
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[f][i] ^= flip;
+            for (int g = 0; g < KG; ++g) Mma32<TR>::step(s[g], kf[g][f], qf[f]);
+        if (whole) {
 #pragma unroll
-        for (int g = 0; g < KG; ++g) {
-            f32x16 s;
+            for (int g = 0; g < KG; ++g)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = 0.f;
+                for (int i = 0; i < 16; ++i) sum[g][i] += exp2_fast(fmaf(s[g][i], a.c, -low));
+        } else {
 #pragma unroll
-            for (int f = 0; f < NF; ++f) Mma32<TR>::step(s, kf[g][f], qf[f]);
+            for (int g = 0; g < KG; ++g)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int t = key0 + 32 * g + 8 * (i >> 2) + 4 * half + (i & 3);
-                float p = exp2_fast(fmaf(s[i], a.c, -low));
-                if (!whole && (t >= end || t < begin)) p = 0.f;
-                sum[g][i] += p;
-            }
+                for (int i = 0; i < 16; ++i) {
+                    // a hidden slot gets nothing, whatever the row's sum is
+                    const int t = key0 + 32 * g + 8 * (i >> 2) + 4 * half + (i & 3);
+                    const float p = exp2_fast(fmaf(s[g][i], a.c, -low));
+                    sum[g][i] += t < end && t >= begin ? p : 0.f;
+                }
         }
     }
 #pragma unroll
@@ -164,24 +192,25 @@ __global__ __launch_bounds__(kThreads) void chunk_weights_kernel(AttnArgs a, int
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[g][i] += __shfl_xor(sum[g][i], o);
-        // a key's place in the registers and its lane are not the same: lane
-        // 8 (i / 4) + 4 half + i % 4 of a half holds key i
+        // lane i of a half writes key 8 (i / 4) + 4 half + i % 4
         float mine = 0.f;
-        int slot = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (col == i) {
-                mine = sum[g][i];
-                slot = 8 * (i >> 2) + 4 * half + (i & 3);
-            }
-        const uint64_t pages = __ballot(there[g]);  // lane = key, both halves the same
-        const int t = key0 + 32 * g + slot;
-        // seen by some row: not past the last one's end, nor before the first one's window
-        const int64_t from = a.window > 0 ? (int64_t)cr.off + 1 - a.window : 0;
-        if (col < 16 && ((pages >> slot) & 1) && t < cr.off + cr.live && t >= from) {
-            float* w = a.weight_sum + b * a.slot_b + h * a.slot_h + t;
-            *w += mine;
-        }
+        for (int i = 0; i < 16; ++i) mine = col == i ? sum[g][i] : mine;
+        if (col < 16) parts[wave][32 * g + 8 * (col >> 2) + 4 * half + (col & 3)] = mine;
+    }
+    if (apart) __syncthreads();
+    if (apart && wave > 0) return;
+    asm volatile("" ::: "memory");  // (a wave's own LDS writes and reads are in order)
+    // slots that some row sees: not past the last one's end, nor before the first one's window
+    const int64_t from = a.window > 0 ? (int64_t)cr.off + 1 - a.window : 0;
+#pragma unroll
+    for (int g = 0; g < KG; ++g) {
+        const int t = key0 + 32 * g + col;
+        if (half != 0 || !there[g] || t >= cr.off + cr.live || t < from) continue;
+        float add = parts[wave][32 * g + col];
+        if (apart)
+            for (int w = 1; w < kWaves; ++w) add += parts[w][32 * g + col];
+        a.weight_sum[b * a.slot_b + h * a.slot_h + t] += add;
     }
 }
 
@@ -219,11 +248,16 @@ hipError_t chunk_d(const AttnArgs& a, hipStream_t s) {
 template <class TR, int DP>
 hipError_t weights_d(const AttnArgs& a, hipStream_t s) {
     constexpr int NF = DP * (int)sizeof(typename TR::storage) / 32;
-    constexpr int keys = kWaves * 32 * (NF <= 16 ? 2 : 1);
-    const int key_blocks = (a.pages.slots + keys - 1) / keys;
-    if (key_blocks == 0) return hipSuccess;
-    chunk_weights_kernel<TR, DP><<<grid_of((int64_t)a.B * a.Hkv * key_blocks), dim3(kThreads), 0, s>>>(
-        a, key_blocks);
+    constexpr int keys = 32 * (NF <= 8 ? 2 : 1);
+    const int64_t blocks = ((int64_t)a.pages.slots + keys - 1) / keys;
+    if (blocks == 0) return hipSuccess;
+    const int apart = (int64_t)a.B * a.Hkv * blocks < 512 * kWaves;
+    const int key_blocks = (int)(apart ? blocks : (blocks + kWaves - 1) / kWaves);
+    const dim3 grid = grid_of((int64_t)a.B * a.Hkv * key_blocks);
+    if (a.D == DP)
+        chunk_weights_kernel<TR, DP, true><<<grid, dim3(kThreads), 0, s>>>(a, key_blocks, apart);
+    else
+        chunk_weights_kernel<TR, DP, false><<<grid, dim3(kThreads), 0, s>>>(a, key_blocks, apart);
     return hipGetLastError();
 }
 

@@ -13,13 +13,16 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kAtOnce = 4;  // splits of a row whose loads are in flight together
 
-// Join, a workgroup per row tile and head: D / 4 lanes add a row's splits in
-// ascending order.  Tiles of one split have written their results already.
+constexpr int kJoins = 8;   // workgroups of a row tile in the join
+
+// Join: D / 4 lanes add a row's splits in ascending order.  Tiles of one split
+// have written their results already.
 template <class TR>
 __global__ __launch_bounds__(kThreads) void chunk_tile_join_kernel(AttnArgs a) {
     using S = typename TR::storage;
     int b, h, tile, split;
-    if (!chunk_item(a, kThreads / 64, b, h, tile, split) || split > 0) return;
+    const uint32_t number = block_number();
+    if (!chunk_item(a, kThreads / 64, number / kJoins, false, b, h, tile, split)) return;
     const ChunkRows cr = chunk_rows(a, b);
     const int R = cr.live * a.G, row0 = tile * 128;
     const int last = row0 + 127 < R ? row0 + 127 : R - 1;
@@ -31,7 +34,10 @@ __global__ __launch_bounds__(kThreads) void chunk_tile_join_kernel(AttnArgs a) {
     const int pieces = a.D / 4, together = kThreads / pieces;
     const int grp = threadIdx.x / pieces, d = (threadIdx.x - grp * pieces) * 4;
     if (grp >= together) return;
-    for (int row = row0 + grp; row <= last; row += together) {
+    constexpr int kRows = 128 / kJoins;
+    const int from = row0 + (int)(number % kJoins) * kRows;
+    const int to = from + kRows - 1 < last ? from + kRows - 1 : last;
+    for (int row = from + grp; row <= to; row += together) {
         const int lq = (int)fdiv((uint32_t)row, a.fd_G), hq = h * a.G + (row - lq * a.G);
         const int64_t at = (cr.row0 + lq) * a.Hq + hq, p0 = at * a.splits;
         const float* ml = a.part_ml + 2 * p0;
@@ -67,14 +73,14 @@ __global__ __launch_bounds__(kThreads) void chunk_tile_join_kernel(AttnArgs a) {
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        S* to = static_cast<S*>(a.out) + (a.row_starts ? cr.row0 * a.o_row : b * a.o_b) +
-                lq * a.o_row + (int64_t)hq * a.o_head + d;
+        S* out = static_cast<S*>(a.out) + (a.row_starts ? cr.row0 * a.o_row : b * a.o_b) +
+                 lq * a.o_row + (int64_t)hq * a.o_head + d;
         if constexpr (sizeof(S) == 2) {
             u32x2 w{mfma::pack2<TR>(o[0] * inv, o[1] * inv),
                     mfma::pack2<TR>(o[2] * inv, o[3] * inv)};
-            *reinterpret_cast<u32x2*>(to) = w;
+            *reinterpret_cast<u32x2*>(out) = w;
         } else {
-            *reinterpret_cast<f32x4*>(to) = o * inv;
+            *reinterpret_cast<f32x4*>(out) = o * inv;
         }
         if (d == 0) write_lse(a, at, top, sum);
     }
@@ -109,7 +115,7 @@ hipError_t tile_t(const AttnArgs& a, hipStream_t s) {
 template <class TR>
 hipError_t join_t(const AttnArgs& a, hipStream_t s) {
     chunk_tile_join_kernel<TR>
-        <<<grid_of((int64_t)a.row_tiles * a.splits * a.Hkv), dim3(kThreads), 0, s>>>(a);
+        <<<grid_of((int64_t)a.row_tiles * a.Hkv * kJoins), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 

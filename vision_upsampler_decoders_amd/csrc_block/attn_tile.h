@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
     int all_from = 0, all_to = 0;      // CHUNK: the keys that every row of the tile sees
     bool direct = a.direct;
     if constexpr (CHUNK) {
-        if (!chunk_item(a, kThreads / 64, b, h, tile, split)) return;
+        if (!chunk_item(a, kThreads / 64, block_number(), true, b, h, tile, split)) return;
         bh = 0;
         cr = chunk_rows(a, b);
         rows = cr.live * a.G;

@@ -14,10 +14,17 @@ namespace {
 
 constexpr int64_t kMostSequences = 8192;  // tables_kernel keeps 16 bytes of each in LDS
 constexpr int64_t kFusedRows = 2048;
-// More query rows per key head than this: tile_kernel.
-constexpr int64_t kTileFrom = 64;
-// Most keys of a workgroup of tile_kernel.
-constexpr int64_t kMostChunk = 16384;
+// Whether R query rows per key head of `heads` sequences' key heads go to tile_kernel
+// (128 rows that share their keys in LDS), else stream_kernel (keys read once per 16
+// rows).  32 heads on 8, D = 128, us in stream_kernel and in tile_kernel: bf16, 24
+// sequences of 8192 keys, 16 rows 168 and 180, 32 rows 242 and 184, 64 rows 488 and
+// 195; one of 65536, 32 rows 91 and 141, 64 rows 169 and 146.  fp32, whose matrix
+// unit is what takes the time: 24 of 8192, 64 rows 920 and 986, 128 rows 1806 and
+// 1005; one of 65536, 128 rows 600 and 645.
+bool many_rows(int64_t R, int64_t heads, ctconv_dtype dt) {
+    if (dt == CTCONV_F32) return R > 64;
+    return R > 32 || (R > 16 && heads >= 128);
+}
 constexpr double kTwoPi = 6.283185307179586476925;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -51,6 +58,41 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
     a->fd_half = make_fastdiv((uint32_t)a->half);
 }
 
+// Keys per workgroup of tile_kernel, of at most `tiles` row tiles whose rows see at
+// most `keys` each, on a chip that holds `slots` workgroups.
+//  - A split costs the writing, reading and joining of partial rows: 19 k rows of 32
+//    heads over up to 8192 keys take 1565 us whole and 2160 in chunks of 4096.  So,
+//    in steps of 64 keys: the rounds of workgroups, two steps of each to start and
+//    end, and 1/90 of a step per tile for the partial rows (D = 128).
+//  - Of several sequences the lengths may differ, and the longest one's tiles are the
+//    last to end: twice as many workgroups as fill the chip (8 x 64 rows of 32 heads
+//    over up to 32768 keys: 186 us in chunks of 4096, 286 in chunks of 8192, but 426
+//    and 399 where all are that long), of 1024 keys at least.
+//  - So may their rows, where there are fewer than half of n per sequence: one that
+//    goes on by a row has the keys of a tile of 128 rows.  47 such and one of 2048
+//    rows over up to 16384 keys: 411 us in chunks of 4096, 479 of 8192, 636 whole.
+int64_t chunk_keys(int64_t tiles, int64_t keys, int64_t slots, bool several, bool uneven) {
+    const int64_t steps = ceil_div(keys, 64), n = tiles > 0 ? tiles : 1;
+    int64_t best = 1, cost = INT64_MAX;
+    for (int64_t s = 1; s <= 16 && s <= ceil_div(steps, 8); ++s) {
+        const int64_t c = ceil_div(n * s, slots) * (ceil_div(steps, s) + 2) +
+                          (s > 1 ? 4 + n * s / 90 : 0);
+        if (c < cost) {
+            cost = c;
+            best = s;
+        }
+    }
+    int64_t more = 1;
+    if (several && n < slots) more = 2 * slots / n;
+    if (several && uneven) {
+        const int64_t s = 8 * slots / n < 8 ? 8 * slots / n : 8;
+        more = s > more ? s : more;
+    }
+    const int64_t most = ceil_div(keys, 1024);
+    more = more < most ? more : most;
+    return round_up(ceil_div(keys, more > best ? more : best), 128);
+}
+
 struct ChunkPlan {
     bool tile;  // many rows per key head: tile_kernel, else stream_kernel
     bool wide;
@@ -71,7 +113,7 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     if ((__int128)n * G > kMaxInt) return CTCONV_ERR_SHAPE;
     const int64_t R = n * G;
     // (fp32 rows past 512 bytes are too long for its LDS tiles)
-    p->tile = R > kTileFrom && D * (int64_t)esize(dt) <= 512;
+    p->tile = many_rows(R, B * Hkv, dt) && D * (int64_t)esize(dt) <= 512;
     const int64_t height = p->tile ? 128 : 16;
     // of all sequences: each may end inside a tile
     const __int128 all = (__int128)rows * G / 128 + B, most = (__int128)B * ceil_div(R, height);
@@ -83,8 +125,10 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     int64_t span = window > 0 && window + together < max_length ? window + together : max_length;
     span = span > 0 ? span : 1;
     if (p->tile) {
-        p->chunk = tile_chunk((int64_t)tiles, span);
-        if (p->chunk > kMostChunk) p->chunk = kMostChunk;
+        // as tile_d and Shape have it: two workgroups per compute unit where LDS holds them
+        const int64_t width = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+        const int64_t slots = width * (int64_t)esize(dt) <= 256 ? 512 : 256;
+        p->chunk = chunk_keys((int64_t)tiles, span, slots, B > 1, rows * 2 <= B * n);
     } else if (tiles >= 2048) {
         p->chunk = round_up(span, 128);
     } else {
