@@ -73,19 +73,22 @@ __global__ __launch_bounds__(kThreads) void chunk_join_kernel(AttnArgs a) {
 // sums of all slots have to be known before any slot can be weighed, so the
 // scores are computed again.  A wave keeps its keys in registers (32 or 64 of
 // them, a key per row of the matrix instruction) and walks the query rows, 32 at a
-// time, the next ones on their way; a lane adds up its query column and the
-// columns are added at the end.  The waves of a workgroup take keys of their own and
-// the same rows (which they then find in the L1 cache), or, where that would leave
-// compute units idle (apart), the same keys and every fourth rows.
-template <class TR, int DP, bool EXACT>
+// time; a lane adds up its query column and the columns are added at the end.  The
+// rows go through LDS: read straight to the instruction's lanes, 16 bytes of each
+// of 32 rows at a time, they keep the load unit busy for longer than the matrix
+// instructions take.  The waves of a workgroup take keys of their own and the same
+// rows, or, where that would leave compute units idle (APART), the same keys and
+// every fourth rows.
+template <class TR, int DP, bool EXACT, bool APART>
 __global__ __launch_bounds__(kThreads, DP * sizeof(typename TR::storage) > 512 ? 1 : 2) void
-chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
+chunk_weights_kernel(AttnArgs a, int key_blocks) {
     using S = typename TR::storage;
     constexpr int ES = sizeof(S), VEC = 16 / ES;
-    constexpr int NF = DP / (2 * VEC);
+    constexpr int NF = DP / (2 * VEC), PIECES = DP / VEC, ROW = DP * ES, TILE = 32 * ROW;
     constexpr int KG = NF <= 8 ? 2 : 1;  // groups of 32 keys of a wave
-    constexpr bool AHEAD = EXACT || NF != 16;  // (registers for the next rows)
-    __shared__ float parts[kWaves][KG * 32];
+    constexpr int LOADERS = APART ? 64 : kThreads, LOADS = TILE / 16 / LOADERS;
+    static_assert(LOADERS % PIECES == 0, "a thread moves the same piece of every row");
+    extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
     const uint32_t number = block_number();
@@ -93,16 +96,17 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
     const int h = (int)(number % a.Hkv), bk = (int)(number / a.Hkv);
     const int b = bk / key_blocks, kb = bk - b * key_blocks;
     const ChunkRows cr = chunk_rows(a, b);
-    const int key0 = (apart ? kb : kb * kWaves + wave) * KG * 32, key_end = key0 + KG * 32;
-    // rows that see some of the keys
-    int lo = key0 - cr.off;
+    constexpr int KEYS = KG * 32 * (APART ? 1 : kWaves);  // of the workgroup
+    const int key0 = kb * KEYS + (APART ? 0 : wave * KG * 32), key_end = key0 + KG * 32;
+    // rows that see some of the workgroup's keys
+    int lo = kb * KEYS - cr.off;
     lo = lo > 0 ? lo : 0;
     int hi = cr.live;
     if (a.window > 0) {
-        const int64_t most = (int64_t)key_end - 1 - cr.off + a.window;
+        const int64_t most = (int64_t)(kb + 1) * KEYS - 1 - cr.off + a.window;
         hi = most < hi ? (int)most : hi;
     }
-    if (lo >= hi) return;  // (apart: for all waves)
+    if (lo >= hi) return;
 
     u32x4 kf[KG][NF];
     bool there[KG];
@@ -117,7 +121,7 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
             const int d = (2 * f + half) * VEC;
             kf[g][f] = u32x4{0, 0, 0, 0};
             if (there[g] && (EXACT || d < a.D)) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
-            // the sign of the scale (the keys' pieces past a row stay 0)
+            // the sign of the scale
             const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) kf[g][f][i] ^= flip;
@@ -131,34 +135,60 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
     const S* qb = static_cast<const S*>(a.q) + (a.row_starts ? cr.row0 * a.q_row : b * a.q_b) +
                   (int64_t)(h * a.G) * a.q_head;
     const float* lse2 = a.lse2 + cr.row0 * a.Hq + h * a.G;
-    const int r_end = hi * a.G, step = apart ? 32 * kWaves : 32;
-    u32x4 next[NF];
-    float next_low;
-    int next_end;
+    const int r_first = lo * a.G + (APART ? 32 * wave : 0), r_end = hi * a.G;
+    constexpr int STEP = APART ? 32 * kWaves : 32;
     // Rows past the last one are read as that one and weigh nothing.
-    const auto load = [&](int r0) __attribute__((always_inline)) {
-        const int r = r0 + col < r_end ? r0 + col : r_end - 1;
-        const int lq = (int)fdiv((uint32_t)r, a.fd_G), hq = r - lq * a.G;
-        const S* qr = qb + lq * a.q_row + hq * a.q_head;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int d = (2 * f + half) * VEC;
-            next[f] = *reinterpret_cast<const u32x4*>(qr + (EXACT || d < a.D ? d : 0));
-        }
-        next_low = lse2[(int64_t)lq * a.Hq + hq];
-        if (r0 + col >= r_end) next_low = __builtin_huge_valf();
-        next_end = cr.off + lq + 1;
+    const auto row_of = [&](int r, int& lq, int& hq) __attribute__((always_inline)) {
+        r = r < r_end ? r : r_end - 1;
+        lq = (int)fdiv((uint32_t)r, a.fd_G);
+        hq = r - lq * a.G;
     };
-    int r0 = lo * a.G + (apart ? 32 * wave : 0);
-    if (AHEAD && r0 < r_end) load(r0);
-    for (; r0 < r_end; r0 += step) {
-        if (!AHEAD) load(r0);
-        u32x4 qf[NF];
+    char* const mine = lds + (APART ? wave * 2 * TILE : 0);
+    const int loader = APART ? lane : tid, piece = loader % PIECES, first = loader / PIECES;
+    u32x4 moved[LOADS];
+    float low_next = 0.f;
+    int end_next = 0;
+    const auto load = [&](int r0) __attribute__((always_inline)) {
+        int lq, hq;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) qf[f] = next[f];
-        const float low = next_low;
-        const int end = next_end, begin = a.window > 0 ? end - a.window : 0;
-        if (AHEAD && r0 + step < r_end) load(r0 + step);
+        for (int i = 0; i < LOADS; ++i) {
+            row_of(r0 + first + i * (LOADERS / PIECES), lq, hq);
+            const int d = piece * VEC;
+            moved[i] = *reinterpret_cast<const u32x4*>(qb + lq * a.q_row + hq * a.q_head +
+                                                       (EXACT || d < a.D ? d : 0));
+        }
+    };
+    const auto load_low = [&](int r0) __attribute__((always_inline)) {
+        int lq, hq;
+        row_of(r0 + col, lq, hq);
+        low_next = lse2[(int64_t)lq * a.Hq + hq];
+        if (r0 + col >= r_end) low_next = __builtin_huge_valf();
+        end_next = cr.off + lq + 1;
+    };
+    // piece c of row r at c ^ (r % 16)
+    const auto store = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = first + i * (LOADERS / PIECES);
+            *reinterpret_cast<u32x4*>(mine + buf * TILE + r * ROW +
+                                      ((piece ^ (r & 15 & (PIECES - 1))) << 4)) = moved[i];
+        }
+    };
+    // (a wave's own LDS writes and reads are in order)
+    const auto meet = [] __attribute__((always_inline)) {
+        if constexpr (APART) asm volatile("" ::: "memory");
+        else __syncthreads();
+    };
+    load(r_first);
+    load_low(r_first);
+    store(0);
+    load(r_first + STEP);
+    meet();
+    int buf = 0;
+    for (int r0 = r_first; r0 < r_end; r0 += STEP, buf ^= 1) {
+        const float low = low_next;
+        const int end = end_next, begin = a.window > 0 ? end - a.window : 0;
+        load_low(r0 + STEP);
         const bool whole = __all(begin <= key0 && end >= key_end);
         f32x16 s[KG];
 #pragma unroll
@@ -166,9 +196,15 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[g][i] = 0.f;
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int f = 0; f < NF; ++f) {
+            const u32x4 qf = *reinterpret_cast<const u32x4*>(
+                mine + buf * TILE + col * ROW + (((2 * f + half) ^ (col & 15 & (PIECES - 1))) << 4));
 #pragma unroll
-            for (int g = 0; g < KG; ++g) Mma32<TR>::step(s[g], kf[g][f], qf[f]);
+            for (int g = 0; g < KG; ++g) Mma32<TR>::step(s[g], kf[g][f], qf);
+        }
+        // (read last an iteration ago)
+        store(buf ^ 1);
+        load(r0 + 2 * STEP);
         if (whole) {
 #pragma unroll
             for (int g = 0; g < KG; ++g)
@@ -185,7 +221,10 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
                     sum[g][i] += t < end && t >= begin ? p : 0.f;
                 }
         }
+        meet();
     }
+    __syncthreads();  // (the rows are no longer read)
+    float* parts = reinterpret_cast<float*>(lds) + wave * KG * 32;
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
 #pragma unroll
@@ -193,23 +232,22 @@ chunk_weights_kernel(AttnArgs a, int key_blocks, int apart) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[g][i] += __shfl_xor(sum[g][i], o);
         // lane i of a half writes key 8 (i / 4) + 4 half + i % 4
-        float mine = 0.f;
+        float one = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mine = col == i ? sum[g][i] : mine;
-        if (col < 16) parts[wave][32 * g + 8 * (col >> 2) + 4 * half + (col & 3)] = mine;
+        for (int i = 0; i < 16; ++i) one = col == i ? sum[g][i] : one;
+        if (col < 16) parts[32 * g + 8 * (col >> 2) + 4 * half + (col & 3)] = one;
     }
-    if (apart) __syncthreads();
-    if (apart && wave > 0) return;
-    asm volatile("" ::: "memory");  // (a wave's own LDS writes and reads are in order)
+    __syncthreads();
+    if (APART && wave > 0) return;
     // slots that some row sees: not past the last one's end, nor before the first one's window
     const int64_t from = a.window > 0 ? (int64_t)cr.off + 1 - a.window : 0;
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
         const int t = key0 + 32 * g + col;
         if (half != 0 || !there[g] || t >= cr.off + cr.live || t < from) continue;
-        float add = parts[wave][32 * g + col];
-        if (apart)
-            for (int w = 1; w < kWaves; ++w) add += parts[w][32 * g + col];
+        float add = parts[32 * g + col];
+        if (APART)
+            for (int w = 1; w < kWaves; ++w) add += parts[w * KG * 32 + 32 * g + col];
         a.weight_sum[b * a.slot_b + h * a.slot_h + t] += add;
     }
 }
@@ -245,20 +283,34 @@ hipError_t chunk_d(const AttnArgs& a, hipStream_t s) {
     return chunk_w<TR, DP, 4>(a, lds(4), s);
 }
 
+template <class TR, int DP, bool APART>
+hipError_t weights_a(const AttnArgs& a, int key_blocks, hipStream_t s) {
+    const void* fn =
+        a.D == DP ? reinterpret_cast<const void*>(&chunk_weights_kernel<TR, DP, true, APART>)
+                  : reinterpret_cast<const void*>(&chunk_weights_kernel<TR, DP, false, APART>);
+    const size_t lds = 2 * 32 * DP * sizeof(typename TR::storage) * (APART ? kWaves : 1);
+    if (lds > 64u << 10) {
+        const hipError_t e =
+            hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    AttnArgs args = a;
+    void* params[] = {&args, &key_blocks};
+    return hipLaunchKernel(fn, grid_of((int64_t)a.B * a.Hkv * key_blocks), dim3(kThreads), params,
+                           lds, s);
+}
+
 template <class TR, int DP>
 hipError_t weights_d(const AttnArgs& a, hipStream_t s) {
     constexpr int NF = DP * (int)sizeof(typename TR::storage) / 32;
     constexpr int keys = 32 * (NF <= 8 ? 2 : 1);
     const int64_t blocks = ((int64_t)a.pages.slots + keys - 1) / keys;
     if (blocks == 0) return hipSuccess;
-    const int apart = (int64_t)a.B * a.Hkv * blocks < 512 * kWaves;
-    const int key_blocks = (int)(apart ? blocks : (blocks + kWaves - 1) / kWaves);
-    const dim3 grid = grid_of((int64_t)a.B * a.Hkv * key_blocks);
-    if (a.D == DP)
-        chunk_weights_kernel<TR, DP, true><<<grid, dim3(kThreads), 0, s>>>(a, key_blocks, apart);
-    else
-        chunk_weights_kernel<TR, DP, false><<<grid, dim3(kThreads), 0, s>>>(a, key_blocks, apart);
-    return hipGetLastError();
+    // (fp32 rows of 1 KB: the tiles of four waves do not fit LDS)
+    if constexpr (NF <= 16)
+        if ((int64_t)a.B * a.Hkv * blocks < 512 * kWaves)
+            return weights_a<TR, DP, true>(a, (int)blocks, s);
+    return weights_a<TR, DP, false>(a, (int)((blocks + kWaves - 1) / kWaves), s);
 }
 
 template <class TR>
