@@ -137,33 +137,61 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
     const float* lse2 = a.lse2 + cr.row0 * a.Hq + h * a.G;
     const int r_first = lo * a.G + (APART ? 32 * wave : 0), r_end = hi * a.G;
     constexpr int STEP = APART ? 32 * kWaves : 32;
-    // Rows past the last one are read as that one and weigh nothing.
-    const auto row_of = [&](int r, int& lq, int& hq) __attribute__((always_inline)) {
-        r = r < r_end ? r : r_end - 1;
-        lq = (int)fdiv((uint32_t)r, a.fd_G);
-        hq = r - lq * a.G;
+    // Each lane steps from row to row by additions (row r is row r / G of the
+    // sequence, head r % G).  Rows past the last one are read as that one and weigh
+    // nothing.
+    const int by_row = (int)fdiv((uint32_t)STEP, a.fd_G), by_head = STEP - by_row * a.G;
+    const int64_t q_step = by_row * a.q_row + by_head * a.q_head;
+    const int64_t q_turn = a.q_row - a.G * a.q_head;
+    struct Walk {
+        int row, head;
+    };
+    const auto start = [&](int r) __attribute__((always_inline)) {
+        const int row = (int)fdiv((uint32_t)r, a.fd_G);
+        return Walk{row, r - row * a.G};
     };
     char* const mine = lds + (APART ? wave * 2 * TILE : 0);
     const int loader = APART ? lane : tid, piece = loader % PIECES, first = loader / PIECES;
+    const S* const q_piece = qb + (EXACT || piece * VEC < a.D ? piece * VEC : 0);
     u32x4 moved[LOADS];
+    int q_head[LOADS];
+    const S* q_at[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const Walk w = start(r_first + first + i * (LOADERS / PIECES));
+        q_head[i] = w.head;
+        q_at[i] = q_piece + w.row * a.q_row + w.head * a.q_head;
+    }
+    const Walk end_row = start(r_end - 1), my_row = start(r_first + col);
+    const S* const q_last = q_piece + end_row.row * a.q_row + end_row.head * a.q_head;
+    int low_head = my_row.head, low_row = my_row.row;
     float low_next = 0.f;
     int end_next = 0;
     const auto load = [&](int r0) __attribute__((always_inline)) {
-        int lq, hq;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            row_of(r0 + first + i * (LOADERS / PIECES), lq, hq);
-            const int d = piece * VEC;
-            moved[i] = *reinterpret_cast<const u32x4*>(qb + lq * a.q_row + hq * a.q_head +
-                                                       (EXACT || d < a.D ? d : 0));
+            const bool is = r0 + first + i * (LOADERS / PIECES) < r_end;
+            moved[i] = *reinterpret_cast<const u32x4*>(is ? q_at[i] : q_last);
+            q_head[i] += by_head;
+            q_at[i] += q_step;
+            if (q_head[i] >= a.G) {
+                q_head[i] -= a.G;
+                q_at[i] += q_turn;
+            }
         }
     };
     const auto load_low = [&](int r0) __attribute__((always_inline)) {
-        int lq, hq;
-        row_of(r0 + col, lq, hq);
-        low_next = lse2[(int64_t)lq * a.Hq + hq];
-        if (r0 + col >= r_end) low_next = __builtin_huge_valf();
-        end_next = cr.off + lq + 1;
+        const bool is = r0 + col < r_end;
+        const int row = is ? low_row : end_row.row, head = is ? low_head : end_row.head;
+        low_next = lse2[(int64_t)row * a.Hq + head];
+        if (!is) low_next = __builtin_huge_valf();
+        end_next = cr.off + row + 1;
+        low_head += by_head;
+        low_row += by_row;
+        if (low_head >= a.G) {
+            low_head -= a.G;
+            ++low_row;
+        }
     };
     // piece c of row r at c ^ (r % 16)
     const auto store = [&](int buf) __attribute__((always_inline)) {
@@ -205,22 +233,24 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
         // (read last an iteration ago)
         store(buf ^ 1);
         load(r0 + 2 * STEP);
-        if (whole) {
 #pragma unroll
-            for (int g = 0; g < KG; ++g)
+        for (int g = 0; g < KG; ++g)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sum[g][i] += exp2_fast(fmaf(s[g][i], a.c, -low));
-        } else {
+            for (int i = 0; i < 16; ++i) s[g][i] = exp2_fast(fmaf(s[g][i], a.c, -low));
+        if (!whole) {
 #pragma unroll
             for (int g = 0; g < KG; ++g)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     // a hidden slot gets nothing, whatever the row's sum is
                     const int t = key0 + 32 * g + 8 * (i >> 2) + 4 * half + (i & 3);
-                    const float p = exp2_fast(fmaf(s[g][i], a.c, -low));
-                    sum[g][i] += t < end && t >= begin ? p : 0.f;
+                    s[g][i] = t < end && t >= begin ? s[g][i] : 0.f;
                 }
         }
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[g][i] += s[g][i];
         meet();
     }
     __syncthreads();  // (the rows are no longer read)
