@@ -6,7 +6,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from block_ref import E, U, attend, slot_rows
+from block_ref import E, U, slot_rows
 
 
 def clamp(v, lo, hi):
@@ -85,6 +85,30 @@ def turned(x, positions, frequencies, layout, scale, dt):
     return y, bound
 
 
+def seen_rows(q, k, v, seen, scale, dt):
+    """Attention of rows q [M, D] to k, v [n, D] where seen [M, n]: (out, lse, p) and their bounds,
+    those of block_ref.attend row by row."""
+    M, D = q.shape
+    count = seen.sum(1)
+    s = np.where(seen, scale * (q @ k.T), -np.inf)
+    size = np.where(seen, np.abs(q) @ np.abs(k).T, 0.0)
+    ds = (D + 4) * E * abs(scale) * (size.max(1) if k.shape[0] else np.zeros(M))
+    top = s.max(1, initial=-np.inf)
+    ex = np.exp(s - np.where(np.isinf(top), 0.0, top)[:, None])
+    tot = ex.sum(1)
+    p = ex / np.where(tot == 0, 1.0, tot)[:, None]
+    with np.errstate(divide="ignore"):
+        lse = top + np.log(tot)
+    out = p @ v
+    dp = 2 * ds + (count + 32) * E
+    rnd = 0.0 if dt == "f32" else U[dt]
+    big = np.array([np.abs(v[r]).max(0) if r.any() else np.zeros(D) for r in seen]).reshape(M, D)
+    tiny = count[:, None] * 2.0 ** -25 * big / np.where(tot == 0, 1.0, tot)[:, None] if dt == "f16" else 0.0
+    b_out = U[dt] * np.abs(out) + (dp + rnd + count * E)[:, None] * (p @ np.abs(v)) + tiny + 1e-30
+    b_lse = np.where(count > 0, dp + 4 * E * np.abs(np.where(count > 0, lse, 0)) + 4 * E, 0.0)
+    return (out, lse, p), (b_out, b_lse, dp[:, None] * p + 2.0 ** -126)
+
+
 def chunk(q, kc, vc, table, lengths, counts, page, window, scale, dt, max_length=None):
     """q: a list of [counts[b], Hq, D], caches [P, H, page, D]: lists of (out, lse) and bounds per
     sequence, added weights [B, H, slots] and their bound."""
@@ -99,19 +123,20 @@ def chunk(q, kc, vc, table, lengths, counts, page, window, scale, dt, max_length
         L = clamp(lengths[b], 0, most)
         out, lse = np.zeros((n, Hq, D)), np.full((n, Hq), -np.inf)
         bo, bl = np.zeros((n, Hq, D)), np.zeros((n, Hq))
-        for i in range(n):
-            end = L - int(counts[b]) + i + 1
-            at = np.arange(max(0, end - window) if window else 0, max(end, 0))
-            for h in range(H):
-                r = slice(h * G, (h + 1) * G)
-                kr, ok = slot_rows(kc, table, page, b, h, at)
-                vr, _ = slot_rows(vc, table, page, b, h, at)
-                (o, l, p), (eo, el, ep) = attend(q[b][i, r], kr[ok], vr[ok], scale, dt)
-                out[i, r], lse[i, r], bo[i, r], bl[i, r] = o, l, eo, el
+        at = np.arange(L)
+        end = L - int(counts[b]) + np.arange(n)[:, None] + 1
+        seen = (at[None, :] < end) & (at[None, :] >= (end - window if window else 0))
+        for h in range(H):
+            kr, ok = slot_rows(kc, table, page, b, h, at)
+            vr, _ = slot_rows(vc, table, page, b, h, at)
+            for j in range(h * G, (h + 1) * G):
+                (o, l, p), (eo, el, ep) = seen_rows(q[b][:, j], kr[ok], vr[ok], seen[:, ok], scale, dt)
+                out[:, j], lse[:, j], bo[:, j], bl[:, j] = o, l, eo, el
                 # the weights are taken again, against a rounded log2 of the sum
                 with np.errstate(divide="ignore"):
-                    arg = np.where(p > 0, np.abs(np.log2(p)), 0)
-                again = (1.5 * np.abs(l)[:, None] + arg + 8) * E if len(p[0]) else 0
+                    arg = np.where(p > 0, np.abs(np.log2(np.where(p > 0, p, 1.0))), 0)
+                level = np.where(np.isinf(l), 0.0, np.abs(l))
+                again = (1.5 * level[:, None] + arg + 8) * E
                 w[b, h, at[ok]] += p.sum(0)
                 wb[b, h, at[ok]] += (ep + again * p).sum(0)
         res.append((out, lse, bo, bl))

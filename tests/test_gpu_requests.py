@@ -326,6 +326,23 @@ CHUNK = [
     ([70], [40], 70, 2, 1, 64, 16, 0, "library"),  # rows before the first slot see nothing
 ]
 
+# Enough rows and heads that the tiled kernel is the faster one (the times that the planner
+# compares, in us: 8 + rounds of 64-key steps at 0.9 to 9 each against 10 + a 16-row tile's keys
+# and values at 6.5 GB/ms, over all row tiles).
+MANY = [
+    ([330, 329], [330, 420], 330, 8, 8, 128, 16, 0, "library"),
+    ([700, 1, 0, 257], [700, 1500, 5, 900], 700, 16, 4, 64, 24, 0, "slots"),
+    ([500, 3], [1500, 1601], 500, 12, 4, 96, 7, 200, "both"),
+    ([601], [700], 601, 24, 8, 80, 64, 0, "library"),
+    ([300, 190], [420, 190], 300, 18, 6, 256, 8, 0, "slots"),
+    ([400], [1000], 400, 32, 4, 200, 1, 64, "library"),
+    ([900, 65], [903, 3000], 900, 7, 7, 32, 256, 0, "library"),
+    ([800], [790], 800, 8, 8, 40, 16, 0, "library"),
+    ([17] * 24, [1100 + 10 * i for i in range(24)], 17, 16, 8, 128, 16, 0, "library"),
+    ([200], [1600], 200, 32, 8, 128, 32, 0, "library"),
+    ([210, 3], [1700, 1500], 210, 32, 8, 96, 16, 1200, "slots"),
+]
+
 
 def chunk_inputs(rng, case, dt, cols=None):
     counts, lengths, n, Hq, H, D, page, window, order = case
@@ -348,7 +365,7 @@ def compare(got, lse, ref, what):
 
 
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("case", CHUNK, ids=[str(i) for i in range(len(CHUNK))])
+@pytest.mark.parametrize("case", CHUNK + MANY, ids=[str(i) for i in range(len(CHUNK + MANY))])
 @pytest.mark.parametrize("weights", [False, True])
 def test_chunk_attention(cc, case, dt, weights):  # noqa: F811
     import torch
@@ -393,28 +410,29 @@ def test_chunk_attention(cc, case, dt, weights):  # noqa: F811
 
 
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("n", [6, 90])
-def test_chunk_attention_missing_pages_and_long_lengths(cc, dt, n):  # noqa: F811
+@pytest.mark.parametrize("n,Hq,H,extra", [(6, 4, 2, 0), (90, 4, 2, 0), (150, 32, 16, 992)])
+def test_chunk_attention_missing_pages_and_long_lengths(cc, dt, n, Hq, H, extra):  # noqa: F811
     """Table entries outside the pool, lengths outside the table, a negative scale, strided rows
     of q and out, a bound max_length, row starts outside the rows."""
     import torch
 
     say(f"chunk missing pages {dt} n={n}")
-    B, Hq, H, D, page = 5, 4, 2, 64, 16
+    B, D, page = 5, 64, 16
+    cap = 160 + extra
     rng = np.random.default_rng(5)
-    c = Cache(rng, B, H, D, page, np.full(B, 160), dt)
+    c = Cache(rng, B, H, D, page, np.full(B, cap), dt)
     c.table[0, 3], c.table[2, 0], c.table[2, 9] = -1, -2 ** 31, 2 ** 31 - 1
     c.table[1, :] = 10 ** 6
     td = ints(c.table)
-    given = np.array([160, 160, 2 ** 31 - 1, -5, 161], np.int32)
+    given = np.array([cap, cap, 2 ** 31 - 1, -5, cap + 1], np.int32)
     counts = [n, n - 1, n, 2, n]
     big, b64 = dev(rng.standard_normal((B, n, 3 * Hq, D)), dt)
     q = big[:, :, Hq:2 * Hq]
     q64 = [b64[b, :counts[b], Hq:2 * Hq] for b in range(B)]
-    for most in (160, 150):
+    for most in (cap, cap - 10):
         ref, w, wb = Q.chunk(q64, c.k, c.v, c.table, given, counts, page, 0, -0.1, dt, most)
         wide = torch.full((B, n, 2 * Hq, D), 9.0, dtype=q.dtype, device="cuda")
-        wd = torch.zeros(B, H, 160, device="cuda")
+        wd = torch.zeros(B, H, cap, device="cuda")
         _, lse = cc.chunk_attention(q, c.kd, c.vd, td, ints(given), counts=ints(counts),
                                     max_length=most, scale=-0.1, weight_sum=wd,
                                     out=wide[:, :, Hq:])
@@ -428,22 +446,24 @@ def test_chunk_attention_missing_pages_and_long_lengths(cc, dt, n):  # noqa: F81
     flat = q[0].contiguous()
     starts = ints([-n, 0, n, n + 5, 2 ** 31 - 1, -2 ** 31])
     out = torch.full_like(flat, 9.0)
-    cc.chunk_attention(flat, c.kd, c.vd, ints(np.roll(c.table, 1, 0)), ints([160] * B),
+    cc.chunk_attention(flat, c.kd, c.vd, ints(np.roll(c.table, 1, 0)), ints([cap] * B),
                        row_starts=starts, n=n, scale=-0.1, out=out)
     torch.cuda.synchronize()
-    ref, _, _ = Q.chunk([to_host(flat)], c.k, c.v, c.table[:1], [160], [n], page, 0, -0.1, dt)
+    ref, _, _ = Q.chunk([to_host(flat)], c.k, c.v, c.table[:1], [cap], [n], page, 0, -0.1, dt)
     R.check(to_host(out), ref[0][0], ref[0][2], "first only")
 
 
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("n,G,window", [(7, 2, 0), (9, 1, 4), (100, 1, 0), (40, 4, 0), (90, 2, 20)])
+@pytest.mark.parametrize("n,G,window", [(7, 2, 0), (9, 1, 4), (100, 1, 0), (40, 4, 0), (90, 2, 20),
+                                        (700, 16, 0), (900, 16, 150)])
 def test_chunk_attention_odd_values_reach_only_who_sees_them(cc, dt, n, G, window):  # noqa: F811
     """Infinities and NaN in keys and values of new slots: rows before them are as without."""
     import torch
 
     say(f"chunk odd values {dt} n={n} G={G} window={window}")
     rng = np.random.default_rng(n)
-    D, page, L, H = 64, 16, 200, 1
+    D, page, H = 64, 16, 1
+    L = n + 100
     c = Cache(rng, 1, H, D, page, [L], dt)
     q, starts, q64 = packed([rng.standard_normal((n, G * H, D))], 0, dt)
     ref, _, _ = Q.chunk(q64, c.k, c.v, c.table, [L], [n], page, window, 0.1, dt)

@@ -121,10 +121,6 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
             const int d = (2 * f + half) * VEC;
             kf[g][f] = u32x4{0, 0, 0, 0};
             if (there[g] && (EXACT || d < a.D)) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
-            // the sign of the scale
-            const uint32_t flip = a.negate ? (ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kf[g][f][i] ^= flip;
         }
     }
     f32x16 sum[KG];
@@ -135,6 +131,7 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
     const S* qb = static_cast<const S*>(a.q) + (a.row_starts ? cr.row0 * a.q_row : b * a.q_b) +
                   (int64_t)(h * a.G) * a.q_head;
     const float* lse2 = a.lse2 + cr.row0 * a.Hq + h * a.G;
+    const float c = a.negate ? -a.c : a.c;
     const int r_first = lo * a.G + (APART ? 32 * wave : 0), r_end = hi * a.G;
     constexpr int STEP = APART ? 32 * kWaves : 32;
     // Each lane steps from row to row by additions (row r is row r / G of the
@@ -236,7 +233,7 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
 #pragma unroll
         for (int g = 0; g < KG; ++g)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[g][i] = exp2_fast(fmaf(s[g][i], a.c, -low));
+            for (int i = 0; i < 16; ++i) s[g][i] = exp2_fast(fmaf(s[g][i], c, -low));
         if (!whole) {
 #pragma unroll
             for (int g = 0; g < KG; ++g)

@@ -14,17 +14,6 @@ namespace {
 
 constexpr int64_t kMostSequences = 8192;  // tables_kernel keeps 16 bytes of each in LDS
 constexpr int64_t kFusedRows = 2048;
-// Whether R query rows per key head of `heads` sequences' key heads go to tile_kernel
-// (128 rows that share their keys in LDS), else stream_kernel (keys read once per 16
-// rows).  32 heads on 8, D = 128, us in stream_kernel and in tile_kernel: bf16, 24
-// sequences of 8192 keys, 16 rows 168 and 180, 32 rows 242 and 184, 64 rows 488 and
-// 195; one of 65536, 32 rows 91 and 141, 64 rows 169 and 146.  fp32, whose matrix
-// unit is what takes the time: 24 of 8192, 64 rows 920 and 986, 128 rows 1806 and
-// 1005; one of 65536, 128 rows 600 and 645.
-bool many_rows(int64_t R, int64_t heads, ctconv_dtype dt) {
-    if (dt == CTCONV_F32) return R > 64;
-    return R > 32 || (R > 16 && heads >= 128);
-}
 constexpr double kTwoPi = 6.283185307179586476925;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -58,12 +47,33 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
     a->fd_half = make_fastdiv((uint32_t)a->half);
 }
 
-// Keys per workgroup of tile_kernel, of at most `tiles` row tiles whose rows see at
-// most `keys` each, on a chip that holds `slots` workgroups.
-//  - A split costs the writing, reading and joining of partial rows: 19 k rows of 32
-//    heads over up to 8192 keys take 1565 us whole and 2160 in chunks of 4096.  So,
-//    in steps of 64 keys: the rounds of workgroups, two steps of each to start and
-//    end, and 1/90 of a step per tile for the partial rows (D = 128).
+// The two kernels' times in ns, as far as the host can tell, for the choice between
+// them and the splits.  tile_kernel: rounds of the workgroups that the chip holds, a
+// step per 64 keys and two to start and end, and for split tiles the partial rows,
+// written and read (19 k rows of 32 heads over up to 8192 keys take 1565 us whole
+// and 2160 in chunks of 4096), and the join.  stream_kernel: keys and values once
+// per 16 rows, and workgroups without work where sequences have fewer rows than n.
+// Measured against it (us, stream and tile; 32 heads on 8, D = 128): bf16, 24
+// sequences of 8192 keys, 16 rows per key head 168 and 180, 32 rows 242 and 184, 64
+// rows 488 and 195; one of 8192, 32 rows 23 and 31, 128 rows 52 and 35.  fp32, 24 of
+// 8192, 64 rows 920 and 986, 128 rows 1806 and 1005; one of 8192, 128 rows 91 and 104.
+double tile_time(double tiles, double keys, double splits, int64_t D, ctconv_dtype dt) {
+    const bool f32 = dt == CTCONV_F32;
+    // two workgroups share a compute unit up to 256 bytes a row; a step of both
+    const bool pair = D * (int64_t)esize(dt) <= 256;
+    double step = f32 ? (pair ? 8500 : 9000) : D <= 64 ? 1500 : D <= 128 ? 2300 : 4500;
+    if (pair && tiles * splits <= 256) step *= 0.6;
+    const double rounds = ceil(tiles * splits / (pair ? 512 : 256));
+    double t = 8000 + rounds * (ceil(ceil(keys / 64) / splits) + 2) * step;
+    if (splits > 1) t += 6000 + tiles * splits * 128 * (double)D * 8 / 5000;
+    return t;
+}
+double stream_time(double tiles, double padded, double keys, int64_t D, ctconv_dtype dt) {
+    return 10000 + tiles * keys * 2 * (double)(D * (int64_t)esize(dt)) / 6500 +
+           padded * ceil(keys / 512) * 2;
+}
+
+// Splits of tile_kernel's row tiles, at least two steps of keys each.
 //  - Of several sequences the lengths may differ, and the longest one's tiles are the
 //    last to end: twice as many workgroups as fill the chip (8 x 64 rows of 32 heads
 //    over up to 32768 keys: 186 us in chunks of 4096, 286 in chunks of 8192, but 426
@@ -71,14 +81,16 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
 //  - So may their rows, where there are fewer than half of n per sequence: one that
 //    goes on by a row has the keys of a tile of 128 rows.  47 such and one of 2048
 //    rows over up to 16384 keys: 411 us in chunks of 4096, 479 of 8192, 636 whole.
-int64_t chunk_keys(int64_t tiles, int64_t keys, int64_t slots, bool several, bool uneven) {
-    const int64_t steps = ceil_div(keys, 64), n = tiles > 0 ? tiles : 1;
-    int64_t best = 1, cost = INT64_MAX;
-    for (int64_t s = 1; s <= 16 && s <= ceil_div(steps, 8); ++s) {
-        const int64_t c = ceil_div(n * s, slots) * (ceil_div(steps, s) + 2) +
-                          (s > 1 ? 4 + n * s / 90 : 0);
-        if (c < cost) {
-            cost = c;
+int64_t tile_splits(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, bool several,
+                    bool uneven) {
+    const int64_t n = tiles > 0 ? tiles : 1, steps = ceil_div(keys, 64);
+    const int64_t slots = D * (int64_t)esize(dt) <= 256 ? 512 : 256;
+    int64_t best = 1;
+    double cost = HUGE_VAL;
+    for (int64_t s = 1; s <= 64 && s <= ceil_div(steps, 2); ++s) {
+        const double t = tile_time((double)n, (double)keys, (double)s, D, dt);
+        if (t < cost) {
+            cost = t;
             best = s;
         }
     }
@@ -90,7 +102,7 @@ int64_t chunk_keys(int64_t tiles, int64_t keys, int64_t slots, bool several, boo
     }
     const int64_t most = ceil_div(keys, 1024);
     more = more < most ? more : most;
-    return round_up(ceil_div(keys, more > best ? more : best), 128);
+    return more > best ? more : best;
 }
 
 struct ChunkPlan {
@@ -113,31 +125,42 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     if ((__int128)n * G > kMaxInt) return CTCONV_ERR_SHAPE;
     const int64_t R = n * G;
     // (fp32 rows past 512 bytes are too long for its LDS tiles)
-    p->tile = many_rows(R, B * Hkv, dt) && D * (int64_t)esize(dt) <= 512;
-    const int64_t height = p->tile ? 128 : 16;
-    // of all sequences: each may end inside a tile
-    const __int128 all = (__int128)rows * G / 128 + B, most = (__int128)B * ceil_div(R, height);
-    const __int128 row_tiles = p->tile ? (all < most ? all : most) : most;
-    const __int128 tiles = row_tiles * Hkv;
-    if (tiles > kMaxInt || (__int128)B * Hkv * R > kMaxInt) return CTCONV_ERR_SHAPE;
-    p->row_tiles = (int64_t)(p->tile ? row_tiles : ceil_div(R, height));
-    const int64_t together = n < height ? n : height;  // rows of a tile end up to this far apart
-    int64_t span = window > 0 && window + together < max_length ? window + together : max_length;
-    span = span > 0 ? span : 1;
-    if (p->tile) {
-        // as tile_d and Shape have it: two workgroups per compute unit where LDS holds them
-        const int64_t width = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-        const int64_t slots = width * (int64_t)esize(dt) <= 256 ? 512 : 256;
-        p->chunk = chunk_keys((int64_t)tiles, span, slots, B > 1, rows * 2 <= B * n);
-    } else if (tiles >= 2048) {
-        p->chunk = round_up(span, 128);
-    } else {
-        stream_split((int64_t)tiles, span, D, dt, &p->chunk, &p->wide);
+    // row tiles of all sequences: each may end inside one
+    const auto tiles_of = [&](int64_t height) {
+        const __int128 all = (__int128)rows * G / height + B, most = (__int128)B * ceil_div(R, height);
+        return (all < most ? all : most) * Hkv;
+    };
+    // keys that the rows of one tile see together
+    const auto span_of = [&](int64_t height) {
+        const int64_t together = n < height ? n : height;
+        const int64_t s = window > 0 && window + together < max_length ? window + together
+                                                                       : max_length;
+        return s > 0 ? s : 1;
+    };
+    const __int128 padded = (__int128)B * Hkv * ceil_div(R, 16);
+    if (tiles_of(16) > kMaxInt || padded > kMaxInt || (__int128)B * Hkv * R > kMaxInt)
+        return CTCONV_ERR_SHAPE;
+    // (fp32 rows past 512 bytes are too long for the tile kernel's LDS)
+    const int64_t tiles = (int64_t)tiles_of(128);
+    int64_t span = span_of(128);
+    if (R > 16 && D * (int64_t)esize(dt) <= 512) {
+        const int64_t splits = tile_splits(tiles, span, D, dt, B > 1, rows * 2 <= B * n);
+        p->tile = tile_time((double)tiles, (double)span, (double)splits, D, dt) <
+                  stream_time((double)tiles_of(16), (double)padded, (double)span_of(16), D, dt);
+        p->chunk = round_up(ceil_div(span, splits), 128);
+        p->row_tiles = tiles / Hkv;
+    }
+    if (!p->tile) {
+        p->row_tiles = ceil_div(R, 16);
+        span = span_of(16);
+        if (padded >= 2048) p->chunk = round_up(span, 128);
+        else stream_split((int64_t)padded, span, D, dt, &p->chunk, &p->wide);
     }
     p->splits = ceil_div(span, p->chunk);
     const __int128 values = (__int128)rows * Hq;
     const __int128 parts = p->splits > 1 ? values * p->splits : 0;
-    if (tiles * p->splits > kMaxInt - 8 || parts * D > ((__int128)1 << 59) ||
+    const __int128 groups = (p->tile ? (__int128)tiles : padded) * p->splits;
+    if (groups > kMaxInt - 8 || parts * D > ((__int128)1 << 59) ||
         values > ((__int128)1 << 59))
         return CTCONV_ERR_SHAPE;
     p->part_o_bytes = (int64_t)parts * D * 4;
