@@ -18,6 +18,7 @@ namespace block {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kAtOnce = 4;
 constexpr int kRowThreads = 256;
 constexpr uint32_t kMost = INT32_MAX;
 
@@ -63,7 +64,7 @@ __device__ inline void map_row(const TablesArgs& a, const uint32_t* ends, int r)
 
 __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
     extern __shared__ __align__(16) uint32_t lds[];
-    __shared__ uint32_t sums[3][kWaves], found[2][kWaves];
+    __shared__ uint32_t sums[3][kWaves], found[2][kAtOnce][kWaves];
     uint32_t *need = lds, *back = lds + a.B, *grow = back + a.B, *rows = grow + a.B;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int slots = a.max_pages * a.page_size;
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             uint32_t s = before[i];
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = 0; w < kWaves && b0 + 64 * w < a.B; ++w) {
                 if (w == wave) v[i] = add(v[i], s);
                 s = add(s, sums[i][w]);
             }
@@ -115,34 +116,57 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
         __syncthreads();
     }
 
-    // given back, pages only, in order
+    // given back, pages only, in order: kAtOnce entries of a thread on their way together
     const uint32_t given = before[0], taken = before[1];
-    for (uint32_t e0 = 0, turn = 0; e0 < given; e0 += kThreads, turn ^= 1) {
-        const uint32_t e = e0 + tid;
-        int page = -1;
-        if (e < given) {
-            const int b = sequence_of(back, a.B, e);
-            page = a.table[b * a.table_stride + need[b] + (e - (b > 0 ? back[b - 1] : 0))];
+    for (uint32_t e0 = 0, turn = 0; e0 < given; e0 += kAtOnce * kThreads, turn ^= 1) {
+        int page[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const uint32_t e = e0 + k * kThreads + tid;
+            page[k] = -1;
+            if (e < given) {
+                const int b = sequence_of(back, a.B, e);
+                page[k] = a.table[b * a.table_stride + need[b] + (e - (b > 0 ? back[b - 1] : 0))];
+            }
         }
-        const bool is = page >= 0 && page < a.num_pages;
-        const uint64_t votes = __ballot(is);
-        if (lane == 0) found[turn][wave] = __popcll(votes);
+        uint64_t votes[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            votes[k] = __ballot(page[k] >= 0 && page[k] < a.num_pages);
+            if (lane == 0) found[turn][k][wave] = __popcll(votes[k]);
+        }
         __syncthreads();
-        int at = top;
-        for (int w = 0; w < kWaves; ++w) {
-            const int n = (int)found[turn][w];
-            if (w < wave) at += n;
-            top += n;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (e0 + k * kThreads >= given) break;
+            int at = top;
+            for (int w = 0; w < kWaves; ++w) {
+                const int n = (int)found[turn][k][w];
+                if (w < wave) at += n;
+                top += n;
+            }
+            at += __popcll(votes[k] & ((1ull << lane) - 1));
+            if ((votes[k] >> lane & 1) && at < a.num_pages) a.free_pages[at] = page[k];
+            top = top < a.num_pages ? top : a.num_pages;
         }
-        at += __popcll(votes & ((1ull << lane) - 1));
-        if (is && at < a.num_pages) a.free_pages[at] = page;
-        top = top < a.num_pages ? top : a.num_pages;
     }
     if (given > 0) __syncthreads();
-    for (uint32_t e = tid; e < taken; e += kThreads) {
-        const int page = e < (uint32_t)top ? a.free_pages[top - 1 - (int)e] : -1;
-        const int b = sequence_of(grow, a.B, e);
-        a.table[b * a.table_stride + (need[b] - (grow[b] - e))] = page;
+    for (uint32_t e0 = 0; e0 < taken; e0 += kAtOnce * kThreads) {
+        int page[kAtOnce];
+        int32_t* to[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const uint32_t e = e0 + k * kThreads + tid;
+            page[k] = -1;
+            to[k] = nullptr;
+            if (e >= taken) continue;
+            if (e < (uint32_t)top) page[k] = a.free_pages[top - 1 - (int)e];
+            const int b = sequence_of(grow, a.B, e);
+            to[k] = a.table + b * a.table_stride + (need[b] - (grow[b] - e));
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            if (to[k]) *to[k] = page[k];
     }
     for (int b = tid; b < a.B; b += kThreads) {
         const uint32_t first = b > 0 ? grow[b - 1] : 0, wanted = grow[b] - first;
