@@ -108,21 +108,6 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
     }
     if (lo >= hi) return;
 
-    u32x4 kf[KG][NF];
-    bool there[KG];
-#pragma unroll
-    for (int g = 0; g < KG; ++g) {
-        const int t = key0 + 32 * g + col;
-        const int64_t o = t < cr.len ? slot_offset(a.pages, b, t) : -1;
-        there[g] = o >= 0;
-        const S* kr = static_cast<const S*>(a.k) + h * a.pages.head_stride + (o >= 0 ? o : 0);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int d = (2 * f + half) * VEC;
-            kf[g][f] = u32x4{0, 0, 0, 0};
-            if (there[g] && (EXACT || d < a.D)) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
-        }
-    }
     f32x16 sum[KG];
 #pragma unroll
     for (int g = 0; g < KG; ++g)
@@ -206,6 +191,27 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
     };
     load(r_first);
     load_low(r_first);
+    // slots that some row sees: not past the last one's end, nor before the first one's window
+    const int64_t from = a.window > 0 ? (int64_t)cr.off + 1 - a.window : 0;
+    float* const weights = a.weight_sum + b * a.slot_b + h * a.slot_h + key0 + col;
+    u32x4 kf[KG][NF];
+    bool there[KG], added[KG];
+    float old[KG];
+#pragma unroll
+    for (int g = 0; g < KG; ++g) {
+        const int t = key0 + 32 * g + col;
+        const int64_t o = t < cr.len ? slot_offset(a.pages, b, t) : -1;
+        there[g] = o >= 0;
+        added[g] = there[g] && t < cr.off + cr.live && t >= from;
+        old[g] = added[g] ? weights[32 * g] : 0.f;
+        const S* kr = static_cast<const S*>(a.k) + h * a.pages.head_stride + (o >= 0 ? o : 0);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int d = (2 * f + half) * VEC;
+            kf[g][f] = u32x4{0, 0, 0, 0};
+            if (there[g] && (EXACT || d < a.D)) kf[g][f] = *reinterpret_cast<const u32x4*>(kr + d);
+        }
+    }
     store(0);
     load(r_first + STEP);
     meet();
@@ -254,28 +260,32 @@ chunk_weights_kernel(AttnArgs a, int key_blocks) {
     float* parts = reinterpret_cast<float*>(lds) + wave * KG * 32;
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
+        // Each step adds up what two lanes hold of one half of the values and leaves
+        // them a half each: lane col ends with value i.
+        int i = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int n = 8; n > 0; n >>= 1) {
+            const bool upper = col & (2 * n);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[g][i] += __shfl_xor(sum[g][i], o);
-        // lane i of a half writes key 8 (i / 4) + 4 half + i % 4
-        float one = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) one = col == i ? sum[g][i] : one;
-        if (col < 16) parts[32 * g + 8 * (col >> 2) + 4 * half + (col & 3)] = one;
+            for (int j = 0; j < n; ++j) {
+                const float give = upper ? sum[g][j] : sum[g][j + n];
+                const float keep = upper ? sum[g][j + n] : sum[g][j];
+                sum[g][j] = keep + __shfl_xor(give, 2 * n);
+            }
+            i += upper ? n : 0;
+        }
+        const float one = sum[g][0] + __shfl_xor(sum[g][0], 1);
+        if ((col & 1) == 0) parts[32 * g + 8 * (i >> 2) + 4 * half + (i & 3)] = one;
     }
     __syncthreads();
-    if (APART && wave > 0) return;
-    // slots that some row sees: not past the last one's end, nor before the first one's window
-    const int64_t from = a.window > 0 ? (int64_t)cr.off + 1 - a.window : 0;
+    if ((APART && wave > 0) || half != 0) return;
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
-        const int t = key0 + 32 * g + col;
-        if (half != 0 || !there[g] || t >= cr.off + cr.live || t < from) continue;
+        if (!added[g]) continue;
         float add = parts[32 * g + col];
         if (APART)
             for (int w = 1; w < kWaves; ++w) add += parts[w * KG * 32 + 32 * g + col];
-        a.weight_sum[b * a.slot_b + h * a.slot_h + t] += add;
+        weights[32 * g] = old[g] + add;
     }
 }
 
