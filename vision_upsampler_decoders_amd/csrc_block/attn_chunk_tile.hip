@@ -86,12 +86,13 @@ __global__ __launch_bounds__(kThreads) void chunk_tile_join_kernel(AttnArgs a) {
     }
 }
 
-template <class TR, int DP>
+template <class TR, int DP, int DU = DP>
 hipError_t tile_d(const AttnArgs& a, hipStream_t s) {
-    using Sh = Shape<TR, DP>;
+    using Sh = Shape<TR, DP, DU>;
     const size_t lds = Sh::LDS + 4 * Sh::KT * sizeof(int64_t) + sizeof(int);
-    const void* fn = a.D == DP ? reinterpret_cast<const void*>(&tile_kernel<TR, DP, true, true>)
-                               : reinterpret_cast<const void*>(&tile_kernel<TR, DP, false, true>);
+    const void* fn = reinterpret_cast<const void*>(&tile_kernel<TR, DP, false, true, DU>);
+    if constexpr (DU == DP)
+        if (a.D == DP) fn = reinterpret_cast<const void*>(&tile_kernel<TR, DP, true, true>);
     if (lds > 64u << 10) {
         const hipError_t e =
             hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -105,7 +106,9 @@ hipError_t tile_d(const AttnArgs& a, hipStream_t s) {
 
 template <class TR>
 hipError_t tile_t(const AttnArgs& a, hipStream_t s) {
+    if (a.D <= 32) return tile_d<TR, 64, 32>(a, s);
     if (a.D <= 64) return tile_d<TR, 64>(a, s);
+    if (a.D <= 96) return tile_d<TR, 128, 96>(a, s);
     if (a.D <= 128) return tile_d<TR, 128>(a, s);
     // fp32 rows of 1 KB: two tiles of K and of V do not fit LDS
     if constexpr (sizeof(typename TR::storage) == 2) return tile_d<TR, 256>(a, s);

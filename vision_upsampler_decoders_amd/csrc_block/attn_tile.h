@@ -82,7 +82,8 @@ template <>
 constexpr float kTopWeight<TF16> = 5.f;
 constexpr int kAhead = 4;  // LDS operands read ahead of their instruction
 
-template <class TR, int DP>
+// DP: values of a row in LDS; DU of them are used (a multiple of 32).
+template <class TR, int DP, int DU = DP>
 struct Shape {
     static constexpr int ES = sizeof(typename TR::storage);
     static constexpr int VEC = 16 / ES;
@@ -91,8 +92,8 @@ struct Shape {
     static constexpr int BYTES = KT * ROW;              // of a tile of K, or of V
     static constexpr int LDS = 4 * BYTES;
     static constexpr int PER_CU = LDS > (80 << 10) ? 1 : 2;  // workgroups per compute unit
-    static constexpr int NF = DP / (2 * VEC);           // 16-byte pieces of a key per half
-    static constexpr int ND = DP / 32;                  // output tiles
+    static constexpr int NF = DU / (2 * VEC);           // 16-byte pieces of a key per half
+    static constexpr int ND = DU / 32;                  // output tiles
     static constexpr int PIECES = DP / VEC;             // 16-byte pieces of a row
     static constexpr int LOADS = BYTES / (16 * kThreads);
     static constexpr int VD = ES == 2 ? DP / 32 : 1;    // 16-bit: value columns per thread
@@ -119,10 +120,10 @@ struct Weights<TF32> {
 
 // EXACT: D = DP (else K pieces past the row are zeroed on their way).
 // CHUNK: the new rows of sequences over the paged cache (see above).
-template <class TR, int DP, bool EXACT, bool CHUNK = false>
+template <class TR, int DP, bool EXACT, bool CHUNK = false, int DU = DP>
 __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel(AttnArgs a) {
     using S = typename TR::storage;
-    using Sh = Shape<TR, DP>;
+    using Sh = Shape<TR, DP, DU>;
     constexpr int ES = Sh::ES, VEC = Sh::VEC, KT = Sh::KT, NF = Sh::NF, ND = Sh::ND;
     constexpr int PIECES = Sh::PIECES, LOADS = Sh::LOADS, VD = Sh::VD;
     extern __shared__ __align__(16) char lds[];

@@ -61,7 +61,8 @@ double tile_time(double tiles, double keys, double splits, int64_t D, ctconv_dty
     const bool f32 = dt == CTCONV_F32;
     // two workgroups share a compute unit up to 256 bytes a row; a step of both
     const bool pair = D * (int64_t)esize(dt) <= 256;
-    double step = f32 ? (pair ? 8500 : 9000) : D <= 64 ? 1500 : D <= 128 ? 2300 : 4500;
+    double step = f32 ? (D <= 32 ? 5400 : D <= 64 ? 9000 : D <= 96 ? 8000 : 9500)
+                      : D <= 32 ? 1200 : D <= 64 ? 1500 : D <= 96 ? 2100 : D <= 128 ? 2400 : 3600;
     if (pair && tiles * splits <= 256) step *= 0.6;
     const double rounds = ceil(tiles * splits / (pair ? 512 : 256));
     double t = 8000 + rounds * (ceil(ceil(keys / 64) / splits) + 2) * step;
