@@ -264,22 +264,29 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
     // the page that it asked for a tile before), before the barrier; what they
     // replace was read last two barriers ago.
     int64_t* const ring = reinterpret_cast<int64_t*>(lds + Sh::LDS);
-    int32_t page = 0;
+    int32_t page = 0, place = -1;  // of this lane's key of the tile asked for; -1: no key
     uint64_t seen_next[3] = {0, 0, 0};  // of the tile after this one and the ones after that
-    const auto slot_of = [&](int t) __attribute__((always_inline)) {
-        const int key = t * KT + lane;
-        return slot0 + (key < n ? key : n - 1);
-    };
+    const uint64_t page_bytes = (uint64_t)a.pages.page_stride * ES;
+    const uint64_t slot_bytes = (uint64_t)a.pages.slot_stride * ES;
+    const int32_t* const table = a.pages.table + b * a.pages.table_stride;
     const auto ask_page = [&](int t) __attribute__((always_inline)) {
-        page = a.pages.table[b * a.pages.table_stride +
-                             (int)fdiv((uint32_t)slot_of(t), a.pages.fd_page)];
+        const int key = t * KT + lane;
+        const int slot = slot0 + (key < n ? key : n - 1);
+        const int column = (int)fdiv((uint32_t)slot, a.pages.fd_page);
+        place = key < n ? slot - column * a.pages.page_size : -1;
+        page = table[column];
     };
     const auto put_offsets = [&](int t) __attribute__((always_inline)) {
-        const int64_t at = t * KT + lane < n ? offset_in_page(a.pages, slot_of(t), page) : -1;
-        if (lane >> 4 == wave) ring[(t & 3) * KT + lane] = at >= 0 ? at * ES : 0;
+        const bool is = place >= 0 && (uint32_t)page < (uint32_t)a.pages.num_pages;
+        const uint32_t p = is ? page : 0, q = is ? place : 0;
+        uint64_t at = (uint64_t)p * (uint32_t)page_bytes + (uint64_t)q * (uint32_t)slot_bytes;
+        if ((page_bytes | slot_bytes) >> 32)
+            at += (uint64_t)(p * (uint32_t)(page_bytes >> 32) + q * (uint32_t)(slot_bytes >> 32))
+                  << 32;
+        if (lane >> 4 == wave) ring[(t & 3) * KT + lane] = (int64_t)at;
         seen_next[0] = seen_next[1];
         seen_next[1] = seen_next[2];
-        seen_next[2] = __ballot(at >= 0);
+        seen_next[2] = __ballot(is);
     };
     const char* const k_from = reinterpret_cast<const char*>(kb + k_d);
     const char* const v_from4 = reinterpret_cast<const char*>(vb + (ES == 2 ? v_from : k_d));
