@@ -49,7 +49,7 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
 
 // The two kernels' times in ns, as far as the host can tell, for the choice between
 // them and the splits.  tile_kernel: rounds of the workgroups that the chip holds, a
-// step per 64 keys and two to start and end, and for split tiles the partial rows,
+// step per 64 keys, their start and end, and for split tiles the partial rows,
 // written and read (19 k rows of 32 heads over up to 8192 keys take 1565 us whole
 // and 2160 in chunks of 4096), and the join.  stream_kernel: keys and values once
 // per 16 rows, and workgroups without work where sequences have fewer rows than n.
@@ -65,7 +65,7 @@ double tile_time(double tiles, double keys, double splits, int64_t D, ctconv_dty
                       : D <= 32 ? 1200 : D <= 64 ? 1500 : D <= 96 ? 2100 : D <= 128 ? 2400 : 3600;
     if (pair && tiles * splits <= 256) step *= 0.6;
     const double rounds = ceil(tiles * splits / (pair ? 512 : 256));
-    double t = 8000 + rounds * (ceil(ceil(keys / 64) / splits) + 2) * step;
+    double t = 8000 + rounds * (ceil(ceil(keys / 64) / splits) * step + 4500);
     if (splits > 1) t += 6000 + tiles * splits * 128 * (double)D * 8 / 5000;
     return t;
 }
@@ -79,8 +79,8 @@ double stream_time(double tiles, double padded, double keys, int64_t D, ctconv_d
 //    last to end: twice as many workgroups as fill the chip (8 x 64 rows of 32 heads
 //    over up to 32768 keys: 186 us in chunks of 4096, 286 in chunks of 8192, but 426
 //    and 399 where all are that long), of 1024 keys at least.
-//  - So may their rows, where there are fewer than half of n per sequence: one that
-//    goes on by a row has the keys of a tile of 128 rows.  47 such and one of 2048
+//  - So may their rows, where there are several tiles of the longest and in the mean
+//    fewer than half of n: one that goes on by a row has the keys of a whole tile.  47 such and one of 2048
 //    rows over up to 16384 keys: 411 us in chunks of 4096, 479 of 8192, 636 whole.
 int64_t tile_splits(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, bool several,
                     bool uneven) {
@@ -145,7 +145,7 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     const int64_t tiles = (int64_t)tiles_of(128);
     int64_t span = span_of(128);
     if (R > 16 && D * (int64_t)esize(dt) <= 512) {
-        const int64_t splits = tile_splits(tiles, span, D, dt, B > 1, rows * 2 <= B * n);
+        const int64_t splits = tile_splits(tiles, span, D, dt, B > 1, R > 128 && rows * 2 <= B * n);
         p->tile = tile_time((double)tiles, (double)span, (double)splits, D, dt) <
                   stream_time((double)tiles_of(16), (double)padded, (double)span_of(16), D, dt);
         p->chunk = round_up(ceil_div(span, splits), 128);
