@@ -674,7 +674,8 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
  * (ctconv_rotary_append; ctconv_rotary for tensors of their own), and their
  * attention to all that the cache holds, in causal order
  * (ctconv_chunk_attention).  The common rules of the block's functions above
- * hold here too.
+ * hold here too; index and slot arrays need no alignment beyond their own 4
+ * bytes (CTCONV_ERR_ALIGN).
  *
  * New rows are packed (one sequence's rows behind the other's: row i of
  * sequence b is row row_starts[b] + i of `rows` rows) or, for the attention,
@@ -723,8 +724,7 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
  * row_slots are required when rows > 0.
  *
  * B at most 8192, B * max_pages and num_pages * page_size below 2^31
- * (CTCONV_ERR_SHAPE).  Index arrays need no alignment beyond their own 4 bytes
- * (CTCONV_ERR_ALIGN).  No page may be held twice.
+ * (CTCONV_ERR_SHAPE).  No page may be held twice.
  */
 ctconv_status ctconv_cache_pages(const int32_t* lengths, const int32_t* counts,
                                  const int32_t* now, const int32_t* held,

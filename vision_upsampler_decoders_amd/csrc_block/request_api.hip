@@ -80,8 +80,9 @@ double stream_time(double tiles, double padded, double keys, int64_t D, ctconv_d
 //    over up to 32768 keys: 186 us in chunks of 4096, 286 in chunks of 8192, but 426
 //    and 399 where all are that long), of 1024 keys at least.
 //  - So may their rows, where there are several tiles of the longest and in the mean
-//    fewer than half of n: one that goes on by a row has the keys of a whole tile.  47 such and one of 2048
-//    rows over up to 16384 keys: 411 us in chunks of 4096, 479 of 8192, 636 whole.
+//    fewer than half of n: one that goes on by a row has the keys of a whole tile.
+//    47 such and one of 2048 rows over up to 16384 keys: 411 us in chunks of 4096,
+//    479 of 8192, 636 whole.
 int64_t tile_splits(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, bool several,
                     bool uneven) {
     const int64_t n = tiles > 0 ? tiles : 1, steps = ceil_div(keys, 64);
@@ -128,7 +129,8 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     // (fp32 rows past 512 bytes are too long for its LDS tiles)
     // row tiles of all sequences: each may end inside one
     const auto tiles_of = [&](int64_t height) {
-        const __int128 all = (__int128)rows * G / height + B, most = (__int128)B * ceil_div(R, height);
+        const __int128 all = (__int128)rows * G / height + B;
+        const __int128 most = (__int128)B * ceil_div(R, height);
         return (all < most ? all : most) * Hkv;
     };
     // keys that the rows of one tile see together
@@ -161,6 +163,9 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     const __int128 values = (__int128)rows * Hq;
     const __int128 parts = p->splits > 1 ? values * p->splits : 0;
     const __int128 groups = (p->tile ? (__int128)tiles : padded) * p->splits;
+    // workgroups of the join of tiles (8 each) and of the weights (32 keys at least)
+    if (p->tile && p->splits > 1 && (__int128)tiles * 8 > kMaxInt) return CTCONV_ERR_SHAPE;
+    if (weights && (__int128)B * Hkv * ceil_div(max_length, 32) > kMaxInt) return CTCONV_ERR_SHAPE;
     if (groups > kMaxInt - 8 || parts * D > ((__int128)1 << 59) ||
         values > ((__int128)1 << 59))
         return CTCONV_ERR_SHAPE;
