@@ -326,9 +326,7 @@ CHUNK = [
     ([70], [40], 70, 2, 1, 64, 16, 0, "library"),  # rows before the first slot see nothing
 ]
 
-# Enough rows and heads that the tiled kernel is the faster one (the times that the planner
-# compares, in us: 8 + rounds of 64-key steps at 0.9 to 9 each against 10 + a 16-row tile's keys
-# and values at 6.5 GB/ms, over all row tiles).
+# Many rows and heads: in 16 bits most of these take the tiled kernel.
 MANY = [
     ([330, 329], [330, 420], 330, 8, 8, 128, 16, 0, "library"),
     ([700, 1, 0, 257], [700, 1500, 5, 900], 700, 16, 4, 64, 24, 0, "slots"),
@@ -362,6 +360,27 @@ def compare(got, lse, ref, what):
     out = np.concatenate([r[0] for r in ref])
     R.check(got, out, np.concatenate([r[2] for r in ref]), what + " out")
     R.check(lse, np.concatenate([r[1] for r in ref]), np.concatenate([r[3] for r in ref]), what + " lse")
+
+
+# And over keys enough that the tiled kernel is the faster one in this type, too.
+LONG = [
+    ("bf16", ([400], [3000], 400, 8, 2, 256, 8, 0, "library")),
+    ("f16", ([400, 9], [2800, 2500], 400, 8, 2, 200, 16, 0, "slots")),
+    ("f32", ([128], [8000], 128, 32, 8, 128, 16, 0, "library")),
+    ("f32", ([128, 1], [8100, 9000], 128, 32, 8, 96, 24, 0, "both")),
+    ("f32", ([256], [8100], 256, 32, 8, 64, 64, 5000, "library")),
+    ("f32", ([400], [6100], 400, 32, 8, 32, 16, 0, "slots")),
+    ("f32", ([300], [6100], 300, 32, 8, 40, 16, 0, "library")),
+    ("f32", ([200], [6100], 200, 32, 8, 80, 1, 0, "library")),
+    ("f32", ([128], [8000], 128, 32, 8, 120, 16, 0, "library")),
+    ("bf16", ([400], [3000], 400, 16, 4, 120, 16, 0, "library")),
+    ("f16", ([401, 300], [3000, 1700], 401, 16, 4, 104, 16, 0, "both")),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=[str(i) for i in range(len(LONG))])
+def test_chunk_attention_long(cc, case):  # noqa: F811
+    test_chunk_attention(cc, case[1], case[0], True)
 
 
 @pytest.mark.parametrize("dt", DTS)

@@ -102,9 +102,21 @@ stream_kernel(AttnArgs a) {
     int item = (int)block_number();
     const int split = item / tiles;
     item -= split * tiles;
-    const int tile = item % a.row_tiles;
-    const int bh = item / a.row_tiles;
-    const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+    int tile, bh, b, h;
+    if constexpr (CHUNK) {
+        // heads fastest: the row tiles of a head, which read the same keys, follow
+        // each other on one XCD
+        const int bt = item / a.Hkv;
+        h = item - bt * a.Hkv;
+        b = bt / a.row_tiles;
+        tile = bt - b * a.row_tiles;
+        bh = b * a.Hkv + h;
+    } else {
+        tile = item % a.row_tiles;
+        bh = item / a.row_tiles;
+        b = bh / a.Hkv;
+        h = bh - b * a.Hkv;
+    }
     const int row0 = tile * 16;
     ChunkRows cr;
     if constexpr (CHUNK) {

@@ -48,16 +48,19 @@ void rotary_common(int64_t rows, int64_t Hq, int64_t Hk, int64_t D, int64_t R, f
 }
 
 // The two kernels' times in ns, as far as the host can tell, for the choice between
-// them and the splits.  tile_kernel: rounds of the workgroups that the chip holds, a
-// step per 64 keys, their start and end, and for split tiles the partial rows,
-// written and read (19 k rows of 32 heads over up to 8192 keys take 1565 us whole
-// and 2160 in chunks of 4096), and the join.  stream_kernel: keys and values once
-// per 16 rows, and workgroups without work where sequences have fewer rows than n.
-// Measured against it (us, stream and tile; 32 heads on 8, D = 128): bf16, 24
-// sequences of 8192 keys, 16 rows per key head 168 and 180, 32 rows 242 and 184, 64
-// rows 488 and 195; one of 8192, 32 rows 23 and 31, 128 rows 52 and 35.  fp32, 24 of
-// 8192, 64 rows 920 and 986, 128 rows 1806 and 1005; one of 8192, 128 rows 91 and 104.
-double tile_time(double tiles, double keys, double splits, int64_t D, ctconv_dtype dt) {
+// them and the splits.  `once`: all keys and values.  tile_kernel: rounds of the
+// workgroups that the chip holds, a step per 64 keys, their start and end, at least
+// the reading of `once`, and for split tiles the partial rows, written and read (19 k
+// rows of 32 heads over up to 8192 keys take 1565 us whole and 2160 in chunks of
+// 4096), and the join.  stream_kernel: `once` from memory, then again from the L2
+// caches for every 16 rows past the first, and workgroups without work where
+// sequences have fewer rows than n.  Measured (us, stream and tile; 32 heads on 8, D =
+// 128): bf16, 24 sequences of 8192 keys, 32 rows per key head 201 and 180, 64 rows
+// 307 and 187; one of 8192, 32 rows 20 and 28, 128 rows 38 and 32; one of 65536, 32
+// rows 72 and 78.  fp32, 24 of 8192, 64 rows 688 and 985, 128 rows 1274 and 1000; one
+// of 65536, 64 rows 239 and 338, 128 rows 430 and 345.
+double tile_time(double tiles, double keys, double splits, double once, int64_t D,
+                 ctconv_dtype dt) {
     const bool f32 = dt == CTCONV_F32;
     // two workgroups share a compute unit up to 256 bytes a row; a step of both
     const bool pair = D * (int64_t)esize(dt) <= 256;
@@ -65,12 +68,15 @@ double tile_time(double tiles, double keys, double splits, int64_t D, ctconv_dty
                       : D <= 32 ? 1200 : D <= 64 ? 1500 : D <= 96 ? 2100 : D <= 128 ? 2400 : 3600;
     if (pair && tiles * splits <= 256) step *= 0.6;
     const double rounds = ceil(tiles * splits / (pair ? 512 : 256));
-    double t = 8000 + rounds * (ceil(ceil(keys / 64) / splits) * step + 4500);
+    double t = 8000 + fmax(rounds * (ceil(ceil(keys / 64) / splits) * step + 4500), once / 4800);
     if (splits > 1) t += 6000 + tiles * splits * 128 * (double)D * 8 / 5000;
     return t;
 }
-double stream_time(double tiles, double padded, double keys, int64_t D, ctconv_dtype dt) {
-    return 10000 + tiles * keys * 2 * (double)(D * (int64_t)esize(dt)) / 6500 +
+double stream_time(double tiles, double padded, double keys, double once, int64_t D,
+                   ctconv_dtype dt) {
+    const int64_t width = D <= 64 ? 64 : D <= 128 ? 128 : 256;  // as it computes
+    const double all = tiles * keys * 2 * (double)(width * (int64_t)esize(dt));
+    return 10000 + once / 5400 + fmax(all - once, 0) / (dt == CTCONV_F32 ? 12000 : 15000) +
            padded * ceil(keys / 512) * 2;
 }
 
@@ -83,14 +89,14 @@ double stream_time(double tiles, double padded, double keys, int64_t D, ctconv_d
 //    fewer than half of n: one that goes on by a row has the keys of a whole tile.
 //    47 such and one of 2048 rows over up to 16384 keys: 411 us in chunks of 4096,
 //    479 of 8192, 636 whole.
-int64_t tile_splits(int64_t tiles, int64_t keys, int64_t D, ctconv_dtype dt, bool several,
-                    bool uneven) {
+int64_t tile_splits(int64_t tiles, int64_t keys, double once, int64_t D, ctconv_dtype dt,
+                    bool several, bool uneven) {
     const int64_t n = tiles > 0 ? tiles : 1, steps = ceil_div(keys, 64);
     const int64_t slots = D * (int64_t)esize(dt) <= 256 ? 512 : 256;
     int64_t best = 1;
     double cost = HUGE_VAL;
     for (int64_t s = 1; s <= 64 && s <= ceil_div(steps, 2); ++s) {
-        const double t = tile_time((double)n, (double)keys, (double)s, D, dt);
+        const double t = tile_time((double)n, (double)keys, (double)s, once, D, dt);
         if (t < cost) {
             cost = t;
             best = s;
@@ -147,9 +153,13 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     const int64_t tiles = (int64_t)tiles_of(128);
     int64_t span = span_of(128);
     if (R > 16 && D * (int64_t)esize(dt) <= 512) {
-        const int64_t splits = tile_splits(tiles, span, D, dt, B > 1, R > 128 && rows * 2 <= B * n);
-        p->tile = tile_time((double)tiles, (double)span, (double)splits, D, dt) <
-                  stream_time((double)tiles_of(16), (double)padded, (double)span_of(16), D, dt);
+        const double once =
+            (double)B * (double)Hkv * (double)span * 2 * (double)(D * (int64_t)esize(dt));
+        const bool uneven = R > 128 && rows * 2 <= B * n;
+        const int64_t splits = tile_splits(tiles, span, once, D, dt, B > 1, uneven);
+        p->tile = tile_time((double)tiles, (double)span, (double)splits, once, D, dt) <
+                  stream_time((double)tiles_of(16), (double)padded, (double)span_of(16), once, D,
+                              dt);
         p->chunk = round_up(ceil_div(span, splits), 128);
         p->row_tiles = tiles / Hkv;
     }
