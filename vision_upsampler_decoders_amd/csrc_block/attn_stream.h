@@ -219,13 +219,15 @@ stream_kernel(AttnArgs a) {
     const int t0 = first + start;
 
     bool careful = false;  // CHUNK: the second time
+    __shared__ int odd_sums;
+    if (CHUNK && tid == 0) odd_sums = 0;
 again:
     int done = 0;  // keys of earlier pieces
     int n_here = n;
     do {
     if constexpr (CHUNK) {
         n_here = n - done < kPiece ? n - done : kPiece;
-        if (done > 0 || careful) __syncthreads();
+        if (done > 0) __syncthreads();
         stage(done, done + n_here);
         __syncthreads();
     }
@@ -373,18 +375,24 @@ again:
         }
         if constexpr (CHUNK)
             if (__any(odd)) {
-                // this lane's values of output columns (4 g + i) VPL + e, row col
+                // this lane's values of output columns (4 g + i) VPL + e, row col (what
+                // lies past a row's end goes to columns that are not written)
+                constexpr int RUN = VPL < 8 ? VPL : 8;
                 for (int j = 0; j < KB; ++j) {
                     if (!((bits >> j) & 1)) continue;
                     const S* vrow = vbase + offs[kb + j];
-                    const bool sees = (mine >> j) & 1;
+                    const float sees = (mine >> j) & 1 ? 1.f : 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int e = 0; e < VPL; ++e) {
-                            const int d = (4 * g + i) * VPL + e;
-                            const float x = sees && d < a.D ? TR::to_f32(vrow[d]) : 0.f;
-                            if (!(fabsf(x) <= __FLT_MAX__)) acc[e][i] += x;
+                        for (int e0 = 0; e0 < VPL; e0 += RUN) {
+                            const int d = (4 * g + i) * VPL + e0;
+                            const S* run = vrow + (EXACT || d < a.D ? d : 0);
+#pragma unroll
+                            for (int e = 0; e < RUN; ++e) {
+                                const float x = TR::to_f32(run[e]);
+                                if (sees != 0.f && !(fabsf(x) <= __FLT_MAX__)) acc[e0 + e][i] += x;
+                            }
                         }
                 }
             }
@@ -398,7 +406,9 @@ again:
         for (int e = 0; e < VPL; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i) worst += 0.f * acc[e][i];
-        if (__syncthreads_or(worst != 0.f) && !careful) {
+        if (!careful && __any(worst != 0.f)) odd_sums = 1;
+        __syncthreads();  // offs and seen are no longer read
+        if (!careful && odd_sums) {
             careful = true;
 #pragma unroll
             for (int e = 0; e < VPL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -413,7 +423,7 @@ again:
     // Merge the waves: [wave][row][DS] outputs, then [wave][row] maxima and
     // sums.  Who writes a piece of a row weighs the waves by itself: NW
     // exponentials cost less than one more barrier.
-    __syncthreads();  // offs and seen are no longer read
+    if constexpr (!CHUNK) __syncthreads();  // offs and seen are no longer read
     float* mo = reinterpret_cast<float*>(lds);
     float* mm = mo + NW * rows * DS;
     float* ml = mm + NW * 16;

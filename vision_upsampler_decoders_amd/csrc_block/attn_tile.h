@@ -718,10 +718,10 @@ __global__ __launch_bounds__(kThreads, (Shape<TR, DP>::PER_CU)) void tile_kernel
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int at_d = 32 * d + 8 * i;
-                        if (at_d >= a.D) continue;
+                        // (what lies past a row's end goes to columns that are not written)
+                        const int at_d = 32 * d + 8 * i + 4 * half;
                         S v[4];
-                        const S* from = vb + at + at_d + 4 * half;
+                        const S* from = vb + at + (EXACT || at_d < a.D ? at_d : 0);
                         if constexpr (ES == 2)
                             *reinterpret_cast<u32x2*>(v) = *reinterpret_cast<const u32x2*>(from);
                         else
