@@ -82,9 +82,10 @@ double stream_time(double tiles, double padded, double keys, double once, int64_
 
 // Splits of tile_kernel's row tiles, at least two steps of keys each.
 //  - Of several sequences the lengths may differ, and the longest one's tiles are the
-//    last to end: twice as many workgroups as fill the chip (8 x 64 rows of 32 heads
-//    over up to 32768 keys: 186 us in chunks of 4096, 286 in chunks of 8192, but 426
-//    and 399 where all are that long), of 1024 keys at least.
+//    last to end.  Lengths spread evenly make (s + 1) / 2 workgroups of a tile in the
+//    mean: as many as fill the chip, of 1024 keys at least.  24 x 8 rows of 32 heads
+//    over up to 8192 keys: 99 us in chunks of 2048, 118 of 1664 (the second round of
+//    a few), 121 of 4096.
 //  - So may their rows, where there are several tiles of the longest and in the mean
 //    fewer than half of n: one that goes on by a row has the keys of a whole tile.
 //    47 such and one of 2048 rows over up to 16384 keys: 411 us in chunks of 4096,
@@ -103,7 +104,7 @@ int64_t tile_splits(int64_t tiles, int64_t keys, double once, int64_t D, ctconv_
         }
     }
     int64_t more = 1;
-    if (several && n < slots) more = 2 * slots / n;
+    if (several && n < slots) more = 2 * slots / n - 1;
     if (several && uneven) {
         const int64_t s = 8 * slots / n < 8 ? 8 * slots / n : 8;
         more = s > more ? s : more;
