@@ -137,20 +137,20 @@ def test_chunk_attention_validation(lib):  # noqa: F811
     for name in ("q", "k", "v", "table", "lengths", "out", "qs", "kv", "os_"):
         assert _chunk(lib, **{name: None}) == NULL, name
     assert _chunk(lib, w=P[7], slot=None) == NULL
-    padded = dict(starts=None, rows=12, qs=(3072, 512, 64), os_=(3072, 512, 64))
+    padded = dict(starts=None, rows=10, n=5, qs=(2560, 512, 64), os_=(2560, 512, 64))
     for kw in (dict(B=-1), dict(rows=-1), dict(n=-1), dict(Hq=0), dict(Hq=6), dict(H=0), dict(D=60),
                dict(D=512), dict(pages=0), dict(maxlen=81), dict(maxlen=-1), dict(window=-1),
                dict(kv=(-1, 64, 1024)), dict(qs=(0, -512, 64)), dict(os_=(0, 1 << 62, 64)),
                dict(os_=(0, 511 // 8 * 8, 64)), dict(os_=(0, 0, 64)), dict(ts=-5),
                dict(n=1 << 29), dict(w=P[7], slot=(1, -1)), dict(w=P[7], slot=(0, 80)),
-               dict(w=P[7], slot=(320, 40)), {**padded, "rows": 11}, {**padded, "rows": 13},
-               {**padded, "os_": (2560, 512, 64)}, {**padded, "os_": (0, 512, 64)}):
+               dict(w=P[7], slot=(320, 40)), {**padded, "rows": 9}, {**padded, "rows": 11},
+               {**padded, "os_": (2048, 512, 64)}, {**padded, "os_": (0, 512, 64)}):
         assert _chunk(lib, **kw) == SHAPE, kw
     for s in (math.inf, math.nan, -math.inf):
         assert _chunk(lib, scale=s) == PARAM
     assert _chunk(lib, dt=-1) == DTYPE
     for kw in (dict(q=8), dict(k=0x1001), dict(v=0x1008), dict(out=0x1002), dict(ws=0x1008),
-               dict(qs=(0, 512, 60)), dict(kv=(4097, 64, 1024)), {**padded, "qs": (3073, 512, 64)}):
+               dict(qs=(0, 512, 60)), dict(kv=(4097, 64, 1024)), {**padded, "qs": (2561, 512, 64)}):
         assert _chunk(lib, **kw) == ALIGN, kw
     need = C.ctconv_chunk_attention_workspace_bytes(2, 9, 6, 8, 4, 64, 80, 0, True, 1)
     assert need >= 9 * 8 * 4

@@ -1,6 +1,7 @@
 // Attention of a chunk of new rows over the paged cache: the chunk form of the
 // streaming kernel (attn_stream.h) for few rows per key head, the join of its
-// splits, and the weights of the slots.
+// splits (a workgroup per row, as few rows have many splits), and the weights of the
+// slots.
 
 #include "attn_mma.h"
 #include "attn_stream.h"
@@ -85,7 +86,11 @@ constexpr int key_groups(int pieces) {
 // instructions take (4096 rows of 24 heads over 32768 keys twice, f16: 3126 us, and
 // 2005 this way).  The waves of a workgroup take keys of their own and the same
 // rows, or, where that would leave compute units idle (APART), the same keys and
-// every fourth rows.
+// every fourth rows: where those are at most 512 workgroups (bf16, 4 heads of 128
+// channels, apart | together, the call: 4000 rows of 16 heads over 4000 keys, 500
+// workgroups apart, 212 | 487 us; 500 of 32 over 8: 1000 keys, 256 workgroups,
+// 53 | 98, 4000, 1000, 105 | 119, twice 4000, 2000, 198 | 176; 16 rows of 32: 21 | 22,
+// 32 | 25, 52 | 33).
 // 1.55 TFLOP in 1.95 ms there: 0.7 of it for the exponentials, 0.7 for the matrix
 // instructions, 0.35 for two more vector instructions a score; each is busy while the
 // other waits.  Tried: the scores of one group weighed between the next one's matrix
@@ -356,7 +361,7 @@ hipError_t weights_d(const AttnArgs& a, hipStream_t s) {
     if (a.pages.slots == 0) return hipSuccess;
     // (fp32 rows of 1 KB: the tiles of four waves do not fit LDS)
     if constexpr (NF <= 16)
-        if ((int64_t)a.B * a.Hkv * blocks(together) < 512)
+        if ((int64_t)a.B * a.Hkv * blocks(own) <= 512)
             return weights_a<TR, DP, true>(a, blocks(own), s);
     return weights_a<TR, DP, false>(a, blocks(together), s);
 }

@@ -42,6 +42,10 @@
 // two parts of which one is 0.  A workgroup whose sums are not all finite goes
 // over its keys once more: V's infinities and NaN are then taken out of the
 // product and added to the rows that see them.
+// 2 rows of 8 heads over a window of 250, fp32: 9.5 us (one row of a paged call: 8.4).
+// 128 rows per key head over 24 x 8192 keys, D = 128, bf16: 560 us, and 955 with a
+// head's row tiles on different XCDs; a window of 1000 over 3867 rows of 8 heads, D =
+// 64, fp32: 88 us, the matrix unit 59 % busy.
 
 #pragma once
 

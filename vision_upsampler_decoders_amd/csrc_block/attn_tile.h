@@ -58,6 +58,14 @@
 // keys go through LDS, two tiles ahead of their loads.  And every row has its own
 // last (and, in a window, first) key: tiles that some row does not see whole hide
 // scores per lane.  Waves without a row only move tiles.
+// Loads are of 64-bit addresses (a cache may be larger than 4 GB), and the offsets
+// of K's pieces in LDS are turned on their way, so that as many registers are left
+// as the other form has: what lies in scratch memory is not read in the loop (where
+// it is, it waits behind the loads in flight: 1590 us against 1518 below).
+// 8 ragged prompts of 19.4 k rows over up to 8192 slots, 32 heads on 8, D = 128, bf16:
+// 1518 us, 855 TFLOP/s; 2 x 4096 rows over 32768, 24 heads on 4, f16: 3640 us, 850.
+// 32 heads of 4 x 2048 rows over 8192, bf16: D = 32 450 TFLOP/s, 64 717, 96 770, 128
+// 913, 256 615; one sequence in fp32: 100, 116, 99, 109.
 
 #pragma once
 

@@ -1,5 +1,6 @@
 // Internal declarations of the decoder-block operators (not installed):
-// kernel arguments, filled on the host by block_api.hip, and launchers.
+// kernel arguments, filled on the host by block_api.hip and request_api.hip, and
+// launchers.
 #pragma once
 
 #include <hip/hip_runtime.h>

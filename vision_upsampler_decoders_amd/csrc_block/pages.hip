@@ -6,9 +6,11 @@
 // finds its sequence by bisection in those sums.  No atomics: the order on the
 // stack is that of sequences and columns.  A step moves few pages, so its time
 // is a chain of latencies: the lengths, the scan, the stack, the table (48
-// sequences that go on by a row, with slot arrays of 8 heads: see tables_fused).
+// sequences that go on by a row, with slot arrays of 8 heads: 4.9 us).  Where many
+// pages move, four entries of a thread are on their way together: 96 sequences of
+// which a third ends and a third is new, some 8000 pages: 11 us, and 15 one by one.
 // The maps of few rows are written by the same workgroup, of many by a kernel of
-// their own, a row per thread.
+// their own, a row per thread (61 k rows 4 us).
 
 #include "block_internal.h"
 

@@ -8,7 +8,10 @@
 // bytes that they go with, each read and written once by the same thread, so
 // that a call may work in place.  Rotary parts whose half is not a multiple of
 // 16 bytes are taken in pieces of 8, 4 or 2 (one value).
-// Long calls are bound by memory.
+// Long calls are bound by memory: 32768 rows of 40 heads of 128, bf16 (671 MB): 125
+// us, 5.3 TB/s, the rate of a large copy; 16397 rows into the cache, f16 (336 MB), 72
+// us, 4.65.  Value by value (38 of 96 values, bf16) 2.8 and 2.1 TB/s; in fp32 4.8
+// and 3.6.  A step of 48 rows takes 4.8 us, a chain of latencies.
 
 #include "block_internal.h"
 #include "mfma_common.h"
@@ -196,7 +199,8 @@ hipError_t rotary_v(RotaryArgs a, bool append, hipStream_t s) {
     a.fd_items = make_fastdiv((uint32_t)a.items);
     a.fd_half = make_fastdiv((uint32_t)a.half);
     // one round of every thread's pieces per workgroup, if the rows still
-    // spread over the chip
+    // spread over the chip (40 heads of 64 channels, bf16, one row a workgroup |
+    // two: 512 rows 7.0 | 7.3 us, 2048 8.4 | 7.2, 32768 92 | 66)
     int per = kAtOnce * kThreads / a.items;
     per = per < 1 ? 1 : per > kMostRows ? kMostRows : per;
     while (per > 1 && a.rows / per < 1024) per >>= 1;
