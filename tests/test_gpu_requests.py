@@ -428,6 +428,70 @@ def test_chunk_attention(cc, case, dt, weights):  # noqa: F811
         assert (o[b, counts[b]:] == 9).all()
 
 
+@pytest.mark.parametrize("n,Hq", [(3, 4), (2000, 8)])
+def test_chunk_offsets_past_32_bits(cc, n, Hq):  # noqa: F811
+    """A pool of few pages a long stride apart: written by rotary_append, read by
+    chunk_attention with few rows and with many."""
+    import torch
+
+    D, page, L = 64, 512, 2010
+    say(f"chunk far pages n={n}")
+    rng = np.random.default_rng(12)
+    stride = (1 << 31) + 64  # elements; page 3 starts past 2^32 elements
+    pool = torch.empty(3 * stride + page * D, dtype=torch.bfloat16, device="cuda")
+    kd = pool.as_strided((4, 1, page, D), (stride, page * D, D, 1))
+    k, k64 = dev(rng.standard_normal((4, 1, page, D)), "bf16")
+    kd.copy_(k)
+    table = np.array([[3, 1, 2, 0]], np.int32)
+    q, q64 = dev(rng.standard_normal((n, Hq, D)), "bf16")
+    w = torch.zeros(1, 1, 4 * page, device="cuda")
+    out, lse = cc.chunk_attention(q, kd, kd, ints(table), ints([L]), row_starts=ints([0, n]),
+                                  weight_sum=w)
+    torch.cuda.synchronize()
+    ref, rw, rb = Q.chunk([q64], k64, k64, table, [L], [n], page, 0, D ** -0.5, "bf16")
+    compare(to_host(out), to_host(lse), ref, "far")
+    R.check(to_host(w), rw, rb, "weights")
+    f = cc.rotary_frequencies(D, device="cuda")
+    rows, r64 = dev(rng.standard_normal((3, 2, D)), "bf16")
+    slots, pos = [3 * page + 5, 7, 4 * page - 1], np.array([9, 200, 31])
+    v = torch.zeros(4, 1, page, D, dtype=torch.bfloat16, device="cuda")
+    v = pool.new_empty(3 * stride + page * D).as_strided(kd.shape, kd.stride()).copy_(v)
+    cc.rotary_append(None, rows[:, :1], rows[:, 1:], ints(pos), ints(slots), f, kd, v)
+    want, bound = Q.turned(r64, pos, to_host(f), 0, 1.0, "bf16")
+    kw, kb, vw = k64.copy(), np.zeros(k64.shape), np.zeros(k64.shape)
+    for i, t in enumerate(slots):
+        kw[t // page, :, t % page], kb[t // page, :, t % page] = want[i, :1], bound[i, :1]
+        vw[t // page, :, t % page] = r64[i, 1:]
+    R.check(to_host(kd), kw, kb, "k")
+    assert np.array_equal(to_host(v), vw)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("n,Hq,H,D", [(5, 4, 2, 64), (300, 16, 4, 128), (330, 32, 8, 96)])
+def test_chunk_rows_that_do_not_exist(cc, dt, n, Hq, H, D):  # noqa: F811
+    """row_starts that go on past the rows of the call: those that exist have the places that
+    their sequence's full count gives them."""
+    import torch
+
+    say(f"chunk cut rows {dt} n={n}")
+    rng = np.random.default_rng(n)
+    lengths, counts, page, cut = [n + 900, n + 20], [n - 1, n], 16, n // 2
+    c = Cache(rng, 2, H, D, page, lengths, dt)
+    x = rng.standard_normal((sum(counts), Hq, D))
+    live = sum(counts) - cut
+    q, q64 = dev(x[:live], dt)
+    w = torch.zeros(2, H, c.table.shape[1] * page, device="cuda")
+    out = guarded(torch.full((live, Hq, D), 9.0, dtype=q.dtype, device="cuda"))
+    lse = guarded(torch.full((live, Hq), 9.0, device="cuda"))
+    cc.chunk_attention(q, c.kd, c.vd, c.td, c.ld, row_starts=ints([0, n - 1, 2 * n - 1]), n=n,
+                       weight_sum=w, out=out, lse=lse)
+    torch.cuda.synchronize()
+    ref, rw, rb = Q.chunk([q64[:n - 1], q64[n - 1:]], c.k, c.v, c.table, lengths, counts, page, 0,
+                          D ** -0.5, dt)
+    compare(to_host(out), to_host(lse), ref, "cut")
+    R.check(to_host(w), rw, rb, "weights")
+
+
 @pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("n,Hq,H,extra", [(6, 4, 2, 0), (90, 4, 2, 0), (150, 32, 16, 992)])
 def test_chunk_attention_missing_pages_and_long_lengths(cc, dt, n, Hq, H, extra):  # noqa: F811

@@ -158,6 +158,23 @@ def test_chunk_attention_validation(lib):  # noqa: F811
     assert _chunk(lib, w=P[7], nb=need - 1) == WORKSPACE
 
 
+def test_chunk_attention_index_alignment_and_most_rows(lib):  # noqa: F811
+    for kw in (dict(table=P[3] + 2), dict(lengths=P[4] + 1), dict(starts=P[9] + 2),
+               dict(lse=P[6] + 2), dict(w=P[7] + 2),
+               dict(starts=None, rows=10, n=5, qs=(2560, 512, 64), os_=(2560, 512, 64),
+                    counts=P[9] + 2)):
+        assert _chunk(lib, **kw) == ALIGN, kw
+    # the kernels step past the last row: no int32 may end there
+    for weights in (False, True):
+        with pytest.raises(C.CtconvError) as e:
+            C.ctconv_chunk_attention_workspace_bytes(1, 9, 2 ** 31 - 1, 1, 1, 64, 80, 0, weights, 1)
+        assert e.value.status == SHAPE
+        with pytest.raises(C.CtconvError) as e:
+            C.ctconv_chunk_attention_workspace_bytes(1, 9, 2 ** 29 - 1, 4, 1, 64, 80, 0, weights, 1)
+        assert e.value.status == SHAPE
+    assert C.ctconv_chunk_attention_workspace_bytes(1, 9, 2 ** 20, 1, 1, 64, 80, 0, False, 1) == 0
+
+
 def test_chunk_attention_workspace(lib):  # noqa: F811
     f = C.ctconv_chunk_attention_workspace_bytes
     assert f(0, 0, 1, 8, 4, 64, 10000, 0, False, 1) == 0

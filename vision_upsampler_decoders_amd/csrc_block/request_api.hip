@@ -135,7 +135,8 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     if (rows < 0 || rows > kMaxInt || n < 0 || n > kMaxInt) return CTCONV_ERR_SHAPE;
     if (max_length < 0 || max_length > kMaxInt - (1 << 20) || window < 0) return CTCONV_ERR_SHAPE;
     const int64_t G = Hq / Hkv;
-    if ((__int128)n * G > kMaxInt) return CTCONV_ERR_SHAPE;
+    // (kernels step past the last row by less than that)
+    if ((__int128)n * G > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
     const int64_t R = n * G;
     // (fp32 rows past 512 bytes are too long for its LDS tiles)
     // row tiles of all sequences: each may end inside one
@@ -469,6 +470,9 @@ ctconv_status ctconv_chunk_attention(const void* q, const void* k_cache, const v
     if (weight_sum && c.st == CTCONV_OK)
         c.st = slot_strides_ok(slot_strides, B, Hkv, page_size * max_pages);
     st = c.status();
+    for (const void* i : {(const void*)page_table, (const void*)lengths, (const void*)row_starts,
+                          (const void*)counts, (const void*)lse, (const void*)weight_sum})
+        if (st == CTCONV_OK && !aligned4(i)) st = CTCONV_ERR_ALIGN;
     if (st != CTCONV_OK) return st;
     if (!rows_apart(out_strides, {batch, in_batch, Hq}, D) ||
         (weight_sum && !rows_apart(slot_strides, {B, Hkv}, max_length)))
