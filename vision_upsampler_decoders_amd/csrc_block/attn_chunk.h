@@ -25,7 +25,7 @@ __device__ inline ChunkRows chunk_rows(const AttnArgs& a, int b) {
         const int from = a.row_starts[b];
         const int64_t given = (int64_t)a.row_starts[b + 1] - from;
         r.row0 = from;
-        r.count = given < 0 ? 0 : given > a.n ? a.n : (int)given;
+        r.count = given < 0 ? 0 : given > a.most ? a.most : (int)given;
         const int room = from >= 0 && from < a.rows ? a.rows - from : 0;
         r.live = r.count < room ? r.count : room;
     } else {
@@ -84,7 +84,7 @@ __device__ inline uint32_t take_odd(uint32_t& w) {
 __device__ inline int chunk_splits(const AttnArgs& a, const ChunkRows& r) {
     int span = r.off + r.live;
     // (128 rows lie at most this far apart)
-    const int most = a.window + (a.n < 128 ? a.n : 128);
+    const int most = a.window + (a.most < 128 ? a.most : 128);
     span = a.window > 0 && span > most ? most : span;
     return span > a.chunk ? (span + a.chunk - 1) / a.chunk : 1;
 }

@@ -110,7 +110,8 @@ struct AttnArgs {
     // Chunk calls: each sequence's own number of rows.
     const int32_t *row_starts, *counts;
     float* lse2;                 // log2 of the sums of weights, [rows, Hq] (weights)
-    int n, rows;                 // most rows of a sequence, rows of the call
+    int most;                    // what row_starts' counts are clamped to
+    int n, rows;                 // most rows of a sequence that exist, rows of the call
 };
 
 struct NormArgs {

@@ -84,6 +84,33 @@ double stream_time(double tiles, double padded, double keys, double once, int64_
            padded * ceil(keys / 512) * 2;
 }
 
+// Keys per workgroup of stream_kernel: `tiles` row tiles in a grid of `padded`, which a
+// packed call does not fill where one sequence has most of its rows.  From 2048
+// workgroups on
+//  - without a split, if enough of them have rows (32 query heads over 8 of 128
+//    channels, bf16, ragged lengths, whole | split: 512 tiles of 16 rows over at most
+//    4000 keys 90 | 90 us, 1024 145 | 155, 2048 243 | 269; over 8000 167 | 144, 256 |
+//    246, 447 | 450);
+//  - else in no more splits than shorten a workgroup's walk over its keys, some 30
+//    bytes a ns (a key of 64, 128, 256 values: f32 21, 30, 52 ns, bf16 11, 15, 32), by
+//    more than the workgroups without a row take, 2 ns each.  19 sequences with one new
+//    row and one with 101, 24 heads of 64 on 12, up to 23918 keys, fp32 (336 of 3120 have
+//    rows): whole 803 us, in 9 splits 475.
+void stream_chunk(int64_t tiles, int64_t padded, int64_t span, int64_t D, ctconv_dtype dt,
+                  int64_t* chunk, bool* wide) {
+    if (padded >= 2048 && tiles >= 1024) {
+        *chunk = round_up(span, 128);
+        return;
+    }
+    stream_split(padded, span, D, dt, chunk, wide);
+    if (padded < 2048) return;
+    const double walk = (double)span * 2 * (double)(D * (int64_t)esize(dt)) / 30;
+    double most = sqrt(walk / (2 * (double)(padded - tiles)));
+    most = fmax(fmin(most, (double)(kMaxInt / 2) / (double)padded), 1);
+    const int64_t least = round_up((int64_t)ceil((double)span / most), 128);
+    *chunk = *chunk > least ? *chunk : least;
+}
+
 // Splits of tile_kernel's row tiles, at least two steps of keys each.
 //  - Of several sequences the lengths may differ, and the longest one's tiles are the
 //    last to end.  Lengths spread evenly make (s + 1) / 2 workgroups of a tile in the
@@ -121,7 +148,7 @@ int64_t tile_splits(int64_t tiles, int64_t keys, double once, int64_t D, ctconv_
 struct ChunkPlan {
     bool tile;  // many rows per key head: tile_kernel, else stream_kernel
     bool wide;
-    int64_t row_tiles, chunk, splits;
+    int64_t n, row_tiles, chunk, splits;
     int64_t part_o_bytes, part_ml_bytes, lse_bytes, bytes;
 };
 
@@ -137,8 +164,10 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     const int64_t G = Hq / Hkv;
     // (kernels step past the last row by less than that)
     if ((__int128)n * G > kMaxInt - (1 << 20)) return CTCONV_ERR_SHAPE;
-    const int64_t R = n * G;
-    // (fp32 rows past 512 bytes are too long for its LDS tiles)
+    if ((__int128)B * Hkv * n * G > kMaxInt) return CTCONV_ERR_SHAPE;
+    // rows of a sequence that exist: n may be any bound (of a packed call; else rows = B n)
+    p->n = n < rows ? n : rows;
+    const int64_t R = p->n * G;
     // row tiles of all sequences: each may end inside one
     const auto tiles_of = [&](int64_t height) {
         const __int128 all = (__int128)rows * G / height + B;
@@ -153,15 +182,14 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
         return s > 0 ? s : 1;
     };
     const __int128 padded = (__int128)B * Hkv * ceil_div(R, 16);
-    if (tiles_of(16) > kMaxInt || padded > kMaxInt || (__int128)B * Hkv * R > kMaxInt)
-        return CTCONV_ERR_SHAPE;
-    // (fp32 rows past 512 bytes are too long for the tile kernel's LDS)
+    if (tiles_of(16) > kMaxInt) return CTCONV_ERR_SHAPE;
     const int64_t tiles = (int64_t)tiles_of(128);
     int64_t span = span_of(128);
+    // (fp32 rows past 512 bytes are too long for the tile kernel's LDS)
     if (R > 16 && D * (int64_t)esize(dt) <= 512) {
         const double once =
             (double)B * (double)Hkv * (double)span * 2 * (double)(D * (int64_t)esize(dt));
-        const bool uneven = R > 128 && rows * 2 <= B * n;
+        const bool uneven = R > 128 && rows * 2 <= B * p->n;
         const int64_t splits = tile_splits(tiles, span, once, D, dt, B > 1, uneven);
         p->tile = tile_time((double)tiles, (double)span, (double)splits, once, D, dt) <
                   stream_time((double)tiles_of(16), (double)padded, (double)span_of(16), once, D,
@@ -172,11 +200,7 @@ ctconv_status chunk_plan(int64_t B, int64_t rows, int64_t n, int64_t Hq, int64_t
     if (!p->tile) {
         p->row_tiles = ceil_div(R, 16);
         span = span_of(16);
-        // Enough workgroups without a split (32 query heads over 8 of 128 channels,
-        // bf16, ragged lengths, whole | split: 512 tiles of 16 rows over at most
-        // 4000 keys 85 | 78 us, 2048 208 | 229, 8192 408 | 542).
-        if (padded >= 2048) p->chunk = round_up(span, 128);
-        else stream_split((int64_t)padded, span, D, dt, &p->chunk, &p->wide);
+        stream_chunk((int64_t)tiles_of(16), (int64_t)padded, span, D, dt, &p->chunk, &p->wide);
     }
     p->splits = ceil_div(span, p->chunk);
     const __int128 values = (__int128)rows * Hq;
@@ -503,12 +527,13 @@ ctconv_status ctconv_chunk_attention(const void* q, const void* k_cache, const v
         a.slot_h = slot_strides[1];
     }
     a.B = (int)B;
-    a.n = (int)n;
+    a.n = (int)p.n;
+    a.most = (int)n;
     a.rows = (int)rows;
     a.Hq = (int)Hq;
     a.Hkv = (int)Hkv;
     a.G = (int)(Hq / Hkv);
-    a.R = (int)(n * a.G);
+    a.R = (int)(p.n * a.G);
     a.D = (int)D;
     a.window = (int)(window < max_length ? window : 0);
     a.fd_G = make_fastdiv((uint32_t)a.G);
