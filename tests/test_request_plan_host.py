@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+import request_cases as cases
 from test_block_host_sanitizers import CLANGXX, HIPCC, PKG, ROOT, _run
 from vision_upsampler_decoders_amd import ctconv as C
 
@@ -62,3 +63,35 @@ def test_workgroups_without_rows_do_not_stop_a_split(plan, dt, D):
     B, n = 24, 128
     kernel, splits, _, groups = plan(B, B - 1 + n, n, 12, 12, D, 60000, 0, 0, dt)
     assert kernel == "tile" or (splits >= 4 and groups < 1 << 20)
+
+
+CODE = {"f32": F32, "bf16": BF16, "f16": F16}
+
+
+@pytest.mark.parametrize("case", cases.ODD, ids=[str(i) for i in range(len(cases.ODD))])
+def test_cases_of_odd_values_reach_their_kernel(plan, case):
+    dt, counts, lengths, H, G, D, window, kernel, split = case
+    got = plan(len(counts), sum(counts), max(counts), H * G, H, D, max(lengths), window, 0, CODE[dt])
+    assert got[0] == kernel and (got[1] > 1) == split, got
+    if kernel == "stream" and not split and max(lengths) > 1024:
+        assert got[2] > 1024  # its places are staged more than once
+
+
+def test_tiled_cases_reach_the_tiled_kernel(plan):
+    for dt, (counts, lengths, n, Hq, H, D, page, window, _) in cases.TILED:
+        most = (-(-max(lengths) // page) + 1) * page
+        for weights in (0, 1):
+            assert plan(len(counts), sum(counts) + 3, n, Hq, H, D, most, window, weights,
+                        CODE[dt])[0] == "tile", (counts, D)
+            assert plan(len(counts), len(counts) * n, n, Hq, H, D, most, window, weights, CODE[dt],
+                        packed=0)[0] == "tile", (counts, D)
+    for dt, n, Hq, H, D in cases.CUT:
+        most = -(-(n + 900) // 16) * 16
+        assert plan(2, 2 * n - 1 - n // 2, n, Hq, H, D, most, 0, 1, CODE[dt])[0] == "tile"
+    for dt, n, Hq, H, extra in cases.MISSING:
+        for most in (160 + extra, 150 + extra):
+            assert plan(5, 5 * n, n, Hq, H, 64, most, 0, 1, CODE[dt], packed=0)[0] == "tile"
+
+
+def test_page_0_case_reaches_the_tiled_kernel(plan):
+    assert plan(2, 256, 128, 32, 8, 128, 8000, 0, 0, BF16)[0] == "tile"
