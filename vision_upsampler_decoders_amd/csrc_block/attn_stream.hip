@@ -84,10 +84,12 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(AttnArgs a) {
         for (int e = 0; e < 4; ++e) o[e] *= old;
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const float f = s0 + i < n ? exp2_fast(v[i][0] - ref) : 0.f;
+            // (read twice: 0 as a result, too, as 0 times an infinite one is NaN)
+            const bool is = s0 + i < n;
+            const float f = is ? exp2_fast(v[i][0] - ref) : 0.f;
             sum = fmaf(f, v[i][1], sum);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[i][e], o[e]);
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(f, is ? x[i][e] : 0.f, o[e]);
         }
     }
     join_write<TR>(a, b, h, r, d, o, top, sum);
