@@ -1387,11 +1387,11 @@ def rotary_frequencies(R: int, base: float = 10000.0, scaling: int = ROTARY_NONE
     """fp64 [R / 2], radians per position, for rotary and rotary_append (see
     ctconv_rotary_frequencies)."""
     torch = _torch()
-    host = (ctypes.c_double * max(1, int(R) // 2))()
+    host = (ctypes.c_double * 128)()  # the largest R that is accepted has as many
     _check("ctconv_rotary_frequencies",
            load().ctconv_rotary_frequencies(R, base, scaling, factor, original, low, high,
                                             ctypes.addressof(host)))
-    return torch.tensor(list(host), dtype=torch.float64, device=device)
+    return torch.tensor(host[:R // 2], dtype=torch.float64, device=device)
 
 
 def _rotary_rows(q, k, positions, frequencies):
