@@ -185,23 +185,23 @@ stream_kernel(AttnArgs a) {
     const int staged = CHUNK && a.chunk > kPiece ? kPiece : a.chunk;
     uint32_t* seen = reinterpret_cast<uint32_t*>(lds + (PAGED ? (size_t)staged * 8 : 0));
     const auto stage = [&](int from, int to) __attribute__((always_inline)) {
-    const int padded = (to - from + 63) & ~63;
-    for (int i = tid; i < padded; i += (64 * NW)) {
-        bool ok = i < to - from;
-        const int t = first + start + from + i;
-        if constexpr (PAGED) {
-            int64_t o = -1;
-            if (ok)
-                o = !CHUNK && a.window == 0 && i == tid ? offset_in_page(a.pages, t, page0)
-                                                        : slot_offset(a.pages, b, t);
-            ok = o >= 0;
-            offs[i] = ok ? o : 0;  // page 0 exists: a readable row
-        } else {
-            if (ok && a.mask) ok = a.mask[b * a.mask_stride + t] != 0;
+        const int padded = (to - from + 63) & ~63;
+        for (int i = tid; i < padded; i += (64 * NW)) {
+            bool ok = i < to - from;
+            const int t = first + start + from + i;
+            if constexpr (PAGED) {
+                int64_t o = -1;
+                if (ok)
+                    o = !CHUNK && a.window == 0 && i == tid ? offset_in_page(a.pages, t, page0)
+                                                            : slot_offset(a.pages, b, t);
+                ok = o >= 0;
+                offs[i] = ok ? o : 0;  // page 0 exists: a readable row
+            } else {
+                if (ok && a.mask) ok = a.mask[b * a.mask_stride + t] != 0;
+            }
+            const uint64_t w = __ballot(ok);
+            if (lane == 0) *reinterpret_cast<uint64_t*>(seen + (i >> 5)) = w;
         }
-        const uint64_t w = __ballot(ok);
-        if (lane == 0) *reinterpret_cast<uint64_t*>(seen + (i >> 5)) = w;
-    }
     };
     if constexpr (!CHUNK) stage(0, n);
 
@@ -222,188 +222,193 @@ stream_kernel(AttnArgs a) {
     float m = -__builtin_huge_valf(), l = 0.f;
     const int t0 = first + start;
 
-    bool careful = false;  // CHUNK: the second time
     __shared__ int odd_sums;
     if (CHUNK && tid == 0) odd_sums = 0;
-again:
-    int done = 0;  // keys of earlier pieces
-    int n_here = n;
-    do {
-    if constexpr (CHUNK) {
-        n_here = n - done < kPiece ? n - done : kPiece;
-        if (done > 0) __syncthreads();
-        stage(done, done + n_here);
-        __syncthreads();
-    }
-    for (int kb = wave * KB; kb < n_here; kb += NW * KB) {
-        uint32_t bits = seen[kb >> 5];
-        if (KB == 16) bits = (bits >> (kb & 16)) & 0xFFFFu;
-        const uint32_t all = KB == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-        if (bits == 0 && !a.scores) continue;
-        u32x4 kf[NT][NF];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int i = kb + 16 * t + col;
-            int64_t o;
-            if constexpr (PAGED) o = offs[i];
-            else o = (bits >> (16 * t + col)) & 1 ? (int64_t)(t0 + i) * a.k_row : 0;
-            const S* kr = kbase + o;
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const int d = (4 * f + g) * VEC;
-                kf[t][f] = *reinterpret_cast<const u32x4*>(kr + (EXACT || d < a.D ? d : 0));
+    // (CHUNK: once more, carefully, where sums are odd)
+    for (bool careful = false;; careful = true) {
+        int done = 0;  // keys of earlier pieces
+        int n_here = n;
+        do {
+            if constexpr (CHUNK) {
+                n_here = n - done < kPiece ? n - done : kPiece;
+                if (done > 0) __syncthreads();
+                stage(done, done + n_here);
+                __syncthreads();
             }
-        }
-        // Values: key slot j of this lane group is key 4g + j % 4 of score
-        // tile j / 4.
-        uint32_t vr[VK][VW];
+            for (int kb = wave * KB; kb < n_here; kb += NW * KB) {
+                uint32_t bits = seen[kb >> 5];
+                if (KB == 16) bits = (bits >> (kb & 16)) & 0xFFFFu;
+                const uint32_t all = KB == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+                if (bits == 0 && !a.scores) continue;
+                u32x4 kf[NT][NF];
 #pragma unroll
-        for (int j = 0; j < VK; ++j) {
-            const int i = kb + 16 * (j >> 2) + 4 * g + (j & 3);
-            int64_t o;
-            if constexpr (PAGED) o = offs[i];
-            else o = (bits >> (i - kb)) & 1 ? (int64_t)(t0 + i) * a.v_row : 0;
-            const int d = col * VPL;
-            const S* vrow = vbase + o;
-            if constexpr (VW == 2) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(vrow + (EXACT || d < a.D ? d : 0));
-                vr[j][0] = w[0];
-                vr[j][1] = w[1];
-            } else {
+                for (int t = 0; t < NT; ++t) {
+                    const int i = kb + 16 * t + col;
+                    int64_t o;
+                    if constexpr (PAGED) o = offs[i];
+                    else o = (bits >> (16 * t + col)) & 1 ? (int64_t)(t0 + i) * a.k_row : 0;
+                    const S* kr = kbase + o;
 #pragma unroll
-                for (int p = 0; p < VW / 4; ++p) {
-                    const int dp = d + p * VEC;
-                    const u32x4 w =
-                        *reinterpret_cast<const u32x4*>(vrow + (EXACT || dp < a.D ? dp : 0));
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) vr[j][4 * p + q] = w[q];
+                    for (int f = 0; f < NF; ++f) {
+                        const int d = (4 * f + g) * VEC;
+                        kf[t][f] = *reinterpret_cast<const u32x4*>(kr + (EXACT || d < a.D ? d : 0));
+                    }
                 }
-            }
-        }
-        // CHUNK: what this lane's row sees of the block
-        uint32_t mine = bits;
-        bool odd = false;
-        if constexpr (CHUNK) {
-            const int at = t0 + done + kb;
-            if (at < all_from || at + KB > all_to)
-                mine &= low_bits(my_end - at) & ~low_bits(my_begin - at);
-            if (careful) {
+                // Values: key slot j of this lane group is key 4g + j % 4 of score
+                // tile j / 4.
+                uint32_t vr[VK][VW];
 #pragma unroll
-                for (int j = 0; j < VK; ++j)
-                    if ((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1)
+                for (int j = 0; j < VK; ++j) {
+                    const int i = kb + 16 * (j >> 2) + 4 * g + (j & 3);
+                    int64_t o;
+                    if constexpr (PAGED) o = offs[i];
+                    else o = (bits >> (i - kb)) & 1 ? (int64_t)(t0 + i) * a.v_row : 0;
+                    const int d = col * VPL;
+                    const S* vrow = vbase + o;
+                    if constexpr (VW == 2) {
+                        const u32x2 w =
+                            *reinterpret_cast<const u32x2*>(vrow + (EXACT || d < a.D ? d : 0));
+                        vr[j][0] = w[0];
+                        vr[j][1] = w[1];
+                    } else {
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) odd |= take_odd<TR>(vr[j][w]) != 0;
-            }
-        }
-        f32x4 s[NT];
+                        for (int p = 0; p < VW / 4; ++p) {
+                            const int dp = d + p * VEC;
+                            const u32x4 w = *reinterpret_cast<const u32x4*>(
+                                vrow + (EXACT || dp < a.D ? dp : 0));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                u32x4 k = kf[t][f];
-                // the piece past the row was read from its start: not a product
-                if (!EXACT && (4 * f + g) * VEC >= a.D) k = u32x4{0, 0, 0, 0};
-                Mma<TR>::step(s[t], k, qf[f]);
-            }
-        }
-        float top = -__builtin_huge_valf();
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = s[t][i] * a.c;
-                if (mine != all && !((mine >> (16 * t + 4 * g + i)) & 1)) v = -__builtin_huge_valf();
-                s[t][i] = v;
-                top = fmaxf(top, v);
-            }
-        if (a.scores && col < rows) {
-            float* sr = a.scores + ((int64_t)bh * a.R + row0 + col) * a.score_stride + start + kb;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<f32x4*>(sr + 16 * t + 4 * g) = s[t];
-        }
-        if (bits != all) {
-            // what a slot without a visible key holds may be NaN: zero, not 0 * NaN
-#pragma unroll
-            for (int j = 0; j < VK; ++j)
-                if (!((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1))
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) vr[j][w] = 0;
-        }
-        if (__any(top > m + kRaise)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float up = fmaxf(m, top);
-            const float f = m == up ? 1.f : exp2_fast(m - up);
-            m = up;
-            l *= f;
-#pragma unroll
-            for (int e = 0; e < VPL; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[e][i] *= f;
-        }
-        const float ref = reference_of(m);
-        float p[VK];
-#pragma unroll
-        for (int j = 0; j < VK; ++j) {
-            p[j] = exp2_fast(s[j >> 2][j & 3] - ref);
-            l += p[j];
-        }
-        if constexpr (ES == 2) {
-            u32x4 pf, pl;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float p0 = p[2 * w], p1 = p[2 * w + 1];
-                pf[w] = mfma::pack2<TR>(p0, p1);
-                pl[w] = mfma::pack2<TR>(p0 - TR::to_f32((uint16_t)pf[w]),
-                                        p1 - TR::to_f32((uint16_t)(pf[w] >> 16)));
-            }
-#pragma unroll
-            for (int e = 0; e < VPL; ++e) {
-                const unsigned sel = (e & 1) ? 0x07060302u : 0x05040100u;
-                u32x4 vf;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][e >> 1], vr[2 * w][e >> 1], sel);
-                Mma<TR>::step(acc[e], vf, pf);
-                Mma<TR>::step(acc[e], vf, pl);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < VK; ++j)
-#pragma unroll
-                for (int e = 0; e < VPL; ++e)
-                    acc[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(vr[j][e]), p[j],
-                                                                  acc[e], 0, 0, 0);
-        }
-        if constexpr (CHUNK)
-            if (__any(odd)) {
-                // this lane's values of output columns (4 g + i) VPL + e, row col (what
-                // lies past a row's end goes to columns that are not written)
-                constexpr int RUN = VPL < 8 ? VPL : 8;
-                for (int j = 0; j < KB; ++j) {
-                    if (!((bits >> j) & 1)) continue;
-                    const S* vrow = vbase + offs[kb + j];
-                    const float sees = (mine >> j) & 1 ? 1.f : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e0 = 0; e0 < VPL; e0 += RUN) {
-                            const int d = (4 * g + i) * VPL + e0;
-                            const S* run = vrow + (EXACT || d < a.D ? d : 0);
-#pragma unroll
-                            for (int e = 0; e < RUN; ++e) {
-                                const float x = TR::to_f32(run[e]);
-                                if (sees != 0.f && !(fabsf(x) <= __FLT_MAX__)) acc[e0 + e][i] += x;
-                            }
+                            for (int q = 0; q < 4; ++q) vr[j][4 * p + q] = w[q];
                         }
+                    }
                 }
+                // CHUNK: what this lane's row sees of the block
+                uint32_t mine = bits;
+                bool odd = false;
+                if constexpr (CHUNK) {
+                    const int at = t0 + done + kb;
+                    if (at < all_from || at + KB > all_to)
+                        mine &= low_bits(my_end - at) & ~low_bits(my_begin - at);
+                    if (careful) {
+#pragma unroll
+                        for (int j = 0; j < VK; ++j)
+                            if ((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1)
+#pragma unroll
+                                for (int w = 0; w < VW; ++w) odd |= take_odd<TR>(vr[j][w]) != 0;
+                    }
+                }
+                f32x4 s[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) {
+                        u32x4 k = kf[t][f];
+                        // the piece past the row was read from its start: not a product
+                        if (!EXACT && (4 * f + g) * VEC >= a.D) k = u32x4{0, 0, 0, 0};
+                        Mma<TR>::step(s[t], k, qf[f]);
+                    }
+                }
+                float top = -__builtin_huge_valf();
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = s[t][i] * a.c;
+                        if (mine != all && !((mine >> (16 * t + 4 * g + i)) & 1))
+                            v = -__builtin_huge_valf();
+                        s[t][i] = v;
+                        top = fmaxf(top, v);
+                    }
+                if (a.scores && col < rows) {
+                    float* sr = a.scores + ((int64_t)bh * a.R + row0 + col) * a.score_stride +
+                                start + kb;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        *reinterpret_cast<f32x4*>(sr + 16 * t + 4 * g) = s[t];
+                }
+                if (bits != all) {
+                    // what a slot without a visible key holds may be NaN: zero, not 0 * NaN
+#pragma unroll
+                    for (int j = 0; j < VK; ++j)
+                        if (!((bits >> (16 * (j >> 2) + 4 * g + (j & 3))) & 1))
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) vr[j][w] = 0;
+                }
+                if (__any(top > m + kRaise)) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    const float up = fmaxf(m, top);
+                    const float f = m == up ? 1.f : exp2_fast(m - up);
+                    m = up;
+                    l *= f;
+#pragma unroll
+                    for (int e = 0; e < VPL; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[e][i] *= f;
+                }
+                const float ref = reference_of(m);
+                float p[VK];
+#pragma unroll
+                for (int j = 0; j < VK; ++j) {
+                    p[j] = exp2_fast(s[j >> 2][j & 3] - ref);
+                    l += p[j];
+                }
+                if constexpr (ES == 2) {
+                    u32x4 pf, pl;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float p0 = p[2 * w], p1 = p[2 * w + 1];
+                        pf[w] = mfma::pack2<TR>(p0, p1);
+                        pl[w] = mfma::pack2<TR>(p0 - TR::to_f32((uint16_t)pf[w]),
+                                                p1 - TR::to_f32((uint16_t)(pf[w] >> 16)));
+                    }
+#pragma unroll
+                    for (int e = 0; e < VPL; ++e) {
+                        const unsigned sel = (e & 1) ? 0x07060302u : 0x05040100u;
+                        u32x4 vf;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][e >> 1],
+                                                          vr[2 * w][e >> 1], sel);
+                        Mma<TR>::step(acc[e], vf, pf);
+                        Mma<TR>::step(acc[e], vf, pl);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VK; ++j)
+#pragma unroll
+                        for (int e = 0; e < VPL; ++e)
+                            acc[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __uint_as_float(vr[j][e]), p[j], acc[e], 0, 0, 0);
+                }
+                if constexpr (CHUNK)
+                    if (__any(odd)) {
+                        // this lane's values of output columns (4 g + i) VPL + e, row col (what
+                        // lies past a row's end goes to columns that are not written)
+                        constexpr int RUN = VPL < 8 ? VPL : 8;
+                        for (int j = 0; j < KB; ++j) {
+                            if (!((bits >> j) & 1)) continue;
+                            const S* vrow = vbase + offs[kb + j];
+                            const float sees = (mine >> j) & 1 ? 1.f : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int e0 = 0; e0 < VPL; e0 += RUN) {
+                                    const int d = (4 * g + i) * VPL + e0;
+                                    const S* run = vrow + (EXACT || d < a.D ? d : 0);
+#pragma unroll
+                                    for (int e = 0; e < RUN; ++e) {
+                                        const float x = TR::to_f32(run[e]);
+                                        if (sees != 0.f && !(fabsf(x) <= __FLT_MAX__))
+                                            acc[e0 + e][i] += x;
+                                    }
+                                }
+                        }
+                    }
             }
-    }
-    done += n_here;
-    } while (CHUNK && done < n);
-    if constexpr (CHUNK) {
+            done += n_here;
+        } while (CHUNK && done < n);
+        if constexpr (!CHUNK) break;
         // What is not finite in a sum (0 times infinity is NaN) is in it for good.
         float worst = 0.f;
 #pragma unroll
@@ -412,14 +417,11 @@ again:
             for (int i = 0; i < 4; ++i) worst += 0.f * acc[e][i];
         if (!careful && __any(worst != 0.f)) odd_sums = 1;
         __syncthreads();  // offs and seen are no longer read
-        if (!careful && odd_sums) {
-            careful = true;
+        if (careful || !odd_sums) break;
 #pragma unroll
-            for (int e = 0; e < VPL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-            m = -__builtin_huge_valf();
-            l = 0.f;
-            goto again;
-        }
+        for (int e = 0; e < VPL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        m = -__builtin_huge_valf();
+        l = 0.f;
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
