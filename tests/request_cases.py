@@ -39,3 +39,12 @@ TILED = [
 CUT = [("f32", 1000, 32, 8, 128)]
 # (dtype, n, query heads, key heads, slots past 160) of the test of missing pages
 MISSING = [("f32", 300, 32, 2, 992)]
+# (dtype, case): the tiled kernel with few values per head, and with widths that fill its LDS rows
+# by less than half
+NARROW = [
+    ("bf16", ([900], [2000], 900, 16, 1, 8, 16, 0, "library")),
+    ("bf16", ([900], [2000], 900, 16, 1, 16, 8, 0, "slots")),
+    ("f16", ([900], [2000], 900, 16, 1, 24, 16, 0, "both")),
+    ("f32", ([2000], [2000], 2000, 16, 1, 16, 16, 0, "library")),
+    ("bf16", ([900], [2000], 900, 16, 1, 136, 16, 0, "library")),
+]

@@ -188,3 +188,47 @@ def test_odd_values_reach_only_the_rows_that_see_them(cc, case):  # noqa: F811
     assert bool((got[two & ~one][:, mine, 3] == float("-inf")).all())
     assert bool(torch.isnan(got[one & two][:, mine, 3]).all())
     assert torch.equal(got[~one & ~two], clean[~one & ~two])
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("n,G,L,window", [(8, 2, 600, 50), (900, 16, 1400, 100), (2000, 8, 2112, 300)])
+def test_odd_rows_reach_only_the_weights_of_slots_they_see(cc, dt, n, G, L, window):  # noqa: F811
+    """A NaN in a query, or in a key, makes NaN of the weights of the slots that its rows see; the
+    others stay what they are, up to the roundings of the other rows' lse (a few 2^-24 of scores
+    below 2^5)."""
+    import torch
+
+    say(f"odd weights {dt} {n} {G} {L} {window}")
+    H, D, page = 2, 64, 16
+    c = Chunk(dt, [n], [L], H, G, D)
+    cap = c.table.shape[1] * page
+
+    def weights(q, k):
+        w = torch.full((1, H, cap), 0.25, device="cuda")
+        cc.chunk_attention(q, k, c.v, c.table.int(), ints([L]), row_starts=ints([0, n]), n=n,
+                           window=window, scale=0.1, weight_sum=w)
+        torch.cuda.synchronize()
+        return w.cpu()
+
+    clean = weights(c.q, c.k)
+    assert bool(torch.isfinite(clean).all())
+    at = np.arange(L)
+    for what in ("query", "key"):
+        q, k = c.q.clone(), c.k.clone()
+        row = n // 2
+        own = L - n + row  # the slot of that row
+        hit = np.zeros(cap, bool)
+        if what == "query":
+            q[row, G - 1, 3] = float("nan")
+            hit[:L] = (at <= own) & (at > own - window)
+        else:
+            p, o = c.place(0, own)
+            k[p, 0, o, 3] = float("nan")
+            # rows own .. own + window - 1 see it, and so do the slots around them
+            last = min(own + window - 1, L - 1)
+            hit[:L] = (at <= last) & (at > own - window)
+        got = weights(q, k)
+        hit = torch.from_numpy(hit)
+        assert bool(torch.isnan(got[0, 0, hit]).all()), what
+        assert torch.equal(got[0, 1], clean[0, 1]), what
+        assert torch.allclose(got[0, 0, ~hit], clean[0, 0, ~hit], rtol=1e-5, atol=0), what

@@ -20,6 +20,11 @@ def test_tiled(cc, case, weights):  # noqa: F811
     T.test_chunk_attention(cc, case[1], case[0], weights)
 
 
+@pytest.mark.parametrize("case", cases.NARROW, ids=[str(i) for i in range(len(cases.NARROW))])
+def test_tiled_narrow_heads(cc, case):  # noqa: F811
+    T.test_chunk_attention(cc, case[1], case[0], True)
+
+
 @pytest.mark.parametrize("dt,n,Hq,H,D", cases.CUT)
 def test_tiled_rows_that_do_not_exist(cc, dt, n, Hq, H, D):  # noqa: F811
     T.test_chunk_rows_that_do_not_exist(cc, dt, n, Hq, H, D)

@@ -85,6 +85,10 @@ def test_tiled_cases_reach_the_tiled_kernel(plan):
                         CODE[dt])[0] == "tile", (counts, D)
             assert plan(len(counts), len(counts) * n, n, Hq, H, D, most, window, weights, CODE[dt],
                         packed=0)[0] == "tile", (counts, D)
+    for dt, (counts, lengths, n, Hq, H, D, page, window, _) in cases.NARROW:
+        most = (-(-max(lengths) // page) + 1) * page
+        assert plan(len(counts), sum(counts) + 3, n, Hq, H, D, most, window, 1,
+                    CODE[dt])[0] == "tile", (counts, D)
     for dt, n, Hq, H, D in cases.CUT:
         most = -(-(n + 900) // 16) * 16
         assert plan(2, 2 * n - 1 - n // 2, n, Hq, H, D, most, 0, 1, CODE[dt])[0] == "tile"
