@@ -453,7 +453,7 @@ ctconv_status ctconv_clock_probe(void* workspace, size_t workspace_bytes, int it
  * matrix instruction takes both operands in one type) they go in two parts,
  * the rounded weight and the rounded rest; with more than 64 query rows per
  * key head, where the matrix product is what takes the time, they are rounded
- * to the element type.
+ * to the element type (ctconv_chunk_attention: see there).
  *
  * Common rules.  Sizes and strides are int64, strides in elements, at least
  * 0, the last dimension contiguous.  Device pointers are 16-byte aligned and
@@ -695,7 +695,8 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
  * sequences that need more take pages from the top of the stack, in order of
  * sequence and column, and write them to their table rows; when the stack is
  * empty, the columns left over get -1 (slots without a page), and
- * held_out[b] * page_size < lengths[b] says so.
+ * held_out[b] * page_size < lengths[b] says so, as it does of a length past the
+ * table.
  *   lengths, held, held_out   device int32 [B]; held_out (pages now held) may
  *                 be held
  *   page_table    device int32 [B, max_pages], table_stride per row; columns
@@ -708,8 +709,8 @@ ctconv_status ctconv_norm_residual(const void* x, const void* h, const void* pos
  * be repeated: it does the same again.
  *
  * Row maps, when counts is not NULL.  counts[b] (clamped to [0, lengths[b]])
- * are the new rows of b, the last ones of its length, packed one sequence
- * behind the other:
+ * are the new rows of b, the last ones of its length as it is given (rows
+ * past the table have no slot), packed one sequence behind the other:
  *   row_starts    device int32 [B + 1]: the sum of the counts before b
  *   row_positions device int32 [rows]: now[b] - counts[b] + i; -1 behind the
  *                 last row
@@ -819,7 +820,11 @@ ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_sc
  * Attention of each sequence's new rows, the last counts[b] of its lengths[b]
  * slots, to the cache that holds them already: row i sees the slots
  *     t in [max(0, e - window), e),   e = lengths[b] - counts[b] + i + 1
- * (window 0: from 0); s, p, out and lse as in ctconv_paged_attention.
+ * (window 0: from 0); s, p, out and lse as in ctconv_paged_attention.  lengths[b]
+ * is clamped before counts[b] is taken from it: of a sequence that has outgrown
+ * its table or max_length, the new rows are not taken for those that
+ * ctconv_cache_pages and ctconv_cache_append had slots for, but for the last ones
+ * that fit, so cut such a sequence back (held_out tells it) before the call.
  *   q, out        device, q_strides, out_strides = batch, row, head
  *                 row_starts given: [rows, Hq, D] (the batch stride is not
  *                 used); NULL: [B, n, Hq, D], rows = B * n
@@ -838,7 +843,10 @@ ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_sc
  * A row that sees nothing gets out = 0 and lse = -infinity.  Infinities and
  * NaN in a slot reach only the rows that see it.  16-bit weights meet the
  * values in two parts with up to 16 query rows (n times Hq / Hkv) per key head;
- * with more they may be rounded to the element type.  Workspace, D, heads,
+ * with more they may be rounded to the element type (lse and weight_sum are of
+ * the weights before that).  Which it is, and how the slots are split, follows
+ * from the call's sizes: a sequence's results can differ in their roundings
+ * between calls of other B, rows, n or max_length.  Workspace, D, heads,
  * scale and max_length as in ctconv_paged_attention.  out must not overlap an
  * input.
  */

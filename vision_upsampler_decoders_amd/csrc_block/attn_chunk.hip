@@ -84,14 +84,14 @@ constexpr int key_groups(int pieces) {
 // rows go through LDS: read straight to the instruction's lanes, 16 bytes of each
 // of 32 rows at a time, they keep the load unit busy for longer than the matrix
 // instructions take (4096 rows of 24 heads over 32768 keys twice, f16: 3126 us, and
-// 2005 this way).  The waves of a workgroup take keys of their own and the same
-// rows, or, where that would leave compute units idle (APART), the same keys and
+// 2005 this way; 1822 now).  The waves of a workgroup take keys of their own and the
+// same rows, or, where that would leave compute units idle (APART), the same keys and
 // every fourth rows: where those are at most 512 workgroups (bf16, 4 heads of 128
 // channels, apart | together, the call: 4000 rows of 16 heads over 4000 keys, 500
 // workgroups apart, 212 | 487 us; 500 of 32 over 8: 1000 keys, 256 workgroups,
 // 53 | 98, 4000, 1000, 105 | 119, twice 4000, 2000, 198 | 176; 16 rows of 32: 21 | 22,
 // 32 | 25, 52 | 33).
-// 1.55 TFLOP in 1.95 ms there: 0.7 of it for the exponentials, 0.7 for the matrix
+// 1.55 TFLOP in 1.82 ms there: 0.7 of it for the exponentials, 0.7 for the matrix
 // instructions, 0.35 for two more vector instructions a score; each is busy while the
 // other waits.  Tried: the scores of one group weighed between the next one's matrix
 // instructions (5.6 ms the call, and 5.5 without).

@@ -55,7 +55,7 @@
 // order) differ in three things.  A workgroup finds its sequence by a scan over
 // their numbers of rows, so that ragged batches take as many workgroups as they
 // have row tiles.  Rows of keys and values lie in pages: the offsets of a tile's
-// keys go through LDS, two tiles ahead of their loads.  And every row has its own
+// keys go through LDS, one tile ahead of their loads.  And every row has its own
 // last (and, in a window, first) key: tiles that some row does not see whole hide
 // scores per lane.  Waves without a row only move tiles.
 // Loads are of 64-bit addresses (a cache may be larger than 4 GB), and the offsets

@@ -116,11 +116,17 @@ void stream_chunk(int64_t tiles, int64_t padded, int64_t span, int64_t D, ctconv
 //    last to end.  Lengths spread evenly make (s + 1) / 2 workgroups of a tile in the
 //    mean: as many as fill the chip, of 1024 keys at least.  24 x 8 rows of 32 heads
 //    over up to 8192 keys: 99 us in chunks of 2048, 118 of 1664 (the second round of
-//    a few), 121 of 4096.
+//    a few), 121 of 4096.  Tiles over up to 4096 keys, bf16, D = 128, whole | 2 | 3 | 4
+//    | 8 splits: 64 110 | 70 | 56 | 52 | 62 (the rule takes 4), 128 112 | 82 | 91 | 89 |
+//    104 (4), 192 123 | 130 | 117 | 113 | 128 (4), 256 145 | 143 | 138 | 156 | 152 (3),
+//    384 188 | 190 | 191 | 179 | 204 (1), 512 208 | 229 | 230 | 232 | 267 (1).
 //  - So may their rows, where there are several tiles of the longest and in the mean
 //    fewer than half of n: one that goes on by a row has the keys of a whole tile.
 //    47 such and one of 2048 rows over up to 16384 keys: 411 us in chunks of 4096,
-//    479 of 8192, 636 whole.
+//    479 of 8192, 636 whole.  Means of five draws of their lengths, whole | 3 | 4 | 8
+//    splits: the same 736 | 720 | 691 | 743 (the rule takes 4), 11 of 16384 624 | 496 |
+//    457 | 517 (6), 95 of 8192 472 | 524 | 528 | 566 (3), 23 and 512 rows of 4096 126 |
+//    124 | 127 | 145 (4), of 16384 and 47 490 | 469 | 478 | 490 (7).
 int64_t tile_splits(int64_t tiles, int64_t keys, double once, int64_t D, ctconv_dtype dt,
                     bool several, bool uneven) {
     const int64_t n = tiles > 0 ? tiles : 1, steps = ceil_div(keys, 64);

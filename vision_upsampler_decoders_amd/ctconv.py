@@ -1329,7 +1329,8 @@ def cache_pages(page_table, held, free_pages, free_count, lengths, num_pages=Non
                 weight_sum=None, stream=None):
     """Make page tables follow the lengths, in place (see ctconv_cache_pages):
     page_table int32 [B, max_pages], held int32 [B], the stack free_pages int32
-    [num_pages] with free_count int32 [1] on it.  With counts int32 [B], the
+    [num_pages] with free_count int32 [1] on it (num_pages, if given, has to be
+    free_pages' size; page_size is that of the cache).  With counts int32 [B], the
     new rows of each sequence (lengths counts them already), returns their maps
     (row_starts [B + 1], row_positions [rows], row_slots [rows]) for `rows` rows
     in all, and sets positions int32 and weight_sum fp32 [B, Hkv, slots] (or
@@ -1485,9 +1486,10 @@ def chunk_attention(q, k_cache, v_cache, page_table, lengths, row_starts=None, c
     """(out, lse) of each sequence's new rows over the paged cache that holds them
     already (see ctconv_chunk_attention).  Packed: q [rows, Hq, D] with
     row_starts int32 [B + 1] and n, a bound on the rows of a sequence (default:
-    rows; a closer one saves workgroups without rows).  Padded: q [B, n, Hq, D] with counts int32 [B] or None.  lse fp32
-    [rows, Hq] or [B, n, Hq].  weight_sum fp32 [B, Hkv, slots] or None is added
-    to.  Without out and lse, what lies behind a sequence's rows is undefined."""
+    rows; a closer one saves workgroups without rows).  Padded: q [B, n, Hq, D]
+    with counts int32 [B] or None.  lse fp32 [rows, Hq] or [B, n, Hq].
+    weight_sum fp32 [B, Hkv, slots] or None is added to.  Without out and lse,
+    what lies behind a sequence's rows is undefined."""
     torch = _torch()
     if not q.is_cuda:
         raise ValueError("q must be a device tensor")
