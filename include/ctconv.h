@@ -833,8 +833,9 @@ ctconv_status ctconv_rotary_frequencies(int64_t R, double base, ctconv_rotary_sc
  *                 not exist
  *   counts        device int32 [B] or NULL (n), clamped to [0, n]; not used with
  *                 row_starts
- *   n             a bound on counts that the caller knows; the closer, the fewer
- *                 workgroups without rows (past `rows` it makes no difference)
+ *   n             a bound on counts that the caller knows; the kernel and its
+ *                 splits are chosen by it, the better the closer it is (past
+ *                 `rows` it makes no difference)
  *   lse           device fp32 [rows, Hq] dense (row b * n + i when padded), or NULL
  *   weight_sum    device fp32 [B, Hkv, slots] or NULL: weight_sum[b][h][t] +=
  *                 the sum of p[t] over the new rows and the query heads of h

@@ -1486,7 +1486,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, lengths, row_starts=None, c
     """(out, lse) of each sequence's new rows over the paged cache that holds them
     already (see ctconv_chunk_attention).  Packed: q [rows, Hq, D] with
     row_starts int32 [B + 1] and n, a bound on the rows of a sequence (default:
-    rows; a closer one saves workgroups without rows).  Padded: q [B, n, Hq, D]
+    rows; a closer one makes a faster call).  Padded: q [B, n, Hq, D]
     with counts int32 [B] or None.  lse fp32 [rows, Hq] or [B, n, Hq].
     weight_sum fp32 [B, Hkv, slots] or None is added to.  Without out and lse,
     what lies behind a sequence's rows is undefined."""
